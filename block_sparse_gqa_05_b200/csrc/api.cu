@@ -58,6 +58,42 @@ msa_status check_shape(const msa_shape* s, bool need_attn, bool need_index) {
   return MSA_OK;
 }
 
+// Shared-prefix decode: q_offset is ignored, the T new rows fit the own cache
+// and the tile of one sequence and group (T * r rows) fits one row tile.
+msa_status check_prefix_decode(const msa_shape* s) {
+  if (!s) return MSA_ERR_NULL_PTR;
+  if (s->seq_q < 1 || s->seq_q > s->seq_kv) return MSA_ERR_INVALID_SHAPE;
+  msa_shape c = *s;
+  c.q_offset = c.seq_kv - c.seq_q;
+  const msa_status st = check_shape(&c, true, false);
+  if (st != MSA_OK) return st;
+  const int64_t rows = static_cast<int64_t>(s->seq_q) * (s->n_q_heads / s->n_kv_heads);
+  return rows > 128 ? MSA_ERR_UNSUPPORTED : MSA_OK;
+}
+
+msa_status check_evict(const msa_shape* s) {
+  if (!s) return MSA_ERR_NULL_PTR;
+  msa_shape c = *s;
+  c.seq_q = 1;
+  c.q_offset = 0;
+  return check_shape(&c, true, false);
+}
+
+// num_pages of a paged call: 32-bit TMA coordinates (page*G + g) and row offsets.
+msa_status check_pages(const msa_shape* s, int num_pages) {
+  if (num_pages < 1) return MSA_ERR_INVALID_SHAPE;
+  if (static_cast<int64_t>(num_pages) * s->n_kv_heads >= (1ll << 31) ||
+      static_cast<int64_t>(num_pages) * 128 >= (1ll << 31))
+    return MSA_ERR_UNSUPPORTED;
+  return MSA_OK;
+}
+
+// Whether the n-element 4-byte arrays at a (na elements) and b (nb) share memory.
+bool overlap4(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + static_cast<uintptr_t>(nb) * 4 && y < x + static_cast<uintptr_t>(na) * 4;
+}
+
 msa_status check_decode(const msa_shape* s) {
   if (s->seq_q != 1 || s->q_offset != s->seq_kv - 1) return MSA_ERR_INVALID_SHAPE;
   return MSA_OK;
@@ -261,6 +297,15 @@ msa_status msa_workspace_size(const msa_shape* s, msa_op op, size_t* bytes) {
       if ((st = check_shape(s, true, true)) != MSA_OK) return st;
       if (!prefill_shape_supported(*s)) return MSA_ERR_UNSUPPORTED;
       *bytes = paged_prefill_pooled_bytes(*s) + sel_bytes(*s) + prefill_workspace_bytes(*s);
+      return MSA_OK;
+    case MSA_OP_PREFIX_DECODE:
+    case MSA_OP_PREFIX_DECODE_WEIGHTS:
+      if ((st = check_prefix_decode(s)) != MSA_OK) return st;
+      *bytes = prefix_decode_workspace_bytes(*s, op == MSA_OP_PREFIX_DECODE_WEIGHTS);
+      return MSA_OK;
+    case MSA_OP_CACHE_EVICT:
+      if ((st = check_evict(s)) != MSA_OK) return st;
+      *bytes = evict_workspace_bytes(*s);
       return MSA_OK;
   }
   return MSA_ERR_UNSUPPORTED;
@@ -533,6 +578,161 @@ msa_status msa_forward_prefill_paged(const msa_shape* s, int num_pages,
   if (e == cudaSuccess)
     e = launch_sparse_prefill(*s, q, k, v, sel, o, lse, rest, cs, nullptr, nullptr, pt);
   return from_cuda(e);
+}
+
+// The checks and the launch shared by the contiguous and the paged call.
+static msa_status prefix_decode(const msa_shape* s, const PrefixDecodeArgs& a, void* ws,
+                                size_t ws_bytes, void* stream) {
+  if (!a.q || !a.k || !a.v || !a.o || !a.lens || (a.w_in && !a.w_out)) return MSA_ERR_NULL_PTR;
+  if (!aligned16(a.q) || !aligned16(a.k) || !aligned16(a.v) || !aligned16(a.o) ||
+      !aligned4(a.lens) || !aligned4(a.lse) || !aligned4(a.w_in) || !aligned4(a.w_out))
+    return MSA_ERR_MISALIGNED;
+  const int64_t nw = static_cast<int64_t>(s->batch) * s->n_kv_heads * s->seq_kv;
+  if (a.w_in && a.w_in != a.w_out && overlap4(a.w_in, nw, a.w_out, nw)) return MSA_ERR_UNSUPPORTED;
+  const size_t need = prefix_decode_workspace_bytes(*s, a.w_out != nullptr);
+  if (!ws) return MSA_ERR_NULL_PTR;
+  if (ws_bytes < need) return MSA_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned16(ws)) return MSA_ERR_MISALIGNED;
+  if (!device_ctx()) return MSA_ERR_CUDA;
+  return from_cuda(launch_prefix_decode(*s, a, ws, static_cast<cudaStream_t>(stream)));
+}
+
+msa_status msa_prefix_attn_decode(const msa_shape* s, int prefix_len, int prefix_cap,
+                                  const int32_t* seq_lens, const uint16_t* q,
+                                  const uint16_t* k_prefix, const uint16_t* v_prefix,
+                                  const uint16_t* k, const uint16_t* v, uint16_t* o, float* lse,
+                                  const float* weights, float* weights_out, void* ws,
+                                  size_t ws_bytes, void* stream) {
+  msa::ApiRange nvtx_("msa_prefix_attn_decode");
+  const msa_status st = check_prefix_decode(s);
+  if (st != MSA_OK) return st;
+  if (prefix_len < 0 || prefix_cap < prefix_len) return MSA_ERR_INVALID_SHAPE;
+  if (static_cast<int64_t>(prefix_cap) * s->n_kv_heads >= (1ll << 31)) return MSA_ERR_UNSUPPORTED;
+  if (prefix_len > 0 && (!k_prefix || !v_prefix)) return MSA_ERR_NULL_PTR;
+  if (prefix_len > 0 && (!aligned16(k_prefix) || !aligned16(v_prefix))) return MSA_ERR_MISALIGNED;
+  PrefixDecodeArgs a;
+  a.prefix_len = prefix_len;
+  a.prefix_cap = prefix_cap;
+  a.lens = seq_lens;
+  a.q = q;
+  a.kp = k_prefix;
+  a.vp = v_prefix;
+  a.k = k;
+  a.v = v;
+  a.o = o;
+  a.lse = lse;
+  a.w_in = weights;
+  a.w_out = weights_out;
+  return prefix_decode(s, a, ws, ws_bytes, stream);
+}
+
+msa_status msa_prefix_attn_decode_paged(const msa_shape* s, int num_pages, int prefix_len,
+                                        const int32_t* prefix_pages, const int32_t* seq_lens,
+                                        const int32_t* page_table, const uint16_t* q,
+                                        const uint16_t* k, const uint16_t* v, uint16_t* o,
+                                        float* lse, const float* weights, float* weights_out,
+                                        void* ws, size_t ws_bytes, void* stream) {
+  msa::ApiRange nvtx_("msa_prefix_attn_decode_paged");
+  msa_status st = check_prefix_decode(s);
+  if (st == MSA_OK) st = check_pages(s, num_pages);
+  if (st != MSA_OK) return st;
+  if (prefix_len < 0) return MSA_ERR_INVALID_SHAPE;
+  if (static_cast<int64_t>(prefix_len) * s->n_kv_heads >= (1ll << 31)) return MSA_ERR_UNSUPPORTED;
+  if (!page_table || (prefix_len > 0 && !prefix_pages)) return MSA_ERR_NULL_PTR;
+  if (!aligned4(page_table) || !aligned4(prefix_pages)) return MSA_ERR_MISALIGNED;
+  PrefixDecodeArgs a;
+  a.prefix_len = prefix_len;
+  a.prefix_pages = prefix_pages;
+  a.pages.table = page_table;
+  a.pages.num_pages = num_pages;
+  a.lens = seq_lens;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.o = o;
+  a.lse = lse;
+  a.w_in = weights;
+  a.w_out = weights_out;
+  return prefix_decode(s, a, ws, ws_bytes, stream);
+}
+
+// The checks and the launch shared by the contiguous and the paged eviction.
+static msa_status cache_evict(const msa_shape* s, const EvictArgs& a, void* ws, size_t ws_bytes,
+                              void* stream) {
+  if (a.budget < 1 || a.n_first < 0 || a.n_recent < 0) return MSA_ERR_INVALID_SHAPE;
+  if (!a.lens || !a.w_in || !a.pos_in || !a.k || !a.v || !a.w_out || !a.pos_out || !a.new_lens)
+    return MSA_ERR_NULL_PTR;
+  if (!aligned16(a.k) || !aligned16(a.v) || !aligned4(a.lens) || !aligned4(a.w_in) ||
+      !aligned4(a.pos_in) || !aligned4(a.w_out) || !aligned4(a.pos_out) || !aligned4(a.new_lens))
+    return MSA_ERR_MISALIGNED;
+  const int64_t n = static_cast<int64_t>(s->batch) * s->n_kv_heads * s->seq_kv;
+  const void *wi = a.w_in, *pi = a.pos_in, *wo = a.w_out, *po = a.pos_out;
+  if ((wi != wo && overlap4(wi, n, wo, n)) || (pi != po && overlap4(pi, n, po, n)) ||
+      overlap4(wo, n, po, n) || overlap4(wi, n, po, n) || overlap4(pi, n, wo, n))
+    return MSA_ERR_UNSUPPORTED;
+  const int64_t B = s->batch;
+  if (overlap4(a.lens, B, a.new_lens, B) || overlap4(a.new_lens, B, wi, n) ||
+      overlap4(a.new_lens, B, pi, n) || overlap4(a.new_lens, B, wo, n) ||
+      overlap4(a.new_lens, B, po, n) || overlap4(a.lens, B, wo, n) || overlap4(a.lens, B, po, n))
+    return MSA_ERR_UNSUPPORTED;
+  const size_t need = evict_workspace_bytes(*s);
+  if (!ws) return MSA_ERR_NULL_PTR;
+  if (ws_bytes < need) return MSA_ERR_WORKSPACE_TOO_SMALL;
+  if (!aligned16(ws)) return MSA_ERR_MISALIGNED;
+  if (!device_ctx()) return MSA_ERR_CUDA;
+  return from_cuda(launch_cache_evict(*s, a, ws, static_cast<cudaStream_t>(stream)));
+}
+
+msa_status msa_cache_evict(const msa_shape* s, int budget, int n_first, int n_recent,
+                           const int32_t* seq_lens, const float* weights,
+                           const int32_t* positions, uint16_t* k, uint16_t* v,
+                           float* weights_out, int32_t* positions_out, int32_t* new_lens,
+                           void* ws, size_t ws_bytes, void* stream) {
+  msa::ApiRange nvtx_("msa_cache_evict");
+  const msa_status st = check_evict(s);
+  if (st != MSA_OK) return st;
+  EvictArgs a;
+  a.budget = budget;
+  a.n_first = n_first;
+  a.n_recent = n_recent;
+  a.lens = seq_lens;
+  a.w_in = weights;
+  a.pos_in = positions;
+  a.k = k;
+  a.v = v;
+  a.w_out = weights_out;
+  a.pos_out = positions_out;
+  a.new_lens = new_lens;
+  return cache_evict(s, a, ws, ws_bytes, stream);
+}
+
+msa_status msa_cache_evict_paged(const msa_shape* s, int num_pages, int budget, int n_first,
+                                 int n_recent, const int32_t* seq_lens,
+                                 const int32_t* page_table, const float* weights,
+                                 const int32_t* positions, uint16_t* k, uint16_t* v,
+                                 float* weights_out, int32_t* positions_out, int32_t* new_lens,
+                                 void* ws, size_t ws_bytes, void* stream) {
+  msa::ApiRange nvtx_("msa_cache_evict_paged");
+  msa_status st = check_evict(s);
+  if (st == MSA_OK) st = check_pages(s, num_pages);
+  if (st != MSA_OK) return st;
+  if (!page_table) return MSA_ERR_NULL_PTR;
+  if (!aligned4(page_table)) return MSA_ERR_MISALIGNED;
+  EvictArgs a;
+  a.budget = budget;
+  a.n_first = n_first;
+  a.n_recent = n_recent;
+  a.lens = seq_lens;
+  a.w_in = weights;
+  a.pos_in = positions;
+  a.k = k;
+  a.v = v;
+  a.w_out = weights_out;
+  a.pos_out = positions_out;
+  a.new_lens = new_lens;
+  a.pages.table = page_table;
+  a.pages.num_pages = num_pages;
+  return cache_evict(s, a, ws, ws_bytes, stream);
 }
 
 msa_status msa_dense_attn_prefill(const msa_shape* s, const uint16_t* q, const uint16_t* k,

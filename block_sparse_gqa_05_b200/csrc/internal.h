@@ -127,6 +127,36 @@ cudaError_t prepare_decode(const msa_shape& s, void* ws, cudaStream_t st);
 msa_status check_decode_static_args(const msa_shape* s, const uint16_t* q, const uint16_t* k,
                                     const uint16_t* v, const int32_t* sel, const uint16_t* o,
                                     const float* lse);
+// Shared-prefix decode attention.  prefix_pages / pages.table set: paged caches
+// (kp, vp unused); else kp, vp [G, prefix_cap, d] and k, v [B, G, N, d].
+struct PrefixDecodeArgs {
+  int prefix_len = 0, prefix_cap = 0;
+  const int32_t* lens = nullptr;
+  const uint16_t *q = nullptr, *kp = nullptr, *vp = nullptr, *k = nullptr, *v = nullptr;
+  uint16_t* o = nullptr;
+  float* lse = nullptr;
+  const float* w_in = nullptr;
+  float* w_out = nullptr;
+  const int32_t* prefix_pages = nullptr;
+  PageTable pages;
+};
+size_t prefix_decode_workspace_bytes(const msa_shape& s, bool weights);
+cudaError_t launch_prefix_decode(const msa_shape& s, const PrefixDecodeArgs& a, void* ws,
+                                 cudaStream_t st);
+// Eviction from the own caches by accumulated weight.
+struct EvictArgs {
+  int budget = 0, n_first = 0, n_recent = 0;
+  const int32_t* lens = nullptr;
+  const float* w_in = nullptr;
+  const int32_t* pos_in = nullptr;
+  uint16_t *k = nullptr, *v = nullptr;
+  float* w_out = nullptr;
+  int32_t* pos_out = nullptr;
+  int32_t* new_lens = nullptr;
+  PageTable pages;
+};
+size_t evict_workspace_bytes(const msa_shape& s);
+cudaError_t launch_cache_evict(const msa_shape& s, const EvictArgs& a, void* ws, cudaStream_t st);
 // The bounded waits' limit of each kernel translation unit, on the current
 // device (msa_set_wait_limit_ns).
 cudaError_t set_wait_limit_decode(uint64_t ns);

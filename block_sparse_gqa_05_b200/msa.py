@@ -19,7 +19,8 @@ LIB_PATH = os.path.join(_PKG, "libmsa.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "msa.h")
 
 OP_INDEX_SCORES, OP_BLOCK_TOPK, OP_SPARSE_PREFILL, OP_SPARSE_DECODE, OP_FORWARD, \
-    OP_DENSE_PREFILL, OP_DENSE_DECODE, OP_FORWARD_ALIGNMENT, OP_FORWARD_PREFILL_PAGED = range(9)
+    OP_DENSE_PREFILL, OP_DENSE_DECODE, OP_FORWARD_ALIGNMENT, OP_FORWARD_PREFILL_PAGED, \
+    OP_PREFIX_DECODE, OP_PREFIX_DECODE_WEIGHTS, OP_CACHE_EVICT = range(12)
 
 STATUS = {0: "MSA_OK", 1: "MSA_ERR_INVALID_SHAPE", 2: "MSA_ERR_NULL_PTR", 3: "MSA_ERR_MISALIGNED",
           4: "MSA_ERR_WORKSPACE_TOO_SMALL", 5: "MSA_ERR_UNSUPPORTED", 6: "MSA_ERR_CUDA",
@@ -75,6 +76,17 @@ _SIGS = {
                                 ctypes.c_size_t, _vp], ctypes.c_int),
     "msa_dense_attn_decode": ([ctypes.POINTER(Shape), _vp, _vp, _vp, _vp, _vp, _vp,
                                ctypes.c_size_t, _vp], ctypes.c_int),
+    "msa_prefix_attn_decode": ([ctypes.POINTER(Shape), ctypes.c_int, ctypes.c_int, _vp, _vp, _vp,
+                                _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp],
+                               ctypes.c_int),
+    "msa_prefix_attn_decode_paged": ([ctypes.POINTER(Shape), ctypes.c_int, ctypes.c_int, _vp, _vp,
+                                      _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                      ctypes.c_size_t, _vp], ctypes.c_int),
+    "msa_cache_evict": ([ctypes.POINTER(Shape), ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp, _vp,
+                         _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp], ctypes.c_int),
+    "msa_cache_evict_paged": ([ctypes.POINTER(Shape), ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                               ctypes.c_int, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                               ctypes.c_size_t, _vp], ctypes.c_int),
     "msa_device_status": ([ctypes.POINTER(ctypes.c_uint32)], ctypes.c_int),
     "msa_set_wait_limit_ns": ([ctypes.c_uint64], ctypes.c_int),
     "msa_profile_enable": ([ctypes.c_int], ctypes.c_int),
@@ -119,7 +131,7 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _sizes(shape: Shape, pages: int = 0) -> dict:
+def _sizes(shape: Shape, pages: int = 0, prefix: int = 0) -> dict:
     """dtype and element count of every array argument, from the C-ABI layouts."""
     B, T, N, H, G = shape.batch, shape.seq_q, shape.seq_kv, shape.n_q_heads, shape.n_kv_heads
     d, di, k, nb = shape.head_dim, shape.index_dim, shape.topk, shape.nb
@@ -129,14 +141,18 @@ def _sizes(shape: Shape, pages: int = 0) -> dict:
             "q_idx": (bf16, B * T * G * di), "k_idx": (bf16, B * N * di),
             "pooled": (f32, B * T * G * nb), "sel": (i32, B * T * G * k),
             "lse": (f32, B * T * H), "kl": (f32, B * T * G), "seq_lens": (i32, B),
-            "page_table": (i32, B * nb), "k_pages": (bf16, pages * G * 128 * d),
-            "v_pages": (bf16, pages * G * 128 * d), "kidx_pages": (bf16, pages * 128 * di)}
+            "weights": (f32, B * G * N), "weights_out": (f32, B * G * N),
+            "positions": (i32, B * G * N), "positions_out": (i32, B * G * N),
+            "new_lens": (i32, B), "page_table": (i32, B * nb), "k_pages": (bf16, pages * G * 128 * d),
+            "v_pages": (bf16, pages * G * 128 * d), "kidx_pages": (bf16, pages * 128 * di),
+            "k_prefix": (bf16, G * prefix * d), "v_prefix": (bf16, G * prefix * d),
+            "prefix_pages": (i32, (prefix + 127) // 128)}
 
 
-def _args(shape: Shape, pages: int = 0, **tensors) -> dict:
+def _args(shape: Shape, pages: int = 0, prefix: int = 0, **tensors) -> dict:
     """Device pointers of the named tensors after checking each one's dtype and
     that it holds at least the elements its layout needs (None stays None)."""
-    need = _sizes(shape, pages)
+    need = _sizes(shape, pages, prefix)
     out = {}
     for name, t in tensors.items():
         if t is not None:
@@ -356,6 +372,133 @@ def dense_attn_decode(shape: Shape, q, k, v, o=None, lse=None, ws=None, want_lse
                                        a["lse"], *_ws(ws), _stream(stream)),
            "msa_dense_attn_decode")
     return o, lse
+
+
+def _one_device(*tensors):
+    """The device all given tensors are on (raises when there are several)."""
+    dev = tensors[0].device
+    for t in tensors[1:]:
+        if t is not None and t.device != dev:
+            raise ValueError(f"libmsa takes tensors of one device, got {dev} and {t.device}")
+    return dev
+
+
+def _call(name, dev, stream, fresh, *args):
+    """Calls a C entry point (its arguments up to the stream) on ``dev`` and the
+    given or its current stream.  ``fresh``: tensors that this call allocated,
+    kept from reuse until a stream other than the current one is done with them."""
+    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
+        with torch.cuda.device(dev):
+            return _call(name, dev, stream, fresh, *args)
+    if stream is not None:
+        for t in fresh:
+            t.record_stream(stream)
+    _check(getattr(lib(), name)(*args, _stream(stream)), name)
+
+
+def _prefix_decode(name, shape, q, seq_lens, o, lse, weights, weights_out, ws, want_lse, stream,
+                   caches, lead, order, pages, prefix):
+    """The common part of the two calls: ``lead`` the integers after the shape,
+    ``order`` the C order of the named pointers."""
+    if weights_out is None:
+        weights_out = weights
+    given = (o, lse, ws)
+    o, lse = _attn_out(shape, q, o, lse, want_lse)
+    if ws is None:
+        ws = alloc_workspace(shape, OP_PREFIX_DECODE if weights_out is None
+                             else OP_PREFIX_DECODE_WEIGHTS, q.device)
+    fresh = [t for t, had in zip((o, lse, ws), given) if had is None and t is not None]
+    dev = _one_device(q, seq_lens, o, lse, weights, weights_out, ws, *caches.values())
+    a = _args(shape, pages, prefix, q=q, seq_lens=seq_lens, o=o, lse=lse, weights=weights,
+              weights_out=weights_out, **caches)
+    _call(name, dev, stream, fresh, ctypes.byref(shape), *lead, *[a[n] for n in order], *_ws(ws))
+    return o, lse, weights_out
+
+
+def prefix_attn_decode(shape: Shape, q, k, v, seq_lens, k_prefix=None, v_prefix=None,
+                       prefix_len=None, o=None, lse=None, weights=None, weights_out=None, ws=None,
+                       want_lse=True, stream=None):
+    """msa_prefix_attn_decode: dense decode attention of a batch whose sequences
+    share the prefix k_prefix / v_prefix [G, capacity, d] (its first prefix_len
+    rows, default all; None: no prefix), over own caches k, v
+    [B, G, shape.seq_kv, d] with seq_lens int32 [B] valid rows each, the last
+    shape.seq_q of them the new tokens.  weights [B, G, shape.seq_kv] float32:
+    the softmax weight each own key received is added to it, in place or into
+    weights_out (weights_out alone starts from 0).  Returns (o, lse,
+    weights_out)."""
+    cap = 0 if k_prefix is None else int(k_prefix.shape[-2])
+    n = cap if prefix_len is None else int(prefix_len)
+    return _prefix_decode("msa_prefix_attn_decode", shape, q, seq_lens, o, lse, weights,
+                          weights_out, ws, want_lse, stream,
+                          dict(k_prefix=k_prefix, v_prefix=v_prefix, k=k, v=v), (n, cap),
+                          ("seq_lens", "q", "k_prefix", "v_prefix", "k", "v", "o", "lse",
+                           "weights", "weights_out"), 0, cap)
+
+
+def prefix_attn_decode_paged(shape: Shape, q, k_pages, v_pages, seq_lens, page_table,
+                             prefix_pages=None, prefix_len=0, o=None, lse=None, weights=None,
+                             weights_out=None, ws=None, want_lse=True, stream=None):
+    """msa_prefix_attn_decode_paged: prefix_attn_decode over paged caches.
+    k_pages / v_pages [P, G, 128, d] bf16; prefix_pages int32
+    [ceil(prefix_len / 128)] lists the prefix's pages, page_table int32
+    [B, ceil(shape.seq_kv / 128)] those of the own caches."""
+    n, P = int(prefix_len), int(k_pages.shape[0])
+    return _prefix_decode("msa_prefix_attn_decode_paged", shape, q, seq_lens, o, lse, weights,
+                          weights_out, ws, want_lse, stream,
+                          dict(prefix_pages=prefix_pages, page_table=page_table, k_pages=k_pages,
+                               v_pages=v_pages), (P, n),
+                          ("prefix_pages", "seq_lens", "page_table", "q", "k_pages", "v_pages",
+                           "o", "lse", "weights", "weights_out"), P, n)
+
+
+def _cache_evict(name, shape, k, v, seq_lens, weights, positions, weights_out, positions_out,
+                 new_lens, ws, stream, caches, lead, order, pages=0):
+    fresh = []
+    if weights_out is None:
+        weights_out = weights
+    if positions_out is None:
+        positions_out = positions
+    if new_lens is None:
+        new_lens = torch.empty_like(seq_lens)
+        fresh.append(new_lens)
+    if ws is None:
+        ws = alloc_workspace(shape, OP_CACHE_EVICT, k.device)
+        fresh.append(ws)
+    dev = _one_device(k, v, seq_lens, weights, positions, weights_out, positions_out, new_lens,
+                      ws, *caches.values())
+    a = _args(shape, pages, seq_lens=seq_lens, weights=weights, positions=positions,
+              weights_out=weights_out, positions_out=positions_out, new_lens=new_lens, **caches)
+    _call(name, dev, stream, fresh, ctypes.byref(shape), *lead, *[a[n] for n in order], *_ws(ws))
+    return weights_out, positions_out, new_lens
+
+
+def cache_evict(shape: Shape, k, v, seq_lens, weights, positions, budget, first=0, recent=0,
+                weights_out=None, positions_out=None, new_lens=None, ws=None, stream=None):
+    """msa_cache_evict: every (sequence, group) of the own caches k, v
+    [B, G, shape.seq_kv, d] keeps its ``budget`` rows of largest weight; rows
+    with positions < first, or among the ``recent`` highest positions, come
+    before all others.  k, v are compacted in place; weights and positions
+    [B, G, shape.seq_kv] too unless weights_out / positions_out are given.
+    Returns (weights_out, positions_out, new_lens)."""
+    return _cache_evict("msa_cache_evict", shape, k, v, seq_lens, weights, positions, weights_out,
+                        positions_out, new_lens, ws, stream, dict(k=k, v=v),
+                        (int(budget), int(first), int(recent)),
+                        ("seq_lens", "weights", "positions", "k", "v", "weights_out",
+                         "positions_out", "new_lens"))
+
+
+def cache_evict_paged(shape: Shape, k_pages, v_pages, seq_lens, page_table, weights, positions,
+                      budget, first=0, recent=0, weights_out=None, positions_out=None,
+                      new_lens=None, ws=None, stream=None):
+    """msa_cache_evict_paged: cache_evict over paged caches k_pages / v_pages
+    [P, G, 128, d] with page_table int32 [B, ceil(shape.seq_kv / 128)]."""
+    P = int(k_pages.shape[0])
+    return _cache_evict("msa_cache_evict_paged", shape, k_pages, v_pages, seq_lens, weights,
+                        positions, weights_out, positions_out, new_lens, ws, stream,
+                        dict(page_table=page_table, k_pages=k_pages, v_pages=v_pages),
+                        (P, int(budget), int(first), int(recent)),
+                        ("seq_lens", "page_table", "weights", "positions", "k_pages", "v_pages",
+                         "weights_out", "positions_out", "new_lens"), P)
 
 
 def profile_enable(on: bool = True):

@@ -38,6 +38,8 @@
  *   kl       [B, T, G]      float32 (alignment divergence, msa_forward_alignment)
  *   paged decode caches: k, v [P, G, 128, d], k_idx [P, 128, d_i] bf16 with
  *   a page table [B, nb] int32 (msa_forward_decode_paged)
+ *   weights  [B, G, N]      float32     positions [B, G, N]  int32
+ *   (per-key state of msa_prefix_attn_decode and msa_cache_evict)
  *
  * Ownership: the caller allocates every buffer (device memory unless stated)
  * and the optional workspace.  The library never allocates or frees device
@@ -104,7 +106,10 @@ typedef enum msa_op {
   MSA_OP_DENSE_PREFILL = 5,
   MSA_OP_DENSE_DECODE = 6,
   MSA_OP_FORWARD_ALIGNMENT = 7,
-  MSA_OP_FORWARD_PREFILL_PAGED = 8
+  MSA_OP_FORWARD_PREFILL_PAGED = 8,
+  MSA_OP_PREFIX_DECODE = 9,           /* msa_prefix_attn_decode(_paged), weights_out == NULL */
+  MSA_OP_PREFIX_DECODE_WEIGHTS = 10,  /* the same with weights_out */
+  MSA_OP_CACHE_EVICT = 11             /* msa_cache_evict(_paged) */
 } msa_op;
 
 /* Human-readable name of a status code (static string, never NULL). */
@@ -310,8 +315,108 @@ msa_status msa_sparse_attn_decode_static(const msa_shape* shape, const uint16_t*
                                          const int32_t* sel, uint16_t* o, float* lse,
                                          void* stream);
 
+/* Dense decode attention for a batch whose sequences share a prefix, over own
+ * caches of different lengths (serving; no counterpart on the pages).  The
+ * prefix is attended by all sequences at once: its K/V are read once for the
+ * batch (per 256 query rows of a group), not once per sequence.
+ *   q, o     [B, T, H, d]           T new tokens per sequence, T * r <= 128
+ *   k_prefix, v_prefix [G, prefix_cap, d] bf16, rows 0 .. prefix_len-1 valid,
+ *            seen by every query; NULL when prefix_len == 0
+ *   k, v     [B, G, N, d]           own caches, N = shape.seq_kv the capacity
+ *   seq_lens [B] int32 (device, 4-byte aligned), each in [0, N]: own rows that
+ *            are valid, the T new tokens (already appended) being the last
+ *            ones: query t of sequence b sees own rows x <= seq_lens[b] - T + t
+ *   o   = sum over the prefix and the own rows seen of
+ *         softmax(q . k / sqrt(d)) v;  lse [B, T, H] the natural-log
+ *         normaliser (may be NULL).  A query that sees no key gets o = 0,
+ *         lse = -inf.
+ * With weights_out != NULL the softmax weight that each own key received is
+ * added to a running score per key and group:
+ *   weights_out[b,g,x] = weights[b,g,x] + sum over t and the heads h of group
+ *                        g of exp(q[b,t,h] . k[b,g,x] / sqrt(d) - lse[b,t,h])
+ * for x < seq_lens[b]; entries at or past seq_lens[b] are neither read nor
+ * written.  weights may be NULL (taken as 0) or equal to weights_out (update
+ * in place); they must not overlap otherwise.
+ * shape.q_offset is ignored.  Rows past a length (prefix or own) may hold any
+ * bits.  A length outside [0, N] is clamped into it and sets bit 1 of the
+ * device error word.  Softmax statistics, partial outputs and scores are held
+ * in fp32; the softmax weights are rounded to bf16 only as the operand of the
+ * product with V.  Results do not depend on timing (no atomics).
+ * ws >= msa_workspace_size(MSA_OP_PREFIX_DECODE, or
+ * MSA_OP_PREFIX_DECODE_WEIGHTS with weights_out); the size does not depend on
+ * the prefix.  Calls that can overlap need workspaces of their own.
+ * Errors: T > N, prefix_len < 0 or > prefix_cap -> MSA_ERR_INVALID_SHAPE;
+ * T * r > 128, G * prefix_cap >= 2^31 -> MSA_ERR_UNSUPPORTED; weights without
+ * weights_out -> MSA_ERR_NULL_PTR. */
+msa_status msa_prefix_attn_decode(const msa_shape* shape, int prefix_len, int prefix_cap,
+                                  const int32_t* seq_lens, const uint16_t* q,
+                                  const uint16_t* k_prefix, const uint16_t* v_prefix,
+                                  const uint16_t* k, const uint16_t* v, uint16_t* o, float* lse,
+                                  const float* weights, float* weights_out, void* ws,
+                                  size_t ws_bytes, void* stream);
+
+/* The same over paged caches: k, v [num_pages, G, 128, d]; prefix_pages
+ * [ceil(prefix_len / 128)] int32 lists the pages of the prefix (NULL when
+ * prefix_len == 0), page_table [B, nb] those of the own caches, nb =
+ * ceil(seq_kv / 128); only entries of valid rows are read.  weights stay
+ * [B, G, N].  A page id outside [0, num_pages) is clamped into it (results
+ * that read that block are then wrong) and sets bit 2 of the device error
+ * word.  Errors as above, and num_pages < 1 -> MSA_ERR_INVALID_SHAPE;
+ * num_pages * G or num_pages * 128 >= 2^31 -> MSA_ERR_UNSUPPORTED. */
+msa_status msa_prefix_attn_decode_paged(const msa_shape* shape, int num_pages, int prefix_len,
+                                        const int32_t* prefix_pages, const int32_t* seq_lens,
+                                        const int32_t* page_table, const uint16_t* q,
+                                        const uint16_t* k, const uint16_t* v, uint16_t* o,
+                                        float* lse, const float* weights, float* weights_out,
+                                        void* ws, size_t ws_bytes, void* stream);
+
+/* Eviction from the own caches by accumulated attention weight (serving; no
+ * counterpart on the pages).  Every (sequence, group) keeps n =
+ * min(seq_lens[b], budget) rows, the first n under the order
+ *   (rows that always stay, weight descending, row ascending),
+ * where a row always stays (before every other one) when positions < n_first
+ * or positions > (largest position of its (sequence, group)) - n_recent; a
+ * NaN weight counts as the lowest, -0 as 0.  The cache is compacted in place
+ * by moving as few rows as possible: the kept rows x >= n, ascending, go to
+ * the dropped rows x < n, ascending; every other kept row stays where it is.
+ *   k, v           [B, G, N, d], rows of the moved keys are overwritten; rows
+ *                  at or past n keep their bits
+ *   weights_out, positions_out [B, G, N]: weight and position of the row now
+ *                  in x for x < n; 0 and -1 for n <= x < seq_lens[b] (a row
+ *                  appended there starts at weight 0); untouched past that.
+ *                  Each may equal its input (in place) and must not overlap
+ *                  the inputs or each other otherwise.
+ *   new_lens       [B] int32, receives n; must not be seq_lens itself
+ * The attention is the same for any order of the rows before the new tokens,
+ * so msa_prefix_attn_decode runs on the compacted cache with new_lens.
+ * Positions are whatever increasing numbers the caller gives its rows.  With
+ * the same weights, positions and lengths a repeated call moves the same rows.
+ * shape.seq_q, q_offset, n_q_heads, topk and index_dim are only validated.
+ * A length outside [0, N] is clamped into it and sets bit 1 of the device
+ * error word.  ws >= msa_workspace_size(MSA_OP_CACHE_EVICT).
+ * Errors: budget < 1, n_first < 0, n_recent < 0 -> MSA_ERR_INVALID_SHAPE;
+ * overlapping arrays -> MSA_ERR_UNSUPPORTED. */
+msa_status msa_cache_evict(const msa_shape* shape, int budget, int n_first, int n_recent,
+                           const int32_t* seq_lens, const float* weights,
+                           const int32_t* positions, uint16_t* k, uint16_t* v,
+                           float* weights_out, int32_t* positions_out, int32_t* new_lens,
+                           void* ws, size_t ws_bytes, void* stream);
+
+/* The same over paged caches: k, v [num_pages, G, 128, d], page_table
+ * [B, nb] int32.  Pages past ceil(n / 128) come free.  No page may be listed
+ * twice among the entries of valid rows (a shared prefix belongs in
+ * prefix_pages, not in the tables).  A row whose page id lies outside
+ * [0, num_pages) is not moved in k and v, and sets bit 2 of the device error
+ * word.  Errors as above, and num_pages as in msa_prefix_attn_decode_paged. */
+msa_status msa_cache_evict_paged(const msa_shape* shape, int num_pages, int budget, int n_first,
+                                 int n_recent, const int32_t* seq_lens,
+                                 const int32_t* page_table, const float* weights,
+                                 const int32_t* positions, uint16_t* k, uint16_t* v,
+                                 float* weights_out, int32_t* positions_out, int32_t* new_lens,
+                                 void* ws, size_t ws_bytes, void* stream);
+
 /* Reads and clears the device error word of the current device (bit 0: a
- * bounded wait timed out; bit 1: a ragged-decode cache length was out of
+ * bounded wait timed out; bit 1: a cache length was out of
  * range; bit 2: a page-table entry was out of range; bit 3: a prefill
  * selection entry lay past its query's block).  Synchronises the current
  * device.  Returns MSA_ERR_DEVICE_TIMEOUT if any bit was set, MSA_OK

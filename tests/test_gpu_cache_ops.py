@@ -1,0 +1,533 @@
+"""GPU parity of the shared-prefix decode attention and of the eviction by
+accumulated weight, through the public calls, against float64 oracles.
+
+Tolerances of the attention, derived per element (no fitted constants):
+* a logit is a sum of d products of bf16 values accumulated in fp32 (tensor
+  cores may truncate: one whole unit per term), scaled and exponentiated in
+  fp32: |ds| <= delta = (d + 8) 2^-23 reach + 2^-20, reach the largest
+  sum |q k| / sqrt(d) of a seen key;
+* hence |d lse| <= delta + (n + 8) 2^-23 (n keys summed in fp32) + |lse| 2^-23;
+* a softmax weight p has relative error <= delta + |d lse| + 2^-22;
+* in o = sum p v every p is also rounded to bf16 (2^-8 relative) before the
+  product and o once after it: |do| <= (2^-8 + error of p + (n + 8) 2^-23)
+  sum p |v| + 2^-8 (|o| + that);
+* a score adds T r of them to the old one: |dw| <= (error of p) sum p + T r 2^-23 |w|.
+"""
+import numpy as np
+import pytest
+import torch
+
+import block_sparse_gqa_05_b200 as M
+from oracle import cache_oracle as CO
+
+pytestmark = pytest.mark.gpu
+NAN = float("nan")
+
+
+def mshape(B, T, H, G, d, C):
+    return M.Shape(B, T, C, 0, H, G, d, 64, 128, 4)
+
+
+class Case:
+    """Inputs on the CPU; rows past a length hold NaN and Inf in K and V."""
+
+    def __init__(self, B, T, H, G, d, Np, C, lens, seed=0, slack=0, scale=2.0):
+        g = torch.Generator().manual_seed(1000 + seed)
+        bf = torch.bfloat16
+        self.B, self.T, self.H, self.G, self.d, self.Np, self.C, self.lens = B, T, H, G, d, Np, C, lens
+        self.q = (torch.randn(B, T, H, d, generator=g) * scale).to(bf)
+        self.k, self.v = (torch.randn(B, G, C, d, generator=g).to(bf) for _ in range(2))
+        self.kp, self.vp = (torch.randn(G, Np + slack, d, generator=g).to(bf) for _ in range(2))
+        for b, n in enumerate(lens):
+            self.k[b, :, max(n, 0):] = NAN
+            self.v[b, :, max(n, 0):] = NAN
+            self.v[b, :, max(n, 0) + 1:] = float("inf")
+        self.kp[:, Np:], self.vp[:, Np:] = NAN, NAN
+        self.w = torch.rand(B, G, C, generator=g)
+        self.shape = mshape(B, T, H, G, d, C)
+        self.seed = seed
+
+    def oracle(self):
+        lens = [min(max(n, 0), self.C) for n in self.lens]
+        return CO.prefix_attention(self.q, self.kp[:, :self.Np], self.vp[:, :self.Np], self.k, self.v, lens,
+                                   self.w)
+
+    def dev(self, x):
+        return x.contiguous().cuda()
+
+    def run(self, scored=True, **kw):
+        kw = dict(kw)
+        if scored:
+            kw.setdefault("weights", self.dev(self.w))
+            kw.setdefault("weights_out", torch.full_like(kw["weights"], -7.0))
+        lens = torch.tensor(self.lens, dtype=torch.int32).cuda()
+        pre = {}
+        if self.kp.shape[1]:
+            pre = dict(k_prefix=self.dev(self.kp), v_prefix=self.dev(self.vp), prefix_len=self.Np)
+        return M.prefix_attn_decode(self.shape, self.dev(self.q), self.dev(self.k), self.dev(self.v), lens,
+                                    **pre, **kw)
+
+    def paged(self):
+        """Pools with shuffled pages, unused pages NaN, table entries past each length -1."""
+        B, G, d, C, Np = self.B, self.G, self.d, self.C, self.Np
+        nb, npb = -(-C // 128), -(-Np // 128)
+        P = B * nb + npb + 3
+        perm = np.random.default_rng(self.seed).permutation(P)
+        kp, vp = (torch.full((P, G, 128, d), NAN, dtype=torch.bfloat16) for _ in range(2))
+        table = np.full((B, nb), -1, dtype=np.int32)
+        for b, n in enumerate(self.lens):
+            for j in range(-(-n // 128)):
+                pg = table[b, j] = perm[b * nb + j]
+                r1 = min((j + 1) * 128, C)
+                kp[pg, :, :r1 - j * 128], vp[pg, :, :r1 - j * 128] = \
+                    self.k[b, :, j * 128:r1], self.v[b, :, j * 128:r1]
+        pages = perm[B * nb:B * nb + npb].astype(np.int32)
+        for j, pg in enumerate(pages):
+            r1 = min((j + 1) * 128, Np)
+            kp[pg, :, :r1 - j * 128], vp[pg, :, :r1 - j * 128] = \
+                self.kp[:, j * 128:r1], self.vp[:, j * 128:r1]
+        return kp, vp, table, pages
+
+    def run_paged(self, tables=None, **kw):
+        kp, vp, table, pages = tables or self.paged()
+        kw["weights"] = self.dev(self.w)
+        kw["weights_out"] = torch.full_like(kw["weights"], -7.0)
+        lens = torch.tensor(self.lens, dtype=torch.int32).cuda()
+        return M.prefix_attn_decode_paged(self.shape, self.dev(self.q), self.dev(kp), self.dev(vp), lens,
+                                          torch.from_numpy(table).cuda(), torch.from_numpy(pages).cuda(),
+                                          self.Np, **kw)
+
+    def check(self, o, lse, w, ref=None, skip=()):
+        ro, rl, rw, absum, reach = ref or self.oracle()
+        n = self.Np + max([1] + [min(max(x, 0), self.C) for x in self.lens])
+        r = self.H // self.G
+        delta = (self.d + 8) * 2.0**-23 * reach + 2.0**-20
+        dl = delta + (n + 8) * 2.0**-23 + np.where(np.isfinite(rl), np.abs(rl), 0) * 2.0**-23
+        dp = delta + dl + 2.0**-22
+        do = (2.0**-8 + dp[..., None] + (n + 8) * 2.0**-23) * absum
+        do = do + 2.0**-8 * (np.abs(ro) + do)
+        rows = [b for b in range(self.B) if b not in skip]
+        go, gl = o.double().cpu().numpy(), None if lse is None else lse.double().cpu().numpy()
+        for b in rows:
+            err = np.abs(go[b] - ro[b])
+            assert np.all(err <= do[b]), f"o of {b}: {err.max():.3g}, {np.nanmax(err - do[b]):.3g} over"
+            if gl is not None:
+                assert np.array_equal(np.isneginf(gl[b]), np.isneginf(rl[b]))
+                fin = np.isfinite(rl[b])
+                err = np.abs(gl[b][fin] - rl[b][fin])
+                assert np.all(err <= dl[b][fin]), f"lse of {b}: {err.max():.3g}"
+        if w is None:
+            return
+        gw = w.double().cpu().numpy()
+        for b in rows:
+            ln = min(max(self.lens[b], 0), self.C)
+            for g in range(self.G):
+                e = dp[b, :, g * r:(g + 1) * r].max()
+                add = rw[b, g, :ln] - self.w[b, g, :ln].double().numpy()
+                tol = e * add + (self.T * r + 2) * 2.0**-23 * rw[b, g, :ln] + 1e-12
+                err = np.abs(gw[b, g, :ln] - rw[b, g, :ln])
+                assert np.all(err <= tol), f"weights of {b}, {g}: {err.max():.3g}, {(err - tol).max():.3g} over"
+                assert np.all(gw[b, g, ln:] == -7.0), "a score past the length was written"
+
+
+CASES = [
+    # one block, one sequence, the smallest sizes
+    dict(B=1, T=1, H=1, G=1, d=64, Np=0, C=1, lens=[1]),
+    dict(B=1, T=1, H=2, G=1, d=128, Np=1, C=1, lens=[0]),
+    dict(B=2, T=1, H=8, G=2, d=64, Np=200, C=96, lens=[90, 1]),
+    # ragged own caches with empty and full ones, lengths around the block size
+    dict(B=9, T=1, H=16, G=2, d=128, Np=300, C=300, lens=[0, 1, 2, 127, 128, 129, 255, 256, 300], slack=5),
+    # every ratio of heads to groups
+    dict(B=3, T=1, H=4, G=4, d=64, Np=129, C=140, lens=[1, 130, 140]),
+    dict(B=3, T=2, H=8, G=4, d=128, Np=128, C=140, lens=[2, 130, 140]),
+    dict(B=2, T=3, H=16, G=4, d=64, Np=127, C=131, lens=[3, 131]),
+    dict(B=2, T=1, H=32, G=2, d=128, Np=515, C=257, lens=[17, 257]),
+    # drafted tokens: fewer own rows than new tokens, causal among the new ones
+    dict(B=5, T=5, H=8, G=1, d=128, Np=0, C=200, lens=[0, 2, 5, 133, 200]),
+    dict(B=4, T=16, H=8, G=1, d=64, Np=260, C=270, lens=[16, 3, 128, 270]),     # 128 rows a sequence
+    dict(B=2, T=128, H=1, G=1, d=128, Np=70, C=400, lens=[400, 131]),
+    dict(B=2, T=8, H=16, G=1, d=128, Np=1000, C=130, lens=[130, 129]),
+    # one row tile and one row over, several tiles, an odd number of tiles
+    dict(B=16, T=1, H=8, G=1, d=64, Np=1000, C=40, lens=list(range(16))),
+    dict(B=17, T=1, H=8, G=1, d=128, Np=700, C=40, lens=list(range(17))),
+    dict(B=33, T=1, H=16, G=2, d=64, Np=390, C=40, lens=list(range(33))),
+    dict(B=50, T=1, H=8, G=1, d=128, Np=256, C=17, lens=[i % 18 for i in range(50)]),
+    # more work than one block per SM, long own caches, no prefix
+    dict(B=6, T=1, H=16, G=4, d=128, Np=0, C=3000, lens=[3000, 5, 0, 1234, 2999, 128]),
+    dict(B=3, T=2, H=8, G=2, d=64, Np=9000, C=2100, lens=[2100, 2, 1]),
+    dict(B=200, T=1, H=4, G=2, d=64, Np=64, C=9, lens=[i % 10 for i in range(200)]),
+]
+
+
+@pytest.mark.parametrize("i", range(len(CASES)))
+def test_prefix_attention(i):
+    c = Case(seed=i, **CASES[i])
+    o, lse, w = c.run()
+    torch.cuda.synchronize()
+    assert M.device_status() == 0
+    c.check(o, lse, w)
+    # without the scores, the same outputs; without lse too
+    o2, lse2, none = c.run(scored=False)
+    assert none is None and torch.equal(o, o2) and torch.equal(lse, lse2)
+    o3, none, _ = c.run(scored=False, want_lse=False)
+    assert none is None and torch.equal(o, o3)
+
+
+@pytest.mark.parametrize("i", [2, 3, 6, 8, 9, 13, 16, 17])
+def test_paged_caches_give_the_contiguous_result(i):
+    c = Case(seed=50 + i, **CASES[i])
+    o, lse, w = c.run()
+    op, lp, wp = c.run_paged()
+    torch.cuda.synchronize()
+    assert M.device_status() == 0                     # no entry past a length was read
+    assert torch.equal(o, op) and torch.equal(lse, lp) and torch.equal(w, wp)
+    c.check(op, lp, wp)
+
+
+def test_scores_in_place_and_from_zero():
+    c = Case(seed=70, **CASES[3])
+    _, _, w = c.run()
+    mine = c.dev(c.w)
+    _, _, same = c.run(weights=mine, weights_out=mine)
+    live = torch.arange(c.C)[None, None] < torch.tensor(c.lens)[:, None, None]
+    live = live.expand(c.B, c.G, c.C).cuda()
+    assert same is mine and torch.equal(mine[live], w[live])
+    assert torch.equal(mine[~live].cpu(), c.w[~live.cpu()])       # untouched past each length
+    zero = torch.full_like(mine, NAN)
+    sh, lens = c.shape, torch.tensor(c.lens, dtype=torch.int32).cuda()
+    _, _, z = M.prefix_attn_decode(sh, c.dev(c.q), c.dev(c.k), c.dev(c.v), lens, c.dev(c.kp), c.dev(c.vp),
+                                   prefix_len=c.Np, weights_out=zero)
+    got = z[live].double() + c.w[live.cpu()].cuda().double()
+    assert torch.allclose(got, w[live].double(), rtol=2e-7, atol=1e-7) and torch.isnan(z[~live]).all()
+
+
+def test_large_logits_and_equal_logits():
+    # logits of several hundred: the running maximum moves by far more than fp32's range of exp
+    c = Case(B=3, T=1, H=8, G=2, d=64, Np=700, C=300, lens=[300, 1, 129], seed=71, scale=60.0)
+    c.check(*c.run())
+    # all keys equal: every weight is 1 / n
+    c = Case(B=2, T=2, H=8, G=1, d=128, Np=333, C=260, lens=[260, 7], seed=72)
+    c.k[:, :, :], c.kp[:, :c.Np] = c.k[0, 0, 0], c.k[0, 0, 0]
+    c.check(*c.run())
+    # keys that rise along the cache: the maximum grows in every block
+    c = Case(B=1, T=1, H=4, G=1, d=64, Np=2000, C=900, lens=[900], seed=73)
+    c.kp[:] = (torch.arange(c.Np)[None, :, None] / c.Np * 3).to(torch.bfloat16)
+    c.k[:] = (3 + torch.arange(c.C)[None, None, :, None] / c.C * 3).to(torch.bfloat16)
+    c.q[:] = 2.0
+    c.check(*c.run())
+
+
+def test_repeated_calls_are_bit_identical():
+    c = Case(B=20, T=1, H=32, G=4, d=128, Np=5000, C=700, lens=[37 * i % 701 for i in range(20)], seed=74)
+    first = c.run()
+    for _ in range(3):
+        again = c.run()
+        assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
+def test_bad_lengths_are_clamped_and_flagged():
+    c = Case(B=3, T=1, H=8, G=2, d=64, Np=50, C=200, lens=[-4, 200, 60], seed=75)
+    given = c.lens
+    c.lens = [-4, 777, 60]
+    o, lse, w = c.run()
+    assert M.device_status() == 2
+    c.lens = given
+    c.check(o, lse, w)
+
+
+def test_bad_pages_are_flagged():
+    c = Case(B=3, T=1, H=8, G=2, d=64, Np=300, C=300, lens=[300, 200, 60], seed=76)
+    kp, vp, table, pages = c.paged()
+    table[0, 1] = kp.shape[0] + 5
+    o, lse, w = c.run_paged(tables=(kp, vp, table, pages))
+    assert M.device_status() == 4
+    c.check(o, lse, w, skip=(0,))
+    table[0, 1] = -3
+    c.run_paged(tables=(kp, vp, table, pages))
+    assert M.device_status() == 4
+
+
+# ------------------------------------------------------------------ eviction
+
+def scores(kind, B, G, C, g):
+    if kind == "ties":
+        return torch.randint(0, 4, (B, G, C), generator=g).float()
+    if kind == "equal":
+        return torch.full((B, G, C), 0.25)
+    if kind == "odd":                      # NaN, infinities, signed zeros, denormals, negatives
+        pool = torch.tensor([NAN, -NAN, float("inf"), -float("inf"), 0.0, -0.0, 1e-42, -1e-42, 1.0, -1.0,
+                             3.4e38, -3.4e38])
+        return pool[torch.randint(0, len(pool), (B, G, C), generator=g)]
+    if kind == "close":                    # neighbouring floats
+        return (torch.randint(0, 40, (B, G, C), generator=g) + 0x3f800000).to(torch.int32).view(torch.float32)
+    return torch.exp(2 * torch.randn(B, G, C, generator=g))
+
+
+class Cache:
+    def __init__(self, B, G, d, C, lens, kind="tail", shuffled=False, seed=0):
+        g = torch.Generator().manual_seed(2000 + seed)
+        self.B, self.G, self.d, self.C, self.lens = B, G, d, C, lens
+        self.k, self.v = (torch.randn(B, G, C, d, generator=g).to(torch.bfloat16) for _ in range(2))
+        self.w = scores(kind, B, G, C, g)
+        pos = torch.cumsum(torch.randint(1, 3, (B, G, C), generator=g), -1).to(torch.int32) - 1
+        if shuffled:
+            for b, n in enumerate(lens):
+                for x in range(G):
+                    p = torch.randperm(n, generator=g)
+                    pos[b, x, :n] = pos[b, x, :n][p]
+        self.pos = pos
+        self.shape = M.Shape(B, 1, C, C - 1, G, G, d, 64, 128, 4)
+        self.seed = seed
+
+    def dev(self, x):
+        return x.contiguous().cuda()
+
+    def run(self, budget, first=0, recent=0, in_place=False, **kw):
+        k, v, w, pos = (self.dev(x) for x in (self.k, self.v, self.w, self.pos))
+        if not in_place:
+            kw.update(weights_out=torch.full_like(w, -7.0), positions_out=torch.full_like(pos, -7))
+        lens = torch.tensor(self.lens, dtype=torch.int32).cuda()
+        wo, po, new = M.cache_evict(self.shape, k, v, lens, w, pos, budget, first=first, recent=recent, **kw)
+        torch.cuda.synchronize()
+        if not in_place:
+            assert torch.equal(w.view(torch.int32).cpu(), self.w.view(torch.int32))
+            assert torch.equal(pos.cpu(), self.pos)
+        return k, v, wo, po, new
+
+    def check(self, got, budget, first, recent, in_place=False):
+        k, v, wo, po, new = (x.cpu() for x in got)
+        lens = [min(max(n, 0), self.C) for n in self.lens]
+        rk, rv, rw, rp, rn = CO.evict(self.k, self.v, self.w.numpy(), self.pos.numpy(), lens, budget, first,
+                                      recent)
+        assert np.array_equal(new.numpy(), rn)
+        if not in_place:
+            for b, n in enumerate(lens):
+                rw[b, :, n:], rp[b, :, n:] = -7.0, -7
+        assert np.array_equal(po.numpy(), rp)
+        assert np.array_equal(wo.numpy().view(np.int32), np.ascontiguousarray(rw).view(np.int32))
+        assert torch.equal(k.view(torch.int16), rk.view(torch.int16))
+        assert torch.equal(v.view(torch.int16), rv.view(torch.int16))
+
+
+EVICT = [
+    (dict(B=1, G=1, d=64, C=1, lens=[1]), 1, 0, 0),
+    (dict(B=3, G=1, d=64, C=2, lens=[0, 1, 2]), 1, 0, 0),
+    (dict(B=2, G=2, d=128, C=300, lens=[300, 299]), 256, 4, 32),
+    (dict(B=4, G=2, d=64, C=130, lens=[130, 0, 64, 65], kind="ties", shuffled=True), 64, 2, 10),
+    (dict(B=2, G=1, d=128, C=1000, lens=[1000, 999], kind="equal", shuffled=True), 400, 0, 0),
+    (dict(B=2, G=4, d=64, C=777, lens=[777, 500], kind="odd"), 333, 3, 3),
+    (dict(B=2, G=2, d=64, C=2050, lens=[2050, 2049], kind="close", shuffled=True), 2048, 16, 100),
+    (dict(B=2, G=2, d=64, C=600, lens=[600, 555]), 100, 50, 80),       # more rows stay than the budget
+    (dict(B=2, G=2, d=64, C=600, lens=[600, 555], kind="ties"), 100, 1 << 20, 0),
+    (dict(B=2, G=2, d=64, C=600, lens=[600, 555], kind="ties"), 100, 0, 1 << 30),
+    (dict(B=2, G=2, d=64, C=600, lens=[600, 555]), 600, 0, 0),         # nothing to drop
+    (dict(B=1, G=2, d=128, C=9000, lens=[8999], shuffled=True), 1, 0, 0),
+    (dict(B=3, G=2, d=64, C=5000, lens=[5000, 4097, 100], shuffled=True), 4096, 4, 256),
+    (dict(B=1, G=1, d=64, C=40001, lens=[40000], kind="ties"), 10000, 4, 999),
+    (dict(B=1, G=2, d=64, C=70000, lens=[69999], shuffled=True), 35001, 64, 4096),
+    (dict(B=40, G=8, d=64, C=150, lens=[(7 * i) % 151 for i in range(40)], kind="ties"), 70, 1, 5),
+]
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("i", range(len(EVICT)))
+def test_evict(i, in_place):
+    c, budget, first, recent = EVICT[i]
+    c = Cache(seed=i, **c)
+    got = c.run(budget, first, recent, in_place)
+    assert M.device_status() == 0
+    c.check(got, budget, first, recent, in_place)
+
+
+def test_evict_again_moves_the_same_rows():
+    c = Cache(B=2, G=2, d=64, C=900, lens=[900, 700], seed=30)
+    k, v, w, pos = (c.dev(x) for x in (c.k, c.v, c.w, c.pos))
+    lens = torch.tensor(c.lens, dtype=torch.int32).cuda()
+    for _ in range(2):
+        wo, po, new = M.cache_evict(c.shape, k, v, lens, w, pos, 300, 4, 20,
+                                    weights_out=torch.full_like(w, -7.0),
+                                    positions_out=torch.full_like(pos, -7))
+        torch.cuda.synchronize()
+        c.check((k, v, wo, po, new), 300, 4, 20)
+
+
+@pytest.mark.parametrize("i", [2, 3, 6, 12, 15])
+def test_evict_paged(i):
+    c, budget, first, recent = EVICT[i]
+    c = Cache(seed=40 + i, **c)
+    nb = -(-c.C // 128)
+    P = c.B * nb + 2
+    perm = np.random.default_rng(i).permutation(P)
+    table = perm[:c.B * nb].reshape(c.B, nb).astype(np.int32)
+    pools = [torch.full((P, c.G, 128, c.d), 3.0, dtype=torch.bfloat16) for _ in range(2)]
+    for pool, x in zip(pools, (c.k, c.v)):
+        for b in range(c.B):
+            for j in range(nb):
+                r1 = min((j + 1) * 128, c.C)
+                pool[table[b, j], :, :r1 - j * 128] = x[b, :, j * 128:r1]
+    for b, n in enumerate(c.lens):
+        table[b, -(-n // 128):] = -1                  # never read
+    kp, vp, w, pos = (c.dev(x) for x in (*pools, c.w, c.pos))
+    lens = torch.tensor(c.lens, dtype=torch.int32).cuda()
+    wo, po, new = M.cache_evict_paged(c.shape, kp, vp, lens, torch.from_numpy(table).cuda(), w, pos, budget,
+                                      first, recent, weights_out=torch.full_like(w, -7.0),
+                                      positions_out=torch.full_like(pos, -7))
+    torch.cuda.synchronize()
+    assert M.device_status() == 0
+    back = []
+    for pool, x in ((kp, c.k), (vp, c.v)):
+        y = x.clone()
+        for b, n in enumerate(c.lens):
+            for j in range(-(-n // 128)):
+                r1 = min((j + 1) * 128, c.C)
+                y[b, :, j * 128:r1] = pool[table[b, j], :, :r1 - j * 128].cpu()
+        back.append(y)
+    c.check((*back, wo, po, new), budget, first, recent)
+    free = torch.tensor(sorted(set(range(P)) - set(table[table >= 0].tolist())))
+    for pool, old in ((kp, pools[0]), (vp, pools[1])):
+        assert torch.equal(pool.cpu()[free], old[free])            # pages of nobody keep their bits
+
+
+def test_evict_bad_lengths_and_pages_are_flagged():
+    c = Cache(B=3, G=2, d=64, C=300, lens=[300, 0, 200], seed=45)
+    c.lens = [301, -1, 200]
+    got = c.run(100, 2, 9)
+    assert M.device_status() == 2
+    c.lens = [300, 0, 200]
+    c.check(got, 100, 2, 9)
+    # a page that does not exist: its rows stay where they are, everything else moves
+    nb, P = 3, 9
+    table = np.arange(P, dtype=np.int32).reshape(3, nb)
+    pool = torch.zeros(P, 2, 128, 64, dtype=torch.bfloat16)
+    for b in range(3):
+        for j in range(nb):
+            r1 = min((j + 1) * 128, 300)
+            pool[b * nb + j, :, :r1 - j * 128] = c.k[b, :, j * 128:r1]
+    bad = table.copy()
+    bad[0, 2] = P + 1
+    kp, vp = c.dev(pool), c.dev(pool)
+    w, pos = c.dev(c.w), c.dev(c.pos)
+    _, po, new = M.cache_evict_paged(c.shape, kp, vp, torch.tensor(c.lens, dtype=torch.int32).cuda(),
+                                     torch.from_numpy(bad).cuda(), w, pos, 100, 2, 9)
+    torch.cuda.synchronize()
+    assert M.device_status() == 4 and new.tolist() == [100, 0, 100]
+    got, old = kp.cpu(), c.k
+    for b in (0, 2):
+        for g in range(2):
+            frm, to = CO.evict_plan(c.w[b, g].numpy(), c.pos[b, g].numpy(), c.lens[b], 100, 2, 9)
+            for f, t in zip(frm, to):
+                ref = old[b, g, t] if b == 0 and f >= 256 else old[b, g, f]
+                assert torch.equal(got[b * nb + t // 128, g, t % 128], ref)
+
+
+# ------------------------------------------------- both together, as a loop runs them
+
+def _loop_inputs(seed=90):
+    return Case(B=5, T=1, H=16, G=4, d=64, Np=260, C=200, lens=[1, 190, 128, 77, 200], seed=seed)
+
+
+def test_a_bounded_decode_loop():
+    """attend (scored) -> evict -> append, for many steps: every step against
+    the oracle on the caches as they are, the eviction by the scores as they are."""
+    c = _loop_inputs()
+    budget, first, recent, steps = 60, 2, 8, 12
+    gen = torch.Generator().manual_seed(5)
+    k, v = c.dev(torch.nan_to_num(c.k, 0, 0, 0)), c.dev(torch.nan_to_num(c.v, 0, 0, 0))
+    w = c.dev(c.w)
+    pos = torch.arange(c.C, dtype=torch.int32).expand(c.B, c.G, c.C).contiguous().cuda()
+    lens = torch.tensor(c.lens, dtype=torch.int32).cuda()
+    now = torch.tensor(c.lens)
+    rows = torch.arange(c.B).cuda()
+    kp, vp = c.dev(c.kp), c.dev(c.vp)
+    for step in range(steps):
+        q = (torch.randn(c.B, 1, c.H, c.d, generator=gen) * 2).to(torch.bfloat16)
+        c.q, c.k, c.v, c.w, c.lens = q, k.cpu(), v.cpu(), w.cpu(), lens.tolist()
+        before = w.clone()
+        o, lse, _ = M.prefix_attn_decode(c.shape, q.cuda(), k, v, lens, kp, vp, weights=w)
+        torch.cuda.synchronize()
+        shown = w.clone()
+        for b, n in enumerate(c.lens):
+            assert torch.equal(shown[b, :, n:], before[b, :, n:])
+            shown[b, :, n:] = -7.0
+        c.check(o, lse, shown)
+        old = Cache.__new__(Cache)
+        old.__dict__.update(B=c.B, G=c.G, C=c.C, lens=c.lens, k=c.k, v=c.v, w=w.cpu(), pos=pos.cpu())
+        _, _, lens = M.cache_evict(c.shape, k, v, lens, w, pos, budget, first, recent)
+        torch.cuda.synchronize()
+        old.check((k, v, w, pos, lens), budget, first, recent, in_place=True)
+        new = (torch.randn(2, c.B, c.G, c.d, generator=gen)).to(torch.bfloat16).cuda()
+        at = lens.long()
+        k[rows, :, at], v[rows, :, at] = new[0], new[1]
+        w[rows, :, at] = 0.0
+        pos[rows, :, at] = now.to(torch.int32).cuda()[:, None]
+        now += 1
+        lens = lens + 1
+    assert M.device_status() == 0 and int(lens.max()) == budget + 1
+
+
+def test_captured_and_replayed():
+    """One step (scored attention, then eviction) captured once and replayed
+    gives the eager calls' bits, on inputs changed between replays."""
+    c = _loop_inputs(91)
+    d = {n: c.dev(getattr(c, n)) for n in ("q", "k", "v", "kp", "vp", "w")}
+    pos = torch.arange(c.C, dtype=torch.int32).expand(c.B, c.G, c.C).contiguous().cuda()
+    lens = torch.tensor(c.lens, dtype=torch.int32).cuda()
+    out = dict(o=torch.empty_like(d["q"]), lse=torch.empty(c.B, 1, c.H, device="cuda"),
+               ws=M.alloc_workspace(c.shape, M.OP_PREFIX_DECODE_WEIGHTS))
+    ev = dict(positions_out=torch.zeros_like(pos), new_lens=torch.zeros_like(lens),
+              ws=M.alloc_workspace(c.shape, M.OP_CACHE_EVICT))
+    wo = torch.zeros_like(d["w"])
+    kv = [d["k"].clone(), d["v"].clone()]
+
+    def step():
+        kv[0].copy_(d["k"])
+        kv[1].copy_(d["v"])
+        M.prefix_attn_decode(c.shape, d["q"], *kv, lens, d["kp"], d["vp"], weights=d["w"], weights_out=wo, **out)
+        M.cache_evict(c.shape, *kv, lens, wo, pos, 60, 2, 8, **ev)
+        return [x.clone() for x in (out["o"], out["lse"], wo, *kv, ev["positions_out"], ev["new_lens"])]
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    for r in range(3):
+        d["q"].mul_(0.75)
+        lens.copy_(torch.tensor([(n + 31 * r) % (c.C + 1) for n in c.lens], dtype=torch.int32))
+        d["k"].nan_to_num_(0, 0, 0), d["v"].nan_to_num_(0, 0, 0)
+        wo.zero_(), ev["positions_out"].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        replayed = [x.clone() for x in held]
+        wo.zero_(), ev["positions_out"].zero_()
+        eager = step()
+        torch.cuda.synchronize()
+        for a, b in zip(replayed, eager):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    assert M.device_status() == 0
+
+
+def test_on_streams_of_their_own():
+    """Two calls at once on two streams, workspaces and outputs allocated by the
+    calls, give what the calls alone give."""
+    cs = [Case(B=8, T=1, H=32, G=4, d=128, Np=3000, C=500, lens=[60 * i + 7 for i in range(8)], seed=92 + i)
+          for i in range(2)]
+    alone = [c.run() for c in cs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cs]
+    dev = []
+    for c in cs:
+        dev.append([c.dev(x) for x in (c.q, c.k, c.v)] + [torch.tensor(c.lens, dtype=torch.int32).cuda()]
+                   + [c.dev(x) for x in (c.kp, c.vp, c.w)])
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = []
+        for c, s, x in zip(cs, streams, dev):
+            wo = torch.full_like(x[6], -7.0)
+            s.wait_stream(torch.cuda.current_stream())
+            got.append(M.prefix_attn_decode(c.shape, *x[:6], weights=x[6], weights_out=wo, stream=s))
+            junk = [torch.full((1 << 22,), NAN, device="cuda") for _ in range(3)]   # reuse of freed memory
+            del junk
+        torch.cuda.synchronize()
+        for a, b in zip(alone, got):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
