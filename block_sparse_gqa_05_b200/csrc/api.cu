@@ -794,6 +794,7 @@ msa_status msa_set_wait_limit_ns(uint64_t ns) {
   if (e == cudaSuccess) e = set_wait_limit_dense(ns);
   if (e == cudaSuccess) e = set_wait_limit_index(ns);
   if (e == cudaSuccess) e = set_wait_limit_prefill(ns);
+  if (e == cudaSuccess) e = set_wait_limit_prefix(ns);
   return from_cuda(e);
 }
 

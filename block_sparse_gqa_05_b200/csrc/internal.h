@@ -163,6 +163,7 @@ cudaError_t set_wait_limit_decode(uint64_t ns);
 cudaError_t set_wait_limit_dense(uint64_t ns);
 cudaError_t set_wait_limit_index(uint64_t ns);
 cudaError_t set_wait_limit_prefill(uint64_t ns);
+cudaError_t set_wait_limit_prefix(uint64_t ns);
 cudaError_t launch_dense_prefill(const msa_shape& s, const uint16_t* q, const uint16_t* k,
                                  const uint16_t* v, uint16_t* o, float* lse, cudaStream_t st);
 

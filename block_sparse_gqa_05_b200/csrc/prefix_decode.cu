@@ -1,12 +1,34 @@
 // Decode attention of a batch that shares a prefix, over own caches of
 // different lengths, with the softmax weight each own key receives.
 //
-// Every query row (token, head) attends the prefix rows and the own rows it
-// sees; one CTA per row, each of its warps over every fourth key with an
-// online softmax (running maximum and sum, fp32), merged at the end.  The
-// weights follow once the normalisers are known: a warp per own key computes
-// its logits again and adds exp(s - lse) over the rows that see it.
+// The rows of the product are (token, head) pairs of one group.  All rows of
+// the batch see the prefix, so its K/V blocks are streamed once per 256 of
+// them; the own cache of a (sequence, group) is seen by its T * r rows only.
+// A segment is one stream of 128-key blocks:
+//   pair    two 128-row tiles of a group over the prefix: both softmax
+//           warpgroups work on every block, one tile each;
+//   single  one tile (the last one of an odd count, or an own cache): the two
+//           warpgroups take alternate blocks, which keeps two blocks in
+//           flight and splits the keys between two accumulators.
+// The blocks of all segments form one line, weighted by what a block of each
+// kind costs, which is cut evenly over a persistent grid of one CTA per SM
+// (the lengths are read on the device).  Every (CTA, segment, warpgroup) leaves
+// an unnormalised partial output with its running maximum and sum in fp32; a
+// second kernel merges them.  With scores wanted, the logits of own keys go to
+// the workspace (4 T r bytes per key against 4 d for its K and V) and a third
+// kernel turns them into weights once the normalisers are known, which is
+// cheaper than reading K again.
+//
+// In the CTA: warp 0 streams K and V through a ring of tiles by TMA; warps 1
+// and 2 issue the MMAs of the two warpgroups' tiles (S = Q K^T to TMEM, then
+// O += P V with P read from TMEM over S); warp 3 loads the queries and zeroes
+// the V rows of a segment's last block that lie past its length (their weight
+// is zero, but 0 * NaN is not); warps 4..7 and 8..11 are the two softmax
+// warpgroups, one TMEM lane (row) per thread.  O is rescaled only when a row's
+// maximum grows by more than 2^8 over the one it was accumulated with.
 #include <math.h>
+
+#include <algorithm>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -14,186 +36,920 @@
 namespace msa {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kThreads = 384;
+constexpr int kMaxGrid = 256;      // bound of the persistent grid, for the workspace size
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kRescaleLog2 = 8.f;
+
+// Cost of a block on the line, by the kind of its segment, and of a segment.
+constexpr int kCostPair = 5, kCostSingle = 4, kCostSegment = 2;
 
 struct PrefixParams {
-  const uint16_t *q, *kp, *vp, *k, *v;
   uint16_t* o;
-  float *lse, *lse_ws, *w_out;
+  float* lse;
   const float* w_in;
+  float* w_out;
   const int32_t *lens, *prefix_pages, *table;
   uint32_t* err;
-  int B, T, H, G, r, C, nb, Np, Cp, num_pages;
+  long long* starts;   // [B + 1] line cost of one group of sequences 0 .. b-1
+  float* lse2;         // [B*T*H] normalisers, log2
+  float2* ml_p;        // [(nsp + grid) * 2, rows_p]  (maximum, sum) of prefix partials
+  float* o_p;          // [(nsp + grid) * 2, rows_p, D]
+  float2* ml_s;        // [(B*G + grid) * 2, T*r]     of own-cache partials
+  float* o_s;          // [(B*G + grid) * 2, T*r, D]
+  float* logits;       // [B*G, T*r, 128 nb] (log2 units; scores wanted) or nullptr
+  int B, T, H, G, r, C, nb, num_pages;
+  int Np, nbp;         // prefix rows and blocks
+  int ntile, npt, nsp; // prefix row tiles and tile pairs of a group; prefix segments
+  int rows_p, rows_s;  // rows of a prefix / own partial: min(128, B*T*r), T*r
+  int grid;
+  long long cost_pair, cost_group, cost_prefix;   // of a pair segment, a group's, all prefix segments
   float scale_log2;
 };
 
 // Valid rows of sequence b's own cache, clamped into [0, C].
 __device__ __forceinline__ int own_len(const PrefixParams& p, int b) {
-  const int n = p.lens[b];
+  const int n = __ldg(p.lens + b);
   if (n >= 0 && n <= p.C) return n;
   atomicOr(p.err, kErrBadLength);
   return n < 0 ? 0 : p.C;
 }
 
-// Offset, in elements, of prefix row x of group g.
-template <int D>
-__device__ __forceinline__ long long prefix_row(const PrefixParams& p, int g, int x) {
-  if (!p.prefix_pages) return (static_cast<long long>(g) * p.Cp + x) * D;
-  const int pg = page_of(p.prefix_pages, 0, p.num_pages, 0, x >> 7, p.err);
-  return ((static_cast<long long>(pg) * p.G + g) * 128 + (x & 127)) * D;
+__device__ __forceinline__ int blocks_of(int rows) { return (rows + 127) >> 7; }
+
+// Line cost of one group's segment over a sequence's own cache.
+__device__ __forceinline__ int own_cost(int nb) { return nb ? nb * kCostSingle + kCostSegment : 0; }
+
+// Line range [cta_begin(c), cta_begin(c + 1)) of CTA c; a block belongs to the
+// CTA in whose range it starts.
+__device__ __forceinline__ long long cta_begin(long long c, long long total, int grid) {
+  return (c * total + grid - 1) / grid;
+}
+__device__ __forceinline__ int cta_of(long long pos, long long total, int grid) {
+  return static_cast<int>(pos * grid / total);
 }
 
-// Offset, in elements, of own row x of (b, g).
-template <int D>
-__device__ __forceinline__ long long own_row(const PrefixParams& p, int b, int g, int x) {
-  if (!p.table) return ((static_cast<long long>(b) * p.G + g) * p.C + x) * D;
-  const int pg = page_of(p.table, p.nb, p.num_pages, b, x >> 7, p.err);
-  return ((static_cast<long long>(pg) * p.G + g) * 128 + (x & 127)) * D;
+// Blocks of a segment that start at ``start`` and cost ``w`` each, up to line
+// position ``u``.
+__device__ __forceinline__ int blocks_before(long long u, long long start, int w, int nb) {
+  if (u <= start) return 0;
+  const long long d = u - start;
+  return d >= static_cast<long long>(nb) * w ? nb : (static_cast<int>(d) + w - 1) / w;
 }
 
-template <int D>
-__device__ __forceinline__ void load_row(const uint16_t* src, int lane, float* out) {
-#pragma unroll
-  for (int i = 0; i < D / 64; ++i) {
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(src + i * 64 + 2 * lane);
-    out[2 * i] = __uint_as_float(w << 16);
-    out[2 * i + 1] = __uint_as_float(w & 0xFFFF0000u);
-  }
-}
+// One CTA's share of a segment.
+struct Seg {
+  int id;            // index of the segment: prefix segments, then b * G + g
+  int j0, n;         // first block and number of blocks
+  int nb, rows;      // blocks and valid keys of the whole segment
+  int b, g, tile;    // own: sequence and group; prefix: group and first row tile
+  bool own, pair;
+};
 
-template <int D>
-__device__ __forceinline__ float dot_row(const float* a, const float* b) {
-  float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) s = fmaf(a[i], b[i], s);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return s;
-}
+// Walks a CTA's segments along the line, the same way in every role.
+struct Walk {
+  long long u0, u1, pos;
+  int s, b, g, len;
 
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32) prefix_attn_kernel(const PrefixParams p) {
-  __shared__ float sm[kWarps], sl[kWarps], so[kWarps][D];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long row = blockIdx.x;
-  const int h = static_cast<int>(row % p.H), g = h / p.r;
-  const int t = static_cast<int>(row / p.H % p.T), b = static_cast<int>(row / p.H / p.T);
-  const int own = max(0, own_len(p, b) - p.T + t + 1);
-  float q[D / 32], acc[D / 32], kv[D / 32];
-  load_row<D>(p.q + row * D, lane, q);
-#pragma unroll
-  for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
-  float m = -INFINITY, l = 0.f;
-  for (int x = warp; x < p.Np + own; x += kWarps) {
-    const bool pre = x < p.Np;
-    const long long at = pre ? prefix_row<D>(p, g, x) : own_row<D>(p, b, g, x - p.Np);
-    load_row<D>((pre ? p.kp : p.k) + at, lane, kv);
-    const float s = dot_row<D>(q, kv) * p.scale_log2;
-    const float mn = fmaxf(m, s);
-    const float c = mn == -INFINITY ? 1.f : exp2f(m - mn);
-    const float e = mn == -INFINITY ? 0.f : exp2f(s - mn);
-    load_row<D>((pre ? p.vp : p.v) + at, lane, kv);
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) acc[i] = fmaf(acc[i], c, e * kv[i]);
-    l = fmaf(l, c, e);
-    m = mn;
-  }
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
-  }
-#pragma unroll
-  for (int i = 0; i < D / 64; ++i) {
-    so[warp][i * 64 + 2 * lane] = acc[2 * i];
-    so[warp][i * 64 + 2 * lane + 1] = acc[2 * i + 1];
-  }
-  __syncthreads();
-  float M = -INFINITY, L = 0.f, O = 0.f;
-  for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm[w]);
-  for (int w = 0; w < kWarps; ++w) {
-    const float c = sm[w] == -INFINITY ? 0.f : exp2f(sm[w] - M);
-    L = fmaf(sl[w], c, L);
-    if (threadIdx.x < D) O = fmaf(so[w][threadIdx.x], c, O);
-  }
-  if (threadIdx.x < D) {
-    __nv_bfloat16 v = __float2bfloat16_rn(L > 0.f ? O / L : 0.f);
-    p.o[row * D + threadIdx.x] = *reinterpret_cast<uint16_t*>(&v);
-  }
-  if (threadIdx.x == 0) {
-    const float lse2 = L > 0.f ? M + log2f(L) : -INFINITY;
-    if (p.lse_ws) p.lse_ws[row] = lse2;
-    if (p.lse) p.lse[row] = lse2 / kLog2e;
-  }
-}
-
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32) prefix_weights_kernel(const PrefixParams p) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int bg = blockIdx.x, b = bg / p.G, g = bg % p.G;
-  const int len = own_len(p, b);
-  float kv[D / 32], q[D / 32];
-  for (int x = blockIdx.y * kWarps + warp; x < len; x += gridDim.y * kWarps) {
-    load_row<D>(p.k + own_row<D>(p, b, g, x), lane, kv);
-    float w = 0.f;
-    for (int t = max(0, x - (len - p.T)); t < p.T; ++t)
-      for (int j = 0; j < p.r; ++j) {
-        const long long row = (static_cast<long long>(b) * p.T + t) * p.H + g * p.r + j;
-        load_row<D>(p.q + row * D, lane, q);
-        const float s = dot_row<D>(q, kv) * p.scale_log2;
-        w += exp2f(s - p.lse_ws[row]);
+  __device__ __forceinline__ bool next(const PrefixParams& p, Seg& q) {
+    for (;;) {
+      int w;
+      const long long start = pos;
+      if (s < p.nsp) {
+        q.own = false;
+        q.id = s;
+        q.g = s / p.npt;
+        q.tile = 2 * (s - q.g * p.npt);
+        q.pair = q.tile + 1 < p.ntile;
+        q.b = 0;
+        q.nb = p.nbp;
+        q.rows = p.Np;
+        w = q.pair ? kCostPair : kCostSingle;
+        pos += static_cast<long long>(p.nbp) * w + kCostSegment;
+        ++s;
+      } else {
+        if (b >= p.B) return false;
+        if (len < 0) len = own_len(p, b);
+        if (len == 0) {
+          ++b;
+          g = 0;
+          len = -1;
+          continue;
+        }
+        q.own = true;
+        q.pair = false;
+        q.id = p.nsp + b * p.G + g;
+        q.b = b;
+        q.g = g;
+        q.tile = 0;
+        q.nb = blocks_of(len);
+        q.rows = len;
+        w = kCostSingle;
+        pos += own_cost(q.nb);
+        if (++g == p.G) {
+          g = 0;
+          ++b;
+          len = -1;
+        }
       }
-    if (lane == 0) {
-      const long long at = static_cast<long long>(bg) * p.C + x;
-      p.w_out[at] = (p.w_in ? p.w_in[at] : 0.f) + w;
+      if (start >= u1) return false;
+      q.j0 = blocks_before(u0, start, w, q.nb);
+      q.n = blocks_before(u1, start, w, q.nb) - q.j0;
+      if (q.n > 0) return true;
+    }
+  }
+};
+
+// First of the CTA's blocks of a segment that warpgroup ``wg`` takes, and the
+// step to its next one; n0 the number of blocks the CTA had before.  The
+// blocks of single segments alternate along the whole walk, so a warpgroup
+// never skips two blocks in a row: with a ring of four tiles or more the tile
+// it waits for is then the next or the present load of its ring slot, which
+// is what a wait on the parity of a phase can tell apart.
+__device__ __forceinline__ int first_block(const Seg& q, int wg, int n0) {
+  return q.pair ? 0 : ((n0 ^ wg) & 1);
+}
+__device__ __forceinline__ int block_step(const Seg& q) { return q.pair ? 1 : 2; }
+// Whether the CTA's share ends in a block with rows past the segment's length.
+__device__ __forceinline__ bool ragged_end(const Seg& q) {
+  return q.j0 + q.n == q.nb && (q.rows & 127) != 0;
+}
+
+template <int D>
+struct PrefixSmem {
+  static constexpr uint32_t kTile = 128u * D * 2u;
+  static constexpr int kRing = D == 128 ? 5 : 10;       // K or V tiles in the ring
+  static constexpr uint32_t kOffRing = 2 * kTile;       // two query tiles first
+  static constexpr uint32_t kOffBar = kOffRing + kRing * kTile;
+  static constexpr uint32_t kBytes = kOffBar + 512;
+};
+
+struct Bars {
+  uint64_t *full, *empty;            // [ring]
+  uint64_t *qfull, *qempty;          // [2] per warpgroup
+  uint64_t *sfull, *pfull;           // [2]
+  uint64_t *olast, *ofree;           // [2]
+  uint64_t* drain;                   // [2] the MMA threads' last commits
+};
+
+// Sets *word, after everything this thread (and its warp, before a
+// __syncwarp) wrote.
+__device__ __forceinline__ void publish_count(const uint32_t* word, uint32_t v) {
+  asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(smem_u32(word)), "r"(v) : "memory");
+}
+
+// Bounded wait until *word >= want (a count another warp publishes).
+__device__ __forceinline__ bool wait_count(const uint32_t* word, uint32_t want, volatile int* abort,
+                                           uint32_t* err) {
+  const uint32_t a = smem_u32(word);
+  const uint64_t lim = g_wait_limit_ns;
+  uint64_t t0 = 0;
+  for (uint32_t it = 0;; ++it) {
+    uint32_t v;
+    asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    if (static_cast<int32_t>(v - want) >= 0) return true;
+    if (it == 0) t0 = globaltimer();
+    if (*abort) return false;
+    if (lim == 0 || ((it & 63u) == 63u && globaltimer() - t0 > lim)) {
+      atomicOr(err, kErrTimeout);
+      *abort = 1;
+      return false;
     }
   }
 }
 
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+
+// 32 bytes of one thread to global memory (a whole sector), dst 32-byte aligned.
+__device__ __forceinline__ void store8(float* dst, const float* v) {
+  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "f"(v[0]), "f"(v[1]),
+               "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
+}
+
+// The CTA's range of the line and where its walk starts, by all threads.
+// CTA 0 also publishes the sequences' line starts for the merge kernel.
+__device__ __forceinline__ void plan(const PrefixParams& p, long long* scratch, Walk* out) {
+  const int tid = threadIdx.x;
+  const int per = (p.B + kThreads - 1) / kThreads;
+  const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) mine += own_cost(blocks_of(own_len(p, b)));
+  // exclusive scan of the threads' sums
+  const int lane = tid & 31, warp = tid >> 5;
+  long long inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) scratch[warp] = inc;
+  __syncthreads();
+  long long before = inc - mine, all = 0;
+  for (int i = 0; i < kThreads / 32; ++i) {
+    if (i < warp) before += scratch[i];
+    all += scratch[i];
+  }
+  const long long total = p.cost_prefix + all * p.G;
+  const long long u0 = cta_begin(blockIdx.x, total, p.grid);
+  const long long u1 = cta_begin(blockIdx.x + 1, total, p.grid);
+  if (blockIdx.x == 0) {
+    long long at = before;
+    for (int b = b0; b < b1; ++b) {
+      p.starts[b] = at;
+      at += own_cost(blocks_of(own_len(p, b)));
+    }
+    if (tid == 0) p.starts[p.B] = all;
+  }
+  if (u0 < p.cost_prefix) {
+    if (tid == 0) {
+      const int g = static_cast<int>(u0 / p.cost_group);
+      const long long rest = u0 - g * p.cost_group;
+      const int pt = min(static_cast<int>(rest / p.cost_pair), p.npt - 1);
+      out->s = g * p.npt + pt;
+      out->pos = g * p.cost_group + pt * p.cost_pair;
+      out->b = out->g = 0;
+      out->len = -1;
+    }
+  } else {
+    if (tid == 0) {            // past every block, unless a thread below finds its place
+      out->s = p.nsp;
+      out->b = p.B;
+      out->g = 0;
+      out->len = -1;
+      out->pos = total;
+    }
+    __syncthreads();
+    const long long at = u0 - p.cost_prefix;   // < all * G when there is anything left
+    if (at >= before * p.G && at < (before + mine) * p.G) {
+      long long st = before;
+      for (int b = b0; b < b1; ++b) {
+        const int c = own_cost(blocks_of(own_len(p, b)));
+        if (at < (st + c) * p.G) {
+          const int g = static_cast<int>((at - st * p.G) / c);
+          out->b = b;
+          out->g = g;
+          out->pos = p.cost_prefix + st * p.G + static_cast<long long>(g) * c;
+          break;
+        }
+        st += c;
+      }
+    }
+  }
+  if (tid == 0) {
+    out->u0 = u0;
+    out->u1 = u1;
+  }
+}
+
 template <int D>
-cudaError_t launch(const PrefixParams& p, cudaStream_t st) {
+__global__ void __launch_bounds__(kThreads, 1)
+    prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp,
+                       const __grid_constant__ CUtensorMap tm_qs,
+                       const __grid_constant__ CUtensorMap tm_kp,
+                       const __grid_constant__ CUtensorMap tm_vp,
+                       const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v, const PrefixParams p) {
+  using L = PrefixSmem<D>;
+  constexpr int R = L::kRing;
+  constexpr uint32_t kIdescS = idesc_bf16(128, 128, 0, 0);
+  constexpr uint32_t kIdescO = idesc_bf16(128, D, 0, 1);
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ long long scratch[kThreads / 32];
+  __shared__ Walk walk0;
+  if ((smem_u32(smem) & 1023u) != 0u) {
+    if (threadIdx.x == 0) atomicOr(p.err, kErrTimeout);
+    return;
+  }
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
+  Bars m;
+  m.full = bars;
+  m.empty = bars + R;
+  m.qfull = bars + 2 * R;
+  m.qempty = m.qfull + 2;
+  m.sfull = m.qfull + 4;
+  m.pfull = m.qfull + 6;
+  m.olast = m.qfull + 8;
+  m.ofree = m.qfull + 10;
+  m.drain = m.qfull + 12;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(m.qfull + 14);
+  uint32_t* issued = tmem_slot + 1;                  // ragged V tiles loaded so far
+  uint32_t* fixed = tmem_slot + 2;                   // and zeroed past their length
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 3);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < R; ++i) {
+      mbar_init(&m.full[i], 1);
+      mbar_init(&m.empty[i], 2);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&m.qfull[i], 1);
+      mbar_init(&m.qempty[i], 1);
+      mbar_init(&m.sfull[i], 1);
+      mbar_init(&m.pfull[i], 128);
+      mbar_init(&m.olast[i], 1);
+      mbar_init(&m.ofree[i], 128);
+      mbar_init(&m.drain[i], 1);
+    }
+    *issued = *fixed = 0;
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tm_qp);
+    tma_prefetch_desc(&tm_qs);
+    tma_prefetch_desc(&tm_kp);
+    tma_prefetch_desc(&tm_vp);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, 512);
+  tc_fence_before();
+  // the kernel may start while the one before it on the stream finishes;
+  // nothing of that one's is read or overwritten before this
+  griddep_wait();
+  griddep_launch_dependents();
+  __syncthreads();
+  plan(p, scratch, &walk0);
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;   // S/P of the warpgroups at 0 and 128, O at 256 and 384
+  Walk walk = walk0;
+  Seg q;
+
+  if (warp < 4) {
+    regs_dec<80>();
+    if (warp == 0) {
+      // ------------------------------------------------------- K and V tiles
+      if (lane == 0) {
+        int item = 0;      // tiles issued: K of block n is 2n, V is 2n + 1
+        uint32_t ragged = 0;
+        bool ok = true;
+        while (ok && walk.next(p, q)) {
+          const CUtensorMap* mk = q.own || p.prefix_pages ? &tm_k : &tm_kp;
+          const CUtensorMap* mv = q.own || p.prefix_pages ? &tm_v : &tm_vp;
+          for (int j = q.j0; ok && j < q.j0 + q.n; ++j) {
+            int y = j * 128, z = q.own ? q.b * p.G + q.g : q.g;
+            if (q.own ? p.table != nullptr : p.prefix_pages != nullptr) {
+              y = 0;
+              z = (q.own ? page_of(p.table, p.nb, p.num_pages, q.b, j, p.err)
+                         : page_of(p.prefix_pages, 0, p.num_pages, 0, j, p.err)) *
+                      p.G + q.g;
+            }
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv, ++item) {
+              const int st = item % R;
+              if (!(ok = mbar_wait(&m.empty[st], ((item / R) & 1) ^ 1, abort_flag, p.err))) break;
+              mbar_arrive_expect_tx(&m.full[st], L::kTile);
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c)
+                tma_load_3d(smem + L::kOffRing + st * L::kTile + c * 16384, kv ? mv : mk,
+                            &m.full[st], c * 64, y, z);
+            }
+          }
+          if (ok && ragged_end(q)) publish_count(issued, ++ragged);
+        }
+        // every load issued lands before the CTA may exit
+        for (int x = max(0, item - R); x < item; ++x) mbar_drain(&m.full[x % R], (x / R) & 1);
+      }
+      __syncwarp();
+    } else if (warp == 3) {
+      // ------------------------------------- queries, and the ragged V tiles
+      int n0 = 0;                  // blocks of the segments before
+      int jobs[2] = {0, 0};
+      uint32_t ragged = 0;
+      bool ok = true;
+      while (ok && walk.next(p, q)) {
+        if (lane == 0) {
+#pragma unroll
+          for (int wg = 0; wg < 2; ++wg) {
+            if (!ok || first_block(q, wg, n0) >= q.n) continue;
+            if (!(ok = mbar_wait(&m.qempty[wg], (jobs[wg] & 1) ^ 1, abort_flag, p.err))) continue;
+            ++jobs[wg];
+            const CUtensorMap* mq = q.own ? &tm_qs : &tm_qp;
+            const int rows = q.own ? p.rows_s : 128;
+            const int tok = q.own ? q.b * p.T : (q.tile + (q.pair ? wg : 0)) * (128 / p.r);
+            mbar_arrive_expect_tx(&m.qfull[wg], static_cast<uint32_t>(rows * D * 2));
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+              tma_load_3d(smem + wg * L::kTile + c * 16384, mq, &m.qfull[wg], c * 64, q.g * p.r,
+                          tok);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0) != 0;
+        if (ok && ragged_end(q)) {
+          const int item = 2 * (n0 + q.n) - 1;
+          const int st = item % R;
+          // once its load is issued the slot stays this tile's until it is
+          // zeroed, so the parity of its phase is not ambiguous
+          ok = wait_count(issued, ++ragged, abort_flag, p.err);
+          ok = __all_sync(0xffffffffu, ok && mbar_wait(&m.full[st], (item / R) & 1, abort_flag, p.err));
+          if (!ok) break;
+          const int tail = q.rows & 127;
+          uint8_t* v = smem + L::kOffRing + st * L::kTile;
+          for (int x = lane; x < (128 - tail) * (D / 8); x += 32) {
+            const int c = x / ((128 - tail) * 8), y = x - c * (128 - tail) * 8;
+            *reinterpret_cast<uint4*>(v + c * 16384 + tail * 128 + y * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) publish_count(fixed, ragged);
+        }
+        n0 += q.n;
+      }
+      if (lane == 0)
+        for (int wg = 0; wg < 2; ++wg)
+          if (jobs[wg] > 0) mbar_drain(&m.qfull[wg], (jobs[wg] - 1) & 1);
+      __syncwarp();
+    } else {
+      // ---------------------------------------- the MMAs of one warpgroup's tiles
+      const int wg = warp - 1;
+      if (lane == 0) {
+        const uint32_t tS = tmem + wg * 128, tO = tmem + 256 + wg * 128;
+        const uint32_t qa = smem_u32(smem + wg * L::kTile);
+        const uint32_t ring = smem_u32(smem + L::kOffRing);
+        int n0 = 0, i = 0, jobs = 0;
+        uint32_t ragged = 0;
+        bool ok = true;
+        while (ok && walk.next(p, q)) {
+          const bool rag = ragged_end(q);
+          ragged += rag ? 1u : 0u;
+          const int first = first_block(q, wg, n0), step = block_step(q);
+          if (first < q.n) {
+            if (!(ok = mbar_wait(&m.qfull[wg], jobs & 1, abort_flag, p.err))) break;
+            for (int x = first; x < q.n; x += step, ++i) {
+              const bool last = x + step >= q.n;
+              const int ki = 2 * (n0 + x), vi = ki + 1;
+              const int ks_ = ki % R, vs_ = vi % R;
+              // S = Q K^T, over the P that the product before this one has read
+              if (!(ok = mbar_wait(&m.full[ks_], (ki / R) & 1, abort_flag, p.err))) break;
+              tc_fence_after();
+              const uint32_t ka = ring + ks_ * L::kTile;
+#pragma unroll
+              for (int ks = 0; ks < D / 16; ++ks) {
+                const uint32_t off = (ks >> 2) * 16384 + (ks & 3) * 32;
+                tc_mma_ss(tS, smem_desc(qa + off, 16, 1024, 2), smem_desc(ka + off, 16, 1024, 2),
+                          kIdescS, ks > 0 ? 1u : 0u);
+              }
+              tc_commit(&m.sfull[wg]);
+              tc_commit(&m.empty[ks_]);
+              if (!q.pair) tc_commit(&m.empty[ks_]);   // both arrivals are this warpgroup's
+              if (last) tc_commit(&m.qempty[wg]);
+              // O += P V
+              if (!(ok = mbar_wait(&m.pfull[wg], i & 1, abort_flag, p.err))) break;
+              if (x == first && jobs > 0 &&
+                  !(ok = mbar_wait(&m.ofree[wg], (jobs - 1) & 1, abort_flag, p.err)))
+                break;
+              if (!(ok = mbar_wait(&m.full[vs_], (vi / R) & 1, abort_flag, p.err))) break;
+              if (rag && x == q.n - 1 && !(ok = wait_count(fixed, ragged, abort_flag, p.err)))
+                break;
+              tc_fence_after();
+              const uint32_t va = ring + vs_ * L::kTile;
+#pragma unroll
+              for (int ks = 0; ks < 8; ++ks)
+                tc_mma_ts(tO, tS + ks * 8, smem_desc(va + ks * 16 * 128, 16384, 1024, 2), kIdescO,
+                          (x > first || ks > 0) ? 1u : 0u);
+              tc_commit(&m.empty[vs_]);
+              if (!q.pair) tc_commit(&m.empty[vs_]);
+              if (last) tc_commit(&m.olast[wg]);
+            }
+            ++jobs;
+          }
+          n0 += q.n;
+        }
+        // every MMA issued completes before TMEM is released
+        tc_drain(&m.drain[wg], 0);
+      }
+      __syncwarp();
+    }
+  } else {
+    regs_inc<208>();
+    // ------------------------------------------------------ softmax, one row a thread
+    const int wg = (warp >> 2) - 1;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + wg * 128 + lane_off, tO = tmem + 256 + wg * 128 + lane_off;
+    int n0 = 0, i = 0, jobs = 0;
+    bool ok = true;
+    while (ok && walk.next(p, q)) {
+      const int first = first_block(q, wg, n0), step = block_step(q);
+      n0 += q.n;
+      // rows of the tile that exist, this row's last key, and where its partial goes
+      const int tile = q.tile + (q.pair ? wg : 0);
+      const int nrow = q.own ? p.rows_s : min(128, p.B * p.T * p.r - tile * 128);
+      const int last_key = q.own ? q.rows - p.T + row / p.r : q.rows - 1;
+      const bool busy = (warp & 3) * 32 < nrow;      // warps without a row only keep the pace
+      const bool valid = row < nrow;
+      const long long part =
+          2ll * (static_cast<long long>(q.own ? q.id - p.nsp : q.id) + blockIdx.x) + wg;
+      const long long prow = part * (q.own ? p.rows_s : p.rows_p) + row;
+      if (first >= q.n) {              // the one block of a short share is the other warpgroup's
+        if (valid) (q.own ? p.ml_s : p.ml_p)[prow] = make_float2(-INFINITY, 0.f);
+        continue;
+      }
+      float* logit = nullptr;
+      if (q.own && p.logits && valid)
+        logit = p.logits + (static_cast<long long>(q.b * p.G + q.g) * p.rows_s + row) * p.nb * 128;
+      float mref = -INFINITY, l = 0.f;
+      for (int x = first; x < q.n; x += step, ++i) {
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&m.sfull[wg], i & 1, abort_flag, p.err)))) break;
+        if (busy) {
+          tc_fence_after();
+          const int j = q.j0 + x;
+          float sv[128];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, sv + c * 32);
+          tc_wait_ld();
+          const int lim = last_key - j * 128;        // keys past lim are not seen
+          if (!__all_sync(0xffffffffu, lim >= 127)) {
+#pragma unroll
+            for (int y = 0; y < 128; ++y) sv[y] = y <= lim ? sv[y] : -INFINITY;
+          }
+          if (logit) {
+#pragma unroll
+            for (int y = 0; y < 128; y += 8) {
+              float t8[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) t8[e] = sv[y + e] * p.scale_log2;
+              store8(logit + j * 128 + y, t8);
+            }
+          }
+          float m4[4] = {sv[0], sv[1], sv[2], sv[3]};
+#pragma unroll
+          for (int y = 4; y < 128; y += 8) {
+            m4[0] = fmax3(m4[0], sv[y], sv[y + 1]);
+            m4[1] = fmax3(m4[1], sv[y + 2], sv[y + 3]);
+            if (y + 4 < 128) {
+              m4[2] = fmax3(m4[2], sv[y + 4], sv[y + 5]);
+              m4[3] = fmax3(m4[3], sv[y + 6], sv[y + 7]);
+            }
+          }
+          const float mblk = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2;
+          // a row whose maximum outgrew its reference rescales O; S of this block
+          // was issued after the product of the block before, so that one is complete
+          const bool grow = mblk > mref + kRescaleLog2;
+          if (__any_sync(0xffffffffu, grow && x > first)) {
+            const float a = grow ? fast_exp2(mref - mblk) : 1.f;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              float ov[32];
+              tmem_ld32(tO + c * 32, ov);
+              tc_wait_ld();
+#pragma unroll
+              for (int y = 0; y < 32; ++y) ov[y] *= a;
+              tmem_st32(tO + c * 32, ov);
+            }
+            l *= a;
+          }
+          if (grow) mref = mblk;
+          const float mu = mref == -INFINITY ? 0.f : mref;   // a row that has seen no key yet
+          const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2), mm2 = f2_pack(-mu, -mu);
+          uint64_t l2[4] = {0, 0, 0, 0};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int y = 0; y < 32; y += 2) {
+              const float2 e = f2_unpack(ffma2(f2_pack(sv[c * 32 + y], sv[c * 32 + y + 1]), sc2, mm2));
+              const float e0 = fast_exp2(e.x), e1 = fast_exp2(e.y);
+              pk[y >> 1] = pack2(e0, e1);
+              l2[(y >> 1) & 3] = fadd2(l2[(y >> 1) & 3], f2_pack(e0, e1));
+            }
+            tmem_st16(tS + c * 16, pk);
+          }
+          const float2 la = f2_unpack(fadd2(fadd2(l2[0], l2[1]), fadd2(l2[2], l2[3])));
+          l += la.x + la.y;
+          tc_wait_st();
+          tc_fence_before();
+        }
+        mbar_arrive(&m.pfull[wg]);
+      }
+      if (!ok) break;
+      // the partial of this CTA and warpgroup
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&m.olast[wg], jobs & 1, abort_flag, p.err)))) break;
+      if (busy) {
+        tc_fence_after();
+        float* orow = (q.own ? p.o_s : p.o_p) + prow * D;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          float ov[32];
+          tmem_ld32(tO + c * 32, ov);
+          tc_wait_ld();
+          if (valid) {
+#pragma unroll
+            for (int y = 0; y < 32; y += 8) store8(orow + c * 32 + y, ov + y);
+          }
+        }
+        if (valid) (q.own ? p.ml_s : p.ml_p)[prow] = make_float2(mref, l);
+        tc_fence_before();
+      }
+      mbar_arrive(&m.ofree[wg]);
+      ++jobs;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Where one row's partials of a segment lie: of CTAs c0 .. c1, at index
+// (id + c) * 2 + warpgroup.
+struct Parts {
+  long long start;
+  int c0, n, nb, w, id, row, rows;
+  bool own, pair;
+  int wg;       // of a pair: the warpgroup of the row's tile
+};
+
+__device__ __forceinline__ Parts parts_of(const PrefixParams& p, long long total, bool own, int b,
+                                          int t, int h) {
+  Parts s;
+  const int g = h / p.r, hr = h - g * p.r;
+  s.own = own;
+  s.pair = false;
+  s.wg = 0;
+  s.w = kCostSingle;
+  if (own) {
+    s.id = p.nsp + b * p.G + g;
+    s.nb = blocks_of(own_len(p, b));
+    s.start = p.cost_prefix + p.starts[b] * p.G + static_cast<long long>(g) * own_cost(s.nb);
+    s.row = t * p.r + hr;
+    s.rows = p.rows_s;
+  } else {
+    const int at = (b * p.T + t) * p.r + hr, tile = at >> 7, pt = tile >> 1;
+    s.id = g * p.npt + pt;
+    s.pair = 2 * pt + 1 < p.ntile;
+    s.wg = tile & 1;
+    s.nb = p.nbp;
+    if (s.pair) s.w = kCostPair;
+    s.start = g * p.cost_group + pt * p.cost_pair;
+    s.row = at & 127;
+    s.rows = p.rows_p;
+  }
+  s.n = 0;
+  s.c0 = 0;
+  if (s.nb > 0) {
+    s.c0 = cta_of(s.start, total, p.grid);
+    s.n = 2 * (cta_of(s.start + static_cast<long long>(s.nb - 1) * s.w, total, p.grid) - s.c0 + 1);
+  }
+  return s;
+}
+
+// Partial k of the list (two a CTA): its index, or -1 when that CTA had no
+// block of the segment, or of a pair when it is the other tile's.
+__device__ __forceinline__ long long part_at(const PrefixParams& p, const Parts& s, long long total,
+                                             int k) {
+  const int c = s.c0 + (k >> 1), wg = k & 1;
+  const int n = blocks_before(cta_begin(c + 1, total, p.grid), s.start, s.w, s.nb) -
+                blocks_before(cta_begin(c, total, p.grid), s.start, s.w, s.nb);
+  if (n <= 0 || (s.pair && wg != s.wg)) return -1;
+  const long long part = 2ll * ((s.own ? s.id - p.nsp : s.id) + c) + wg;
+  return part * s.rows + s.row;
+}
+
+constexpr int kMergeWarps = 8;
+
+// One warp per row (b, t, h): merges its partials.  With m and l the running
+// maximum and sum of a partial and O its unnormalised output,
+// o = sum 2^(m - M) O / sum 2^(m - M) l, lse = M + log2 of the denominator.
+template <int D>
+__global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const PrefixParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long row = static_cast<long long>(blockIdx.x) * kMergeWarps + warp;
+  if (row >= static_cast<long long>(p.B) * p.T * p.H) return;
+  const int h = static_cast<int>(row % p.H);
+  const int t = static_cast<int>(row / p.H % p.T), b = static_cast<int>(row / p.H / p.T);
+  const long long total = p.cost_prefix + p.starts[p.B] * p.G;
+  float M = -INFINITY, den = 0.f;
+  bool poison = false;
+  constexpr int V = D / 32;
+  float acc[V];
+#pragma unroll
+  for (int y = 0; y < V; ++y) acc[y] = 0.f;
+#pragma unroll 1
+  for (int own = 0; own < 2; ++own) {
+    const Parts s = parts_of(p, total, own != 0, b, t, h);
+    const float2* ml = own ? p.ml_s : p.ml_p;
+    const float* po = own ? p.o_s : p.o_p;
+    for (int k0 = 0; k0 < s.n; k0 += 32) {
+      const long long at = k0 + lane < s.n ? part_at(p, s, total, k0 + lane) : -1;
+      const float2 v = at >= 0 ? __ldcg(ml + at) : make_float2(-INFINITY, 0.f);
+      // fmaxf drops a NaN: a row with a NaN or +inf logit is NaN throughout
+      poison |= __any_sync(0xffffffffu, v.x != v.x || v.y != v.y);
+      float mx = v.x;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const float Mn = fmaxf(M, mx);
+      if (Mn == -INFINITY) continue;
+      const float keep = fast_exp2(M - Mn), wgt = at >= 0 ? fast_exp2(v.x - Mn) : 0.f;
+      float ls = wgt * v.y;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
+      den = den * keep + ls;
+#pragma unroll
+      for (int y = 0; y < V; ++y) acc[y] *= keep;
+      M = Mn;
+      unsigned todo = __ballot_sync(0xffffffffu, wgt > 0.f);
+      while (todo) {
+        // up to four partial rows in flight
+        float x[4][V], wk[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int src = todo ? __ffs(todo) - 1 : 0;
+          wk[u] = todo ? __shfl_sync(0xffffffffu, wgt, src) : 0.f;
+          const long long a = __shfl_sync(0xffffffffu, at, src);
+          if (todo) {
+            const float* f = po + a * D + lane * V;
+            if constexpr (V == 4) {
+              const float4 q4 = __ldcg(reinterpret_cast<const float4*>(f));
+              x[u][0] = q4.x;
+              x[u][1] = q4.y;
+              x[u][2] = q4.z;
+              x[u][3] = q4.w;
+            } else {
+              const float2 q2 = __ldcg(reinterpret_cast<const float2*>(f));
+              x[u][0] = q2.x;
+              x[u][1] = q2.y;
+            }
+          } else {
+#pragma unroll
+            for (int y = 0; y < V; ++y) x[u][y] = 0.f;
+          }
+          todo &= todo - 1;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int y = 0; y < V; ++y) acc[y] = fmaf(wk[u], x[u][y], acc[y]);
+      }
+    }
+  }
+  if (poison) M = den = __int_as_float(0x7fffffff);
+  const float inv = M == -INFINITY ? 0.f : 1.f / den;
+  uint16_t* out = p.o + row * D + lane * V;
+  if constexpr (V == 4)
+    *reinterpret_cast<uint2*>(out) =
+        make_uint2(pack2(acc[0] * inv, acc[1] * inv), pack2(acc[2] * inv, acc[3] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(out) = pack2(acc[0] * inv, acc[1] * inv);
+  if (lane == 0) {
+    const float lse2 = M == -INFINITY ? -INFINITY : M + log2f(den);
+    p.lse2[row] = lse2;
+    if (p.lse) p.lse[row] = lse2 / kLog2e;
+  }
+}
+
+constexpr int kScoreThreads = 256;
+
+// One thread per own key: the weights its rows gave it, from their logits.
+__global__ void __launch_bounds__(kScoreThreads) prefix_score_kernel(const PrefixParams p) {
+  __shared__ float norm[128];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int bg = blockIdx.x, b = bg / p.G, g = bg - b * p.G;
+  const int len = own_len(p, b);
+  if (blockIdx.y * kScoreThreads >= len) return;
+  for (int i = threadIdx.x; i < p.rows_s; i += kScoreThreads) {
+    const int t = i / p.r;
+    const float n = __ldcg(p.lse2 + (static_cast<long long>(b) * p.T + t) * p.H + g * p.r + (i - t * p.r));
+    norm[i] = n == -INFINITY ? 0.f : n;     // a row that sees no key has logits of -inf alone
+  }
+  __syncthreads();
+  const long long stride = static_cast<long long>(p.nb) * 128;
+  for (int x = blockIdx.y * kScoreThreads + threadIdx.x; x < len; x += gridDim.y * kScoreThreads) {
+    const float* s = p.logits + static_cast<long long>(bg) * p.rows_s * stride + x;
+    const long long at = static_cast<long long>(bg) * p.C + x;
+    float w = 0.f;
+#pragma unroll 8
+    for (int i = 0; i < p.rows_s; ++i) w += fast_exp2(__ldcg(s + i * stride) - norm[i]);
+    p.w_out[at] = (p.w_in ? p.w_in[at] : 0.f) + w;
+  }
+}
+
+// Workspace layout.
+struct PrefixWs {
+  size_t starts, lse2, ml_p, o_p, ml_s, o_s, logits, bytes;
+};
+
+PrefixWs ws_layout(const msa_shape& s, bool weights) {
+  const size_t r = s.n_q_heads / s.n_kv_heads, d = s.head_dim;
+  const size_t rows = static_cast<size_t>(s.batch) * s.seq_q * r;
+  const size_t bg = static_cast<size_t>(s.batch) * s.n_kv_heads;
+  const size_t nsp = static_cast<size_t>(ceil_div(ceil_div(rows, 128), 2)) * s.n_kv_heads;
+  const size_t pr = 2 * (nsp + kMaxGrid) * std::min<size_t>(rows, 128);
+  const size_t sr = 2 * (bg + kMaxGrid) * s.seq_q * r;
+  PrefixWs w{};
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t x = at;
+    at += align_up(n, 256);
+    return x;
+  };
+  w.starts = take((static_cast<size_t>(s.batch) + 1) * sizeof(long long));
+  w.lse2 = take(rows * s.n_kv_heads * sizeof(float));
+  w.ml_p = take(pr * sizeof(float2));
+  w.o_p = take(pr * d * sizeof(float));
+  w.ml_s = take(sr * sizeof(float2));
+  w.o_s = take(sr * d * sizeof(float));
+  w.logits = take(weights ? bg * s.seq_q * r * ceil_div(s.seq_kv, 128) * 128 * sizeof(float) : 0);
+  w.bytes = at;
+  return w;
+}
+
+template <int D>
+cudaError_t launch(const msa_shape& s, const PrefixDecodeArgs& a, const PrefixParams& p,
+                   cudaStream_t st) {
+  CUtensorMap tqp, tqs, tkp, tvp, tk, tv;
+  const uint64_t D8 = D;
+  const uint64_t dq[3] = {D8, static_cast<uint64_t>(p.H), static_cast<uint64_t>(p.B) * p.T};
+  const uint64_t sq[2] = {D8 * 2, static_cast<uint64_t>(p.H) * D * 2};
+  const uint32_t bqp[3] = {64, static_cast<uint32_t>(p.r), static_cast<uint32_t>(128 / p.r)};
+  const uint32_t bqs[3] = {64, static_cast<uint32_t>(p.r), static_cast<uint32_t>(p.T)};
+  // contiguous: [B*G][C][d]; paged: [num_pages*G][128][d]
+  const bool paged = a.pages.table != nullptr;
+  const uint64_t rows = paged ? 128 : static_cast<uint64_t>(p.C);
+  const uint64_t mats = static_cast<uint64_t>(paged ? p.num_pages : p.B) * p.G;
+  const uint64_t dk[3] = {D8, rows, mats};
+  const uint64_t sk[2] = {D8 * 2, rows * D * 2};
+  const uint32_t bk[3] = {64, 128, 1};
+  const uint64_t dp[3] = {D8, static_cast<uint64_t>(std::max(a.prefix_cap, 1)),
+                          static_cast<uint64_t>(p.G)};
+  const uint64_t sp[2] = {D8 * 2, dp[1] * D * 2};
+  const bool pre = p.Np > 0 && !paged;    // a prefix array of its own
+  auto enc = [](CUtensorMap* m, const void* base, const uint64_t* dims, const uint64_t* strides,
+                const uint32_t* box) {
+    return encode_tmap(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box,
+                       CU_TENSOR_MAP_SWIZZLE_128B);
+  };
+  if (!enc(&tqp, a.q, dq, sq, bqp) || !enc(&tqs, a.q, dq, sq, bqs) || !enc(&tk, a.k, dk, sk, bk) ||
+      !enc(&tv, a.v, dk, sk, bk) || !enc(&tkp, pre ? a.kp : a.k, pre ? dp : dk, pre ? sp : sk, bk) ||
+      !enc(&tvp, pre ? a.vp : a.v, pre ? dp : dk, pre ? sp : sk, bk))
+    return cudaErrorInvalidValue;
+  const size_t smem = PrefixSmem<D>::kBytes;
+  cudaError_t e = cudaFuncSetAttribute(prefix_attn_kernel<D>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
   {
     ProfScope ps_("prefix_attn", st);
-    prefix_attn_kernel<D><<<static_cast<unsigned>(p.B) * p.T * p.H, kWarps * 32, 0, st>>>(p);
+    e = launch_dependent(prefix_attn_kernel<D>, dim3(static_cast<unsigned>(p.grid)), dim3(kThreads),
+                         smem, st, tqp, tqs, tkp, tvp, tk, tv, p);
   }
-  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  {
+    ProfScope ps_("prefix_merge", st);
+    const long long all = static_cast<long long>(p.B) * p.T * p.H;
+    e = launch_dependent(prefix_merge_kernel<D>, dim3(static_cast<unsigned>(ceil_div(all, kMergeWarps))),
+                         dim3(kMergeWarps * 32), 0, st, p);
+  }
   if (e != cudaSuccess || !p.w_out) return e;
   {
-    ProfScope ps_("prefix_weights", st);
-    const dim3 grid(static_cast<unsigned>(p.B) * p.G,
-                    static_cast<unsigned>(ceil_div(p.C, 64 * kWarps)));
-    prefix_weights_kernel<D><<<grid, kWarps * 32, 0, st>>>(p);
+    ProfScope ps_("prefix_score", st);
+    const int64_t slices = std::min<int64_t>(ceil_div(p.C, kScoreThreads), 65535);   // grid limit
+    e = launch_dependent(prefix_score_kernel,
+                         dim3(static_cast<unsigned>(p.B) * p.G, static_cast<unsigned>(slices)),
+                         dim3(kScoreThreads), 0, st, p);
   }
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace
 
 size_t prefix_decode_workspace_bytes(const msa_shape& s, bool weights) {
-  (void)weights;
-  return align_up(sizeof(float) * static_cast<size_t>(s.batch) * s.seq_q * s.n_q_heads, 256);
+  return ws_layout(s, weights).bytes;
 }
 
 cudaError_t launch_prefix_decode(const msa_shape& s, const PrefixDecodeArgs& a, void* ws,
                                  cudaStream_t st) {
   const DevCtx* ctx = device_ctx();
   if (!ctx) return cudaErrorInitializationError;
+  const PrefixWs w = ws_layout(s, a.w_out != nullptr);
+  char* base = static_cast<char*>(ws);
   PrefixParams p{};
-  p.q = a.q;
-  p.kp = a.prefix_pages ? a.k : a.kp;
-  p.vp = a.prefix_pages ? a.v : a.vp;
-  p.k = a.k;
-  p.v = a.v;
   p.o = a.o;
   p.lse = a.lse;
-  p.lse_ws = static_cast<float*>(ws);
   p.w_in = a.w_in;
   p.w_out = a.w_out;
   p.lens = a.lens;
-  p.prefix_pages = a.prefix_pages;
+  p.prefix_pages = a.prefix_len > 0 ? a.prefix_pages : nullptr;
   p.table = a.pages.table;
   p.num_pages = a.pages.num_pages;
   p.err = ctx->err;
+  p.starts = reinterpret_cast<long long*>(base + w.starts);
+  p.lse2 = reinterpret_cast<float*>(base + w.lse2);
+  p.ml_p = reinterpret_cast<float2*>(base + w.ml_p);
+  p.o_p = reinterpret_cast<float*>(base + w.o_p);
+  p.ml_s = reinterpret_cast<float2*>(base + w.ml_s);
+  p.o_s = reinterpret_cast<float*>(base + w.o_s);
+  p.logits = a.w_out ? reinterpret_cast<float*>(base + w.logits) : nullptr;
   p.B = s.batch;
   p.T = s.seq_q;
   p.H = s.n_q_heads;
@@ -202,9 +958,25 @@ cudaError_t launch_prefix_decode(const msa_shape& s, const PrefixDecodeArgs& a, 
   p.C = s.seq_kv;
   p.nb = static_cast<int>(ceil_div(s.seq_kv, 128));
   p.Np = a.prefix_len;
-  p.Cp = a.prefix_cap;
+  p.nbp = static_cast<int>(ceil_div(a.prefix_len, 128));
+  const int64_t rows = static_cast<int64_t>(p.B) * p.T * p.r;
+  p.ntile = static_cast<int>(ceil_div(rows, 128));
+  p.npt = (p.ntile + 1) / 2;
+  p.nsp = p.Np > 0 ? p.npt * p.G : 0;
+  p.rows_p = static_cast<int>(std::min<int64_t>(rows, 128));
+  p.rows_s = p.T * p.r;
+  p.cost_pair = static_cast<long long>(p.nbp) * kCostPair + kCostSegment;
+  const long long last = (p.ntile & 1) ? static_cast<long long>(p.nbp) * kCostSingle + kCostSegment
+                                       : p.cost_pair;
+  p.cost_group = (p.npt - 1) * p.cost_pair + last;
+  p.cost_prefix = p.Np > 0 ? p.cost_group * p.G : 0;
   p.scale_log2 = kLog2e / sqrtf(static_cast<float>(s.head_dim));
-  return s.head_dim == 128 ? launch<128>(p, st) : launch<64>(p, st);
+  // no more CTAs than blocks there can be
+  const int64_t most = static_cast<int64_t>(p.nsp) * p.nbp + static_cast<int64_t>(p.B) * p.G * p.nb;
+  p.grid = static_cast<int>(std::min<int64_t>(most, std::min(std::max(ctx->num_sms, 1), kMaxGrid)));
+  return s.head_dim == 128 ? launch<128>(s, a, p, st) : launch<64>(s, a, p, st);
 }
+
+cudaError_t set_wait_limit_prefix(uint64_t ns) { return set_wait_limit_here(ns); }
 
 }  // namespace msa

@@ -531,3 +531,39 @@ def test_on_streams_of_their_own():
         torch.cuda.synchronize()
         for a, b in zip(alone, got):
             assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_expired_waits_are_reported_and_the_context_recovers():
+    """With a wait limit of 0 every wait that is not complete at once gives up:
+    the call returns, the error word says so, the next call is right again."""
+    c = Case(B=20, T=1, H=32, G=4, d=128, Np=5000, C=700, lens=[37 * i % 701 for i in range(20)], seed=95)
+    good = c.run()
+    torch.cuda.synchronize()
+    assert M.device_status() == 0
+    try:
+        M.set_wait_limit_ns(0)
+        c.run()
+        torch.cuda.synchronize()
+        flags = M.device_status()
+    finally:
+        M.set_wait_limit_ns(2_000_000_000)
+    assert flags & 1, flags
+    again = c.run()
+    torch.cuda.synchronize()
+    assert M.device_status() == 0 and all(torch.equal(a, b) for a, b in zip(good, again))
+
+
+def test_nan_and_infinite_queries_stay_in_their_rows():
+    c = Case(B=3, T=2, H=8, G=2, d=64, Np=300, C=200, lens=[200, 2, 90], seed=96)
+    c.check(*c.run())
+    ref = c.run()
+    c.q[1, 0, 3, 5] = NAN
+    c.q[2, 1, 0] = float("inf")
+    o, lse, w = c.run()
+    torch.cuda.synchronize()
+    assert torch.isnan(o[1, 0, 3]).all() and torch.isnan(lse[1, 0, 3])
+    assert torch.isnan(o[2, 1, 0]).all() and torch.isnan(lse[2, 1, 0])
+    hit = torch.zeros(3, 2, 8, dtype=torch.bool)
+    hit[1, 0, 3] = hit[2, 1, 0] = True
+    assert torch.equal(o.cpu()[~hit], ref[0].cpu()[~hit]) and torch.equal(lse.cpu()[~hit], ref[1].cpu()[~hit])
+    assert M.device_status() == 0
