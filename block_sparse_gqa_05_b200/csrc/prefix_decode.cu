@@ -187,7 +187,8 @@ struct PrefixSmem {
 struct Bars {
   uint64_t *full, *empty;            // [ring]
   uint64_t *qfull, *qempty;          // [2] per warpgroup
-  uint64_t *sfull, *pfull;           // [2]
+  uint64_t* sfull;                   // [2]
+  uint64_t* pfull;                   // [2][2] per warpgroup and half of the keys
   uint64_t *olast, *ofree;           // [2]
   uint64_t* drain;                   // [2] the MMA threads' last commits
 };
@@ -228,6 +229,23 @@ __device__ __forceinline__ void store8(float* dst, const float* v) {
   asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "f"(v[0]), "f"(v[1]),
                "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
                : "memory");
+}
+
+// Keys 64 hf .. 64 hf + 63 of this thread's row of S, those past lim at -inf.
+__device__ __forceinline__ void load_half(uint32_t tS, int hf, int lim, bool whole, float* sv) {
+  tmem_ld32(tS + hf * 64, sv);
+  tmem_ld32(tS + hf * 64 + 32, sv + 32);
+  tc_wait_ld();
+  if (!whole) {
+#pragma unroll
+    for (int y = 0; y < 64; ++y) sv[y] = hf * 64 + y <= lim ? sv[y] : -INFINITY;
+  }
+}
+
+// mbar_wait with a probe before anything else: most waits here are complete.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t phase, volatile int* abort,
+                                         uint32_t* err) {
+  return mbar_test(bar, phase) || mbar_wait(bar, phase, abort, err);
 }
 
 // The CTA's range of the line and where its walk starts, by all threads.
@@ -332,10 +350,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   m.qempty = m.qfull + 2;
   m.sfull = m.qfull + 4;
   m.pfull = m.qfull + 6;
-  m.olast = m.qfull + 8;
-  m.ofree = m.qfull + 10;
-  m.drain = m.qfull + 12;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(m.qfull + 14);
+  m.olast = m.qfull + 10;
+  m.ofree = m.qfull + 12;
+  m.drain = m.qfull + 14;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(m.qfull + 16);
   uint32_t* issued = tmem_slot + 1;                  // ragged V tiles loaded so far
   uint32_t* fixed = tmem_slot + 2;                   // and zeroed past their length
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 3);
@@ -350,7 +368,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&m.qfull[i], 1);
       mbar_init(&m.qempty[i], 1);
       mbar_init(&m.sfull[i], 1);
-      mbar_init(&m.pfull[i], 128);
+      mbar_init(&m.pfull[2 * i], 128);
+      mbar_init(&m.pfull[2 * i + 1], 128);
       mbar_init(&m.olast[i], 1);
       mbar_init(&m.ofree[i], 128);
       mbar_init(&m.drain[i], 1);
@@ -401,8 +420,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv, ++item) {
               const int st = item % R;
-              if (!(ok = mbar_wait(&m.empty[st], ((item / R) & 1) ^ 1, abort_flag, p.err))) break;
+              if (!(ok = wait_bar(&m.empty[st], ((item / R) & 1) ^ 1, abort_flag, p.err))) break;
               mbar_arrive_expect_tx(&m.full[st], L::kTile);
+              if (!q.pair) mbar_arrive(&m.empty[st]);   // only one warpgroup will release it
 #pragma unroll
               for (int c = 0; c < D / 64; ++c)
                 tma_load_3d(smem + L::kOffRing + st * L::kTile + c * 16384, kv ? mv : mk,
@@ -426,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int wg = 0; wg < 2; ++wg) {
             if (!ok || first_block(q, wg, n0) >= q.n) continue;
-            if (!(ok = mbar_wait(&m.qempty[wg], (jobs[wg] & 1) ^ 1, abort_flag, p.err))) continue;
+            if (!(ok = wait_bar(&m.qempty[wg], (jobs[wg] & 1) ^ 1, abort_flag, p.err))) continue;
             ++jobs[wg];
             const CUtensorMap* mq = q.own ? &tm_qs : &tm_qp;
             const int rows = q.own ? p.rows_s : 128;
@@ -445,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // once its load is issued the slot stays this tile's until it is
           // zeroed, so the parity of its phase is not ambiguous
           ok = wait_count(issued, ++ragged, abort_flag, p.err);
-          ok = __all_sync(0xffffffffu, ok && mbar_wait(&m.full[st], (item / R) & 1, abort_flag, p.err));
+          ok = __all_sync(0xffffffffu, ok && wait_bar(&m.full[st], (item / R) & 1, abort_flag, p.err));
           if (!ok) break;
           const int tail = q.rows & 127;
           uint8_t* v = smem + L::kOffRing + st * L::kTile;
@@ -478,13 +498,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           ragged += rag ? 1u : 0u;
           const int first = first_block(q, wg, n0), step = block_step(q);
           if (first < q.n) {
-            if (!(ok = mbar_wait(&m.qfull[wg], jobs & 1, abort_flag, p.err))) break;
+            if (!(ok = wait_bar(&m.qfull[wg], jobs & 1, abort_flag, p.err))) break;
             for (int x = first; x < q.n; x += step, ++i) {
               const bool last = x + step >= q.n;
               const int ki = 2 * (n0 + x), vi = ki + 1;
               const int ks_ = ki % R, vs_ = vi % R;
               // S = Q K^T, over the P that the product before this one has read
-              if (!(ok = mbar_wait(&m.full[ks_], (ki / R) & 1, abort_flag, p.err))) break;
+              if (!(ok = wait_bar(&m.full[ks_], (ki / R) & 1, abort_flag, p.err))) break;
               tc_fence_after();
               const uint32_t ka = ring + ks_ * L::kTile;
 #pragma unroll
@@ -495,24 +515,26 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               tc_commit(&m.sfull[wg]);
               tc_commit(&m.empty[ks_]);
-              if (!q.pair) tc_commit(&m.empty[ks_]);   // both arrivals are this warpgroup's
               if (last) tc_commit(&m.qempty[wg]);
-              // O += P V
-              if (!(ok = mbar_wait(&m.pfull[wg], i & 1, abort_flag, p.err))) break;
+              // O += P V, the upper half of the keys first
               if (x == first && jobs > 0 &&
-                  !(ok = mbar_wait(&m.ofree[wg], (jobs - 1) & 1, abort_flag, p.err)))
+                  !(ok = wait_bar(&m.ofree[wg], (jobs - 1) & 1, abort_flag, p.err)))
                 break;
-              if (!(ok = mbar_wait(&m.full[vs_], (vi / R) & 1, abort_flag, p.err))) break;
+              if (!(ok = wait_bar(&m.full[vs_], (vi / R) & 1, abort_flag, p.err))) break;
               if (rag && x == q.n - 1 && !(ok = wait_count(fixed, ragged, abort_flag, p.err)))
                 break;
-              tc_fence_after();
               const uint32_t va = ring + vs_ * L::kTile;
 #pragma unroll
-              for (int ks = 0; ks < 8; ++ks)
-                tc_mma_ts(tO, tS + ks * 8, smem_desc(va + ks * 16 * 128, 16384, 1024, 2), kIdescO,
-                          (x > first || ks > 0) ? 1u : 0u);
+              for (int hf = 1; hf >= 0; --hf) {
+                if (!(ok = wait_bar(&m.pfull[2 * wg + hf], i & 1, abort_flag, p.err))) break;
+                tc_fence_after();
+#pragma unroll
+                for (int ks = 4 * hf; ks < 4 * hf + 4; ++ks)
+                  tc_mma_ts(tO, tS + 64 + ks * 8, smem_desc(va + ks * 16 * 128, 16384, 1024, 2),
+                            kIdescO, (x > first || ks != 4) ? 1u : 0u);
+              }
+              if (!ok) break;
               tc_commit(&m.empty[vs_]);
-              if (!q.pair) tc_commit(&m.empty[vs_]);
               if (last) tc_commit(&m.olast[wg]);
             }
             ++jobs;
@@ -554,45 +576,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         logit = p.logits + (static_cast<long long>(q.b * p.G + q.g) * p.rows_s + row) * p.nb * 128;
       float mref = -INFINITY, l = 0.f;
       for (int x = first; x < q.n; x += step, ++i) {
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&m.sfull[wg], i & 1, abort_flag, p.err)))) break;
+        if (!(ok = __all_sync(0xffffffffu, wait_bar(&m.sfull[wg], i & 1, abort_flag, p.err)))) break;
         if (busy) {
           tc_fence_after();
           const int j = q.j0 + x;
-          float sv[128];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, sv + c * 32);
-          tc_wait_ld();
           const int lim = last_key - j * 128;        // keys past lim are not seen
-          if (!__all_sync(0xffffffffu, lim >= 127)) {
+          const bool whole = __all_sync(0xffffffffu, lim >= 127);
+          // Half of the row's 128 logits is in registers at a time: keys 0..63
+          // for the maximum alone, then 64..127 for both, then 0..63 again
+          // (TMEM is read at 4 times the rate at which the rest goes).
+          float sv[64];
+          float mraw = -INFINITY;
 #pragma unroll
-            for (int y = 0; y < 128; ++y) sv[y] = y <= lim ? sv[y] : -INFINITY;
-          }
-          if (logit) {
+          for (int hf = 0; hf < 2; ++hf) {
+            load_half(tS, hf, lim, whole, sv);
+            if (logit) {
 #pragma unroll
-            for (int y = 0; y < 128; y += 8) {
-              float t8[8];
+              for (int y = 0; y < 64; y += 8) {
+                float t8[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) t8[e] = sv[y + e] * p.scale_log2;
-              store8(logit + j * 128 + y, t8);
+                for (int e = 0; e < 8; ++e) t8[e] = sv[y + e] * p.scale_log2;
+                store8(logit + j * 128 + hf * 64 + y, t8);
+              }
             }
-          }
-          float m4[4] = {sv[0], sv[1], sv[2], sv[3]};
+            float m4[4] = {mraw, sv[0], sv[1], sv[2]};
 #pragma unroll
-          for (int y = 4; y < 128; y += 8) {
-            m4[0] = fmax3(m4[0], sv[y], sv[y + 1]);
-            m4[1] = fmax3(m4[1], sv[y + 2], sv[y + 3]);
-            if (y + 4 < 128) {
-              m4[2] = fmax3(m4[2], sv[y + 4], sv[y + 5]);
-              m4[3] = fmax3(m4[3], sv[y + 6], sv[y + 7]);
-            }
+            for (int y = 3; y + 1 < 64; y += 2)
+              m4[(y >> 1) & 3] = fmax3(m4[(y >> 1) & 3], sv[y], sv[y + 1]);
+            mraw = fmax3(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]), sv[63]);
           }
-          const float mblk = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2;
+          const float mblk = mraw * p.scale_log2;
           // a row whose maximum outgrew its reference rescales O; S of this block
           // was issued after the product of the block before, so that one is complete
           const bool grow = mblk > mref + kRescaleLog2;
           if (__any_sync(0xffffffffu, grow && x > first)) {
             const float a = grow ? fast_exp2(mref - mblk) : 1.f;
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               float ov[32];
               tmem_ld32(tO + c * 32, ov);
@@ -607,28 +626,37 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float mu = mref == -INFINITY ? 0.f : mref;   // a row that has seen no key yet
           const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2), mm2 = f2_pack(-mu, -mu);
           uint64_t l2[4] = {0, 0, 0, 0};
+          // P goes over the columns of the upper half of S, so that the lower
+          // half stays readable
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t pk[16];
+          for (int hf = 1; hf >= 0; --hf) {
+            if (hf == 0) load_half(tS, 0, lim, whole, sv);
 #pragma unroll
-            for (int y = 0; y < 32; y += 2) {
-              const float2 e = f2_unpack(ffma2(f2_pack(sv[c * 32 + y], sv[c * 32 + y + 1]), sc2, mm2));
-              const float e0 = fast_exp2(e.x), e1 = fast_exp2(e.y);
-              pk[y >> 1] = pack2(e0, e1);
-              l2[(y >> 1) & 3] = fadd2(l2[(y >> 1) & 3], f2_pack(e0, e1));
+            for (int c = 0; c < 2; ++c) {
+              uint32_t pk[16];
+#pragma unroll
+              for (int y = 0; y < 32; y += 2) {
+                const float2 e = f2_unpack(ffma2(f2_pack(sv[c * 32 + y], sv[c * 32 + y + 1]), sc2, mm2));
+                const float e0 = fast_exp2(e.x), e1 = fast_exp2(e.y);
+                pk[y >> 1] = pack2(e0, e1);
+                l2[(y >> 1) & 3] = fadd2(l2[(y >> 1) & 3], f2_pack(e0, e1));
+              }
+              tmem_st16(tS + 64 + hf * 32 + c * 16, pk);
             }
-            tmem_st16(tS + c * 16, pk);
+            tc_wait_st();
+            tc_fence_before();
+            mbar_arrive(&m.pfull[2 * wg + hf]);
           }
           const float2 la = f2_unpack(fadd2(fadd2(l2[0], l2[1]), fadd2(l2[2], l2[3])));
           l += la.x + la.y;
-          tc_wait_st();
-          tc_fence_before();
+        } else {
+          mbar_arrive(&m.pfull[2 * wg + 1]);
+          mbar_arrive(&m.pfull[2 * wg]);
         }
-        mbar_arrive(&m.pfull[wg]);
       }
       if (!ok) break;
       // the partial of this CTA and warpgroup
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait(&m.olast[wg], jobs & 1, abort_flag, p.err)))) break;
+      if (!(ok = __all_sync(0xffffffffu, wait_bar(&m.olast[wg], jobs & 1, abort_flag, p.err)))) break;
       if (busy) {
         tc_fence_after();
         float* orow = (q.own ? p.o_s : p.o_p) + prow * D;
