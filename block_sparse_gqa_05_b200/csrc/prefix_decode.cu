@@ -20,12 +20,13 @@
 // cheaper than reading K again.
 //
 // In the CTA: warp 0 streams K and V through a ring of tiles by TMA; warps 1
-// and 2 issue the MMAs of the two warpgroups' tiles (S = Q K^T to TMEM, then
-// O += P V with P read from TMEM over S); warp 3 loads the queries and zeroes
-// the V rows of a segment's last block that lie past its length (their weight
-// is zero, but 0 * NaN is not); warps 4..7 and 8..11 are the two softmax
-// warpgroups, one TMEM lane (row) per thread.  O is rescaled only when a row's
-// maximum grows by more than 2^8 over the one it was accumulated with.
+// and 2 load the queries and issue the MMAs of the two warpgroups' tiles (S = Q
+// K^T to TMEM, then O += P V with P read from TMEM over S); warp 3 zeroes the V
+// rows past a segment's length in its last 16-row step (their weight is zero,
+// but 0 * NaN is not; steps past it are neither loaded nor multiplied); warps
+// 4..7 and 8..11 are the two softmax warpgroups, one TMEM lane (row) per
+// thread.  O is rescaled only when a row's maximum grows by more than 2^8 over
+// the one it was accumulated with.
 #include <math.h>
 
 #include <algorithm>
@@ -61,7 +62,10 @@ struct PrefixParams {
   int B, T, H, G, r, C, nb, num_pages;
   int Np, nbp;         // prefix rows and blocks
   int ntile, npt, nsp; // prefix row tiles and tile pairs of a group; prefix segments
-  int rows_p, rows_s;  // rows of a prefix / own partial: min(128, B*T*r), T*r
+  int rows_p, rows_s;  // rows of a prefix / own tile: min(128, B*T*r), T*r
+  bool spread_p, spread_s;   // such a tile is there four times, a quarter of the keys each
+  bool two_q;          // own queries have two stages, q_stage bytes apart
+  int q_stage;
   int grid;
   long long cost_pair, cost_group, cost_prefix;   // of a pair segment, a group's, all prefix segments
   float scale_log2;
@@ -162,10 +166,8 @@ struct Walk {
 
 // First of the CTA's blocks of a segment that warpgroup ``wg`` takes, and the
 // step to its next one; n0 the number of blocks the CTA had before.  The
-// blocks of single segments alternate along the whole walk, so a warpgroup
-// never skips two blocks in a row: with a ring of four tiles or more the tile
-// it waits for is then the next or the present load of its ring slot, which
-// is what a wait on the parity of a phase can tell apart.
+// blocks of single segments alternate along the whole walk, so that short
+// segments share the warpgroups.
 __device__ __forceinline__ int first_block(const Seg& q, int wg, int n0) {
   return q.pair ? 0 : ((n0 ^ wg) & 1);
 }
@@ -174,6 +176,15 @@ __device__ __forceinline__ int block_step(const Seg& q) { return q.pair ? 1 : 2;
 __device__ __forceinline__ bool ragged_end(const Seg& q) {
   return q.j0 + q.n == q.nb && (q.rows & 127) != 0;
 }
+
+// 16-row steps of a segment's last block that hold valid rows.
+__device__ __forceinline__ int tail_steps(const Seg& q) { return ((q.rows & 127) + 15) >> 4; }
+
+// TMA maps: queries of a prefix tile and of a sequence; K and V in blocks of
+// 128 rows and in steps of 16.
+struct PrefixMaps {
+  CUtensorMap qp, qs, kp, vp, k, v, kp16, vp16, k16, v16;
+};
 
 template <int D>
 struct PrefixSmem {
@@ -185,12 +196,13 @@ struct PrefixSmem {
 };
 
 struct Bars {
-  uint64_t *full, *empty;            // [ring]
-  uint64_t *qfull, *qempty;          // [2] per warpgroup
-  uint64_t* sfull;                   // [2]
-  uint64_t* pfull;                   // [2][2] per warpgroup and half of the keys
-  uint64_t *olast, *ofree;           // [2]
-  uint64_t* drain;                   // [2] the MMA threads' last commits
+  uint64_t *full, *empty;   // [ring] K or V tile loaded / released by both warpgroups
+  uint64_t* qfull;          // [2][2] per warpgroup: queries loaded, alternating
+  uint64_t* sfull;          // [2] S complete
+  uint64_t* pfull;          // [2][2] per warpgroup and half of the keys: P written
+  uint64_t *olast, *ofree;  // [2] a segment's O complete / read
+  uint64_t* turn;           // [2] of a pair: the warpgroup's turn at the tensor cores
+  uint64_t* drain;          // [2] the MMA threads' last commits
 };
 
 // Sets *word, after everything this thread (and its warp, before a
@@ -246,6 +258,18 @@ __device__ __forceinline__ void load_half(uint32_t tS, int hf, int lim, bool who
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t phase, volatile int* abort,
                                          uint32_t* err) {
   return mbar_test(bar, phase) || mbar_wait(bar, phase, abort, err);
+}
+
+// Waits for K or V tile ``item`` of the ring.  The parity of a slot's phase
+// tells its present load from the one before, but not from the one before
+// that; a warp that skips tiles (another warpgroup's) may come that early, as
+// loads complete in any order.  So it first waits for the load to be issued,
+// which happens after the slot's previous tile was loaded and released.
+template <int R>
+__device__ __forceinline__ bool wait_tile(const Bars& m, const uint32_t* issued, int item,
+                                          volatile int* abort, uint32_t* err) {
+  return wait_count(issued, static_cast<uint32_t>(item) + 1u, abort, err) &&
+         wait_bar(&m.full[item % R], (item / R) & 1, abort, err);
 }
 
 // The CTA's range of the line and where its walk starts, by all threads.
@@ -325,12 +349,7 @@ __device__ __forceinline__ void plan(const PrefixParams& p, long long* scratch, 
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    prefix_attn_kernel(const __grid_constant__ CUtensorMap tm_qp,
-                       const __grid_constant__ CUtensorMap tm_qs,
-                       const __grid_constant__ CUtensorMap tm_kp,
-                       const __grid_constant__ CUtensorMap tm_vp,
-                       const __grid_constant__ CUtensorMap tm_k,
-                       const __grid_constant__ CUtensorMap tm_v, const PrefixParams p) {
+    prefix_attn_kernel(const __grid_constant__ PrefixMaps tm, const PrefixParams p) {
   using L = PrefixSmem<D>;
   constexpr int R = L::kRing;
   constexpr uint32_t kIdescS = idesc_bf16(128, 128, 0, 0);
@@ -347,15 +366,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   m.full = bars;
   m.empty = bars + R;
   m.qfull = bars + 2 * R;
-  m.qempty = m.qfull + 2;
   m.sfull = m.qfull + 4;
   m.pfull = m.qfull + 6;
   m.olast = m.qfull + 10;
   m.ofree = m.qfull + 12;
-  m.drain = m.qfull + 14;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(m.qfull + 16);
-  uint32_t* issued = tmem_slot + 1;                  // ragged V tiles loaded so far
-  uint32_t* fixed = tmem_slot + 2;                   // and zeroed past their length
+  m.turn = m.qfull + 14;
+  m.drain = m.qfull + 16;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(m.qfull + 18);
+  uint32_t* issued = tmem_slot + 1;                  // K and V tiles whose loads were issued
+  uint32_t* fixed = tmem_slot + 2;                   // ragged V tiles zeroed past their length
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 3);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -365,24 +384,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&m.empty[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&m.qfull[i], 1);
-      mbar_init(&m.qempty[i], 1);
+      mbar_init(&m.qfull[2 * i], 1);
+      mbar_init(&m.qfull[2 * i + 1], 1);
       mbar_init(&m.sfull[i], 1);
       mbar_init(&m.pfull[2 * i], 128);
       mbar_init(&m.pfull[2 * i + 1], 128);
       mbar_init(&m.olast[i], 1);
       mbar_init(&m.ofree[i], 128);
+      mbar_init(&m.turn[i], 1);
       mbar_init(&m.drain[i], 1);
     }
     *issued = *fixed = 0;
     *abort_flag = 0;
     fence_barrier_init();
-    tma_prefetch_desc(&tm_qp);
-    tma_prefetch_desc(&tm_qs);
-    tma_prefetch_desc(&tm_kp);
-    tma_prefetch_desc(&tm_vp);
-    tma_prefetch_desc(&tm_k);
-    tma_prefetch_desc(&tm_v);
+    tma_prefetch_desc(&tm.qp);
+    tma_prefetch_desc(&tm.qs);
+    tma_prefetch_desc(&tm.kp);
+    tma_prefetch_desc(&tm.vp);
+    tma_prefetch_desc(&tm.k);
+    tma_prefetch_desc(&tm.v);
   }
   if (warp == 1) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
@@ -399,16 +419,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   Seg q;
 
   if (warp < 4) {
-    regs_dec<80>();
+    regs_dec<104>();
     if (warp == 0) {
       // ------------------------------------------------------- K and V tiles
       if (lane == 0) {
         int item = 0;      // tiles issued: K of block n is 2n, V is 2n + 1
-        uint32_t ragged = 0;
         bool ok = true;
         while (ok && walk.next(p, q)) {
-          const CUtensorMap* mk = q.own || p.prefix_pages ? &tm_k : &tm_kp;
-          const CUtensorMap* mv = q.own || p.prefix_pages ? &tm_v : &tm_vp;
+          const bool own = q.own || p.prefix_pages;   // which maps
+          const bool rag = ragged_end(q);
           for (int j = q.j0; ok && j < q.j0 + q.n; ++j) {
             int y = j * 128, z = q.own ? q.b * p.G + q.g : q.g;
             if (q.own ? p.table != nullptr : p.prefix_pages != nullptr) {
@@ -417,94 +436,110 @@ __global__ void __launch_bounds__(kThreads, 1)
                          : page_of(p.prefix_pages, 0, p.num_pages, 0, j, p.err)) *
                       p.G + q.g;
             }
+            // of a block with rows past the length only the 16-row steps with valid ones
+            const int part = rag && j == q.nb - 1 ? tail_steps(q) : 0;
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv, ++item) {
               const int st = item % R;
               if (!(ok = wait_bar(&m.empty[st], ((item / R) & 1) ^ 1, abort_flag, p.err))) break;
-              mbar_arrive_expect_tx(&m.full[st], L::kTile);
               if (!q.pair) mbar_arrive(&m.empty[st]);   // only one warpgroup will release it
+              uint8_t* dst = smem + L::kOffRing + st * L::kTile;
+              if (part == 0) {
+                const CUtensorMap* map = kv ? (own ? &tm.v : &tm.vp) : (own ? &tm.k : &tm.kp);
+                mbar_arrive_expect_tx(&m.full[st], L::kTile);
 #pragma unroll
-              for (int c = 0; c < D / 64; ++c)
-                tma_load_3d(smem + L::kOffRing + st * L::kTile + c * 16384, kv ? mv : mk,
-                            &m.full[st], c * 64, y, z);
+                for (int c = 0; c < D / 64; ++c)
+                  tma_load_3d(dst + c * 16384, map, &m.full[st], c * 64, y, z);
+              } else {
+                const CUtensorMap* map =
+                    kv ? (own ? &tm.v16 : &tm.vp16) : (own ? &tm.k16 : &tm.kp16);
+                mbar_arrive_expect_tx(&m.full[st], static_cast<uint32_t>(part * 16 * D * 2));
+                for (int u = 0; u < part; ++u)
+#pragma unroll
+                  for (int c = 0; c < D / 64; ++c)
+                    tma_load_3d(dst + c * 16384 + u * 2048, map, &m.full[st], c * 64, y + u * 16, z);
+              }
+              publish_count(issued, static_cast<uint32_t>(item) + 1u);
             }
           }
-          if (ok && ragged_end(q)) publish_count(issued, ++ragged);
         }
         // every load issued lands before the CTA may exit
         for (int x = max(0, item - R); x < item; ++x) mbar_drain(&m.full[x % R], (x / R) & 1);
       }
       __syncwarp();
     } else if (warp == 3) {
-      // ------------------------------------- queries, and the ragged V tiles
+      // ------------------------- V rows past a length, within its last 16 rows
       int n0 = 0;                  // blocks of the segments before
-      int jobs[2] = {0, 0};
       uint32_t ragged = 0;
-      bool ok = true;
-      while (ok && walk.next(p, q)) {
-        if (lane == 0) {
-#pragma unroll
-          for (int wg = 0; wg < 2; ++wg) {
-            if (!ok || first_block(q, wg, n0) >= q.n) continue;
-            if (!(ok = wait_bar(&m.qempty[wg], (jobs[wg] & 1) ^ 1, abort_flag, p.err))) continue;
-            ++jobs[wg];
-            const CUtensorMap* mq = q.own ? &tm_qs : &tm_qp;
-            const int rows = q.own ? p.rows_s : 128;
-            const int tok = q.own ? q.b * p.T : (q.tile + (q.pair ? wg : 0)) * (128 / p.r);
-            mbar_arrive_expect_tx(&m.qfull[wg], static_cast<uint32_t>(rows * D * 2));
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c)
-              tma_load_3d(smem + wg * L::kTile + c * 16384, mq, &m.qfull[wg], c * 64, q.g * p.r,
-                          tok);
-          }
-        }
-        ok = __shfl_sync(0xffffffffu, ok, 0) != 0;
-        if (ok && ragged_end(q)) {
-          const int item = 2 * (n0 + q.n) - 1;
-          const int st = item % R;
-          // once its load is issued the slot stays this tile's until it is
-          // zeroed, so the parity of its phase is not ambiguous
-          ok = wait_count(issued, ++ragged, abort_flag, p.err);
-          ok = __all_sync(0xffffffffu, ok && wait_bar(&m.full[st], (item / R) & 1, abort_flag, p.err));
-          if (!ok) break;
-          const int tail = q.rows & 127;
-          uint8_t* v = smem + L::kOffRing + st * L::kTile;
-          for (int x = lane; x < (128 - tail) * (D / 8); x += 32) {
-            const int c = x / ((128 - tail) * 8), y = x - c * (128 - tail) * 8;
-            *reinterpret_cast<uint4*>(v + c * 16384 + tail * 128 + y * 16) = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) publish_count(fixed, ragged);
-        }
+      while (walk.next(p, q)) {
         n0 += q.n;
+        if (!ragged_end(q)) continue;
+        const int item = 2 * n0 - 1;
+        const int st = item % R;
+        if (!__all_sync(0xffffffffu, wait_tile<R>(m, issued, item, abort_flag, p.err))) break;
+        ++ragged;
+        const int tail = q.rows & 127, rows = tail_steps(q) * 16 - tail;
+        uint8_t* v = smem + L::kOffRing + st * L::kTile + tail * 128;
+        for (int x = lane; x < rows * 8; x += 32)
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            *reinterpret_cast<uint4*>(v + c * 16384 + x * 16) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) publish_count(fixed, ragged);
       }
-      if (lane == 0)
-        for (int wg = 0; wg < 2; ++wg)
-          if (jobs[wg] > 0) mbar_drain(&m.qfull[wg], (jobs[wg] - 1) & 1);
-      __syncwarp();
     } else {
-      // ---------------------------------------- the MMAs of one warpgroup's tiles
+      // ------------------------- queries and MMAs of one warpgroup's tiles
       const int wg = warp - 1;
       if (lane == 0) {
         const uint32_t tS = tmem + wg * 128, tO = tmem + 256 + wg * 128;
-        const uint32_t qa = smem_u32(smem + wg * L::kTile);
+        uint8_t* qbuf = smem + wg * L::kTile;
         const uint32_t ring = smem_u32(smem + L::kOffRing);
-        int n0 = 0, i = 0, jobs = 0;
+        // Queries are loaded one segment ahead.  Own segments use two stages
+        // when their rows fit twice; otherwise the tile is free once the
+        // softmax has read the segment's last S.
+        Walk ahead = walk;
+        Seg nq;
+        int n0 = 0, n0a = 0, i = 0, jobs = 0, loads = 0, pairs = 0, stage = 0;
         uint32_t ragged = 0;
+        auto load_next = [&]() {
+          while (ahead.next(p, nq)) {
+            const int first = first_block(nq, wg, n0a);
+            n0a += nq.n;
+            if (first >= nq.n) continue;
+            const int sg = nq.own && p.two_q ? loads & 1 : 0;
+            uint64_t* bar = &m.qfull[2 * wg + (loads & 1)];
+            ++loads;
+            const CUtensorMap* map = nq.own ? &tm.qs : &tm.qp;
+            const int rows = nq.own ? p.rows_s : p.rows_p;
+            const int tok = nq.own ? nq.b * p.T : (nq.tile + (nq.pair ? wg : 0)) * (128 / p.r);
+            const int copies = (nq.own ? p.spread_s : p.spread_p) ? 4 : 1;
+            mbar_arrive_expect_tx(bar, static_cast<uint32_t>(copies * rows * D * 2));
+            for (int u = 0; u < copies; ++u)
+#pragma unroll
+              for (int c = 0; c < D / 64; ++c)
+                tma_load_3d(qbuf + sg * p.q_stage + c * 16384 + u * 4096, map, bar, c * 64,
+                            nq.g * p.r, tok);
+            return;
+          }
+        };
+        load_next();
         bool ok = true;
         while (ok && walk.next(p, q)) {
           const bool rag = ragged_end(q);
           ragged += rag ? 1u : 0u;
           const int first = first_block(q, wg, n0), step = block_step(q);
           if (first < q.n) {
-            if (!(ok = wait_bar(&m.qfull[wg], jobs & 1, abort_flag, p.err))) break;
-            for (int x = first; x < q.n; x += step, ++i) {
-              const bool last = x + step >= q.n;
-              const int ki = 2 * (n0 + x), vi = ki + 1;
-              const int ks_ = ki % R, vs_ = vi % R;
-              // S = Q K^T, over the P that the product before this one has read
-              if (!(ok = wait_bar(&m.full[ks_], (ki / R) & 1, abort_flag, p.err))) break;
+            stage = q.own && p.two_q ? jobs & 1 : 0;
+            const uint32_t qa = smem_u32(qbuf + stage * p.q_stage);
+            if (!(ok = wait_bar(&m.qfull[2 * wg + (jobs & 1)], (jobs >> 1) & 1, abort_flag, p.err)))
+              break;
+            const bool early = q.own && p.two_q;
+            if (early) load_next();
+            // S = Q K^T, over the P that the product before this one has read
+            auto issue_s = [&](int x) -> bool {
+              const int ki = 2 * (n0 + x), ks_ = ki % R;
+              if (!wait_tile<R>(m, issued, ki, abort_flag, p.err)) return false;
               tc_fence_after();
               const uint32_t ka = ring + ks_ * L::kTile;
 #pragma unroll
@@ -515,72 +550,209 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               tc_commit(&m.sfull[wg]);
               tc_commit(&m.empty[ks_]);
-              if (last) tc_commit(&m.qempty[wg]);
-              // O += P V, the upper half of the keys first
+              return true;
+            };
+            if (!(ok = issue_s(first))) break;
+            for (int x = first; x < q.n; x += step, ++i) {
+              const bool last = x + step >= q.n;
+              const int vi = 2 * (n0 + x) + 1, vs_ = vi % R;
+              // O += P V, the upper half of the keys first; past a length only
+              // the 16-key steps that hold valid rows
               if (x == first && jobs > 0 &&
                   !(ok = wait_bar(&m.ofree[wg], (jobs - 1) & 1, abort_flag, p.err)))
                 break;
-              if (!(ok = wait_bar(&m.full[vs_], (vi / R) & 1, abort_flag, p.err))) break;
-              if (rag && x == q.n - 1 && !(ok = wait_count(fixed, ragged, abort_flag, p.err)))
-                break;
+              if (!(ok = wait_tile<R>(m, issued, vi, abort_flag, p.err))) break;
+              int steps = 8;
+              if (rag && x == q.n - 1) {
+                steps = tail_steps(q);
+                if (!(ok = wait_count(fixed, ragged, abort_flag, p.err))) break;
+              }
+              // Of a pair the two warpgroups take turns at the tensor cores,
+              // O += P V and the next S together, so that one is in its
+              // softmax while the other's products run
+              if (q.pair) {
+                if (wg == 0) {
+                  if (pairs > 0 &&
+                      !(ok = wait_bar(&m.turn[0], (pairs - 1) & 1, abort_flag, p.err)))
+                    break;
+                } else if (!(ok = wait_bar(&m.turn[1], pairs & 1, abort_flag, p.err))) {
+                  break;
+                }
+                ++pairs;
+              }
               const uint32_t va = ring + vs_ * L::kTile;
+              uint32_t acc = x > first ? 1u : 0u;
 #pragma unroll
               for (int hf = 1; hf >= 0; --hf) {
                 if (!(ok = wait_bar(&m.pfull[2 * wg + hf], i & 1, abort_flag, p.err))) break;
                 tc_fence_after();
 #pragma unroll
-                for (int ks = 4 * hf; ks < 4 * hf + 4; ++ks)
+                for (int ks = 4 * hf; ks < 4 * hf + 4; ++ks) {
+                  if (ks >= steps) break;
                   tc_mma_ts(tO, tS + 64 + ks * 8, smem_desc(va + ks * 16 * 128, 16384, 1024, 2),
-                            kIdescO, (x > first || ks != 4) ? 1u : 0u);
+                            kIdescO, acc);
+                  acc = 1u;
+                }
               }
               if (!ok) break;
               tc_commit(&m.empty[vs_]);
-              if (last) tc_commit(&m.olast[wg]);
+              if (last)
+                tc_commit(&m.olast[wg]);
+              else if (!(ok = issue_s(x + step)))
+                break;
+              if (q.pair) mbar_arrive(&m.turn[1 - wg]);
             }
             ++jobs;
+            if (ok && !early) load_next();
           }
           n0 += q.n;
         }
-        // every MMA issued completes before TMEM is released
+        // every load and MMA issued completes before TMEM is released
+        for (int x = max(0, loads - 2); x < loads; ++x)
+          mbar_drain(&m.qfull[2 * wg + (x & 1)], (x >> 1) & 1);
         tc_drain(&m.drain[wg], 0);
       }
       __syncwarp();
     }
   } else {
-    regs_inc<208>();
+    regs_inc<192>();
     // ------------------------------------------------------ softmax, one row a thread
-    const int wg = (warp >> 2) - 1;
-    const int row = (warp & 3) * 32 + lane;
-    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const int wg = (warp >> 2) - 1, quarter = warp & 3;
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t tS = tmem + wg * 128 + lane_off, tO = tmem + 256 + wg * 128 + lane_off;
     int n0 = 0, i = 0, jobs = 0;
     bool ok = true;
+    // The output of a segment is written after the softmax of the next one's
+    // first block, so that its last product runs meanwhile.
+    bool pend = false, pend_busy = false, pend_valid = false;
+    float* pend_o = nullptr;
+    auto write_out = [&]() -> bool {
+      if (!pend) return true;
+      pend = false;
+      if (!__all_sync(0xffffffffu, wait_bar(&m.olast[wg], (jobs - 1) & 1, abort_flag, p.err)))
+        return false;
+      if (pend_busy) {
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          float ov[64];
+          tmem_ld32(tO + c * 64, ov);
+          tmem_ld32(tO + c * 64 + 32, ov + 32);
+          tc_wait_ld();
+          if (pend_valid) {
+#pragma unroll
+            for (int y = 0; y < 64; y += 8) store8(pend_o + c * 64 + y, ov + y);
+          }
+        }
+        tc_fence_before();
+      }
+      mbar_arrive(&m.ofree[wg]);
+      return true;
+    };
     while (ok && walk.next(p, q)) {
       const int first = first_block(q, wg, n0), step = block_step(q);
       n0 += q.n;
-      // rows of the tile that exist, this row's last key, and where its partial goes
+      // Rows of the tile that exist, this thread's row and its last key.  A tile
+      // of few rows is there four times, once per warp, and each warp takes a
+      // quarter of every block's keys: four partials.
+      const bool spread = q.own ? p.spread_s : p.spread_p;
       const int tile = q.tile + (q.pair ? wg : 0);
       const int nrow = q.own ? p.rows_s : min(128, p.B * p.T * p.r - tile * 128);
-      const int last_key = q.own ? q.rows - p.T + row / p.r : q.rows - 1;
-      const bool busy = (warp & 3) * 32 < nrow;      // warps without a row only keep the pace
+      const int row = spread ? lane : quarter * 32 + lane;
+      const bool busy = spread || quarter * 32 < nrow;   // a warp without a row only keeps the pace
       const bool valid = row < nrow;
+      const int last_key = q.own ? q.rows - p.T + row / p.r : q.rows - 1;
       const long long part =
           2ll * (static_cast<long long>(q.own ? q.id - p.nsp : q.id) + blockIdx.x) + wg;
-      const long long prow = part * (q.own ? p.rows_s : p.rows_p) + row;
+      const int rows = q.own ? p.rows_s : p.rows_p;
+      const long long prow = spread ? (part * 4 + quarter) * rows + row : part * rows + row;
+      float2* ml = (q.own ? p.ml_s : p.ml_p) + prow;
       if (first >= q.n) {              // the one block of a short share is the other warpgroup's
-        if (valid) (q.own ? p.ml_s : p.ml_p)[prow] = make_float2(-INFINITY, 0.f);
+        if (valid) *ml = make_float2(-INFINITY, 0.f);
         continue;
       }
       float* logit = nullptr;
       if (q.own && p.logits && valid)
         logit = p.logits + (static_cast<long long>(q.b * p.G + q.g) * p.rows_s + row) * p.nb * 128;
       float mref = -INFINITY, l = 0.f;
+      // O of the rows whose maximum outgrew its reference is rescaled; S of a
+      // block is issued after the product of the block before, so that one is
+      // complete
+      auto new_max = [&](float mblk, bool later) {
+        const bool grow = valid && mblk > mref + kRescaleLog2;
+        if (__any_sync(0xffffffffu, grow && later)) {
+          const float a = grow ? fast_exp2(mref - mblk) : 1.f;
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            float ov[32];
+            tmem_ld32(tO + c * 32, ov);
+            tc_wait_ld();
+#pragma unroll
+            for (int y = 0; y < 32; ++y) ov[y] *= a;
+            tmem_st32(tO + c * 32, ov);
+          }
+          l *= a;
+        }
+        if (grow) mref = mblk;
+        return mref == -INFINITY ? 0.f : mref;   // a row that has seen no key yet
+      };
       for (int x = first; x < q.n; x += step, ++i) {
         if (!(ok = __all_sync(0xffffffffu, wait_bar(&m.sfull[wg], i & 1, abort_flag, p.err)))) break;
-        if (busy) {
+        const int j = q.j0 + x;
+        const int lim = last_key - j * 128;        // keys past lim are not seen
+        const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
+        if (spread) {
           tc_fence_after();
-          const int j = q.j0 + x;
-          const int lim = last_key - j * 128;        // keys past lim are not seen
+          const int k0 = quarter * 32;
+          float sv[32];
+          tmem_ld32(tS + k0, sv);
+          tc_wait_ld();
+          if (!__all_sync(0xffffffffu, lim >= k0 + 31)) {
+#pragma unroll
+            for (int y = 0; y < 32; ++y) sv[y] = k0 + y <= lim ? sv[y] : -INFINITY;
+          }
+          if (logit) {
+#pragma unroll
+            for (int y = 0; y < 32; y += 8) {
+              float t8[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) t8[e] = sv[y + e] * p.scale_log2;
+              store8(logit + j * 128 + k0 + y, t8);
+            }
+          }
+          float m4[4] = {sv[0], sv[1], sv[2], sv[3]};
+#pragma unroll
+          for (int y = 4; y < 32; y += 2)
+            m4[(y >> 1) & 3] = fmax3(m4[(y >> 1) & 3], sv[y], sv[y + 1]);
+          const float mu = new_max(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2,
+                                   x > first);
+          const uint64_t mm2 = f2_pack(-mu, -mu);
+          uint64_t l2[2] = {0, 0};
+          uint32_t pk[16], zero[16];
+#pragma unroll
+          for (int y = 0; y < 32; y += 2) {
+            const float2 e = f2_unpack(ffma2(f2_pack(sv[y], sv[y + 1]), sc2, mm2));
+            const float e0 = fast_exp2(e.x), e1 = fast_exp2(e.y);
+            pk[y >> 1] = pack2(e0, e1);
+            zero[y >> 1] = 0u;
+            l2[(y >> 1) & 1] = fadd2(l2[(y >> 1) & 1], f2_pack(e0, e1));
+          }
+          // this copy's weights of the other warps' keys are zero
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if (c == quarter)
+              tmem_st16(tS + 64 + c * 16, pk);
+            else
+              tmem_st16(tS + 64 + c * 16, zero);
+          }
+          const float2 la = f2_unpack(fadd2(l2[0], l2[1]));
+          l += la.x + la.y;
+          tc_wait_st();
+          tc_fence_before();
+          mbar_arrive(&m.pfull[2 * wg + 1]);
+          mbar_arrive(&m.pfull[2 * wg]);
+        } else if (busy) {
+          tc_fence_after();
           const bool whole = __all_sync(0xffffffffu, lim >= 127);
           // Half of the row's 128 logits is in registers at a time: keys 0..63
           // for the maximum alone, then 64..127 for both, then 0..63 again
@@ -605,26 +777,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               m4[(y >> 1) & 3] = fmax3(m4[(y >> 1) & 3], sv[y], sv[y + 1]);
             mraw = fmax3(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]), sv[63]);
           }
-          const float mblk = mraw * p.scale_log2;
-          // a row whose maximum outgrew its reference rescales O; S of this block
-          // was issued after the product of the block before, so that one is complete
-          const bool grow = mblk > mref + kRescaleLog2;
-          if (__any_sync(0xffffffffu, grow && x > first)) {
-            const float a = grow ? fast_exp2(mref - mblk) : 1.f;
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              float ov[32];
-              tmem_ld32(tO + c * 32, ov);
-              tc_wait_ld();
-#pragma unroll
-              for (int y = 0; y < 32; ++y) ov[y] *= a;
-              tmem_st32(tO + c * 32, ov);
-            }
-            l *= a;
-          }
-          if (grow) mref = mblk;
-          const float mu = mref == -INFINITY ? 0.f : mref;   // a row that has seen no key yet
-          const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2), mm2 = f2_pack(-mu, -mu);
+          const float mu = new_max(mraw * p.scale_log2, x > first);
+          const uint64_t mm2 = f2_pack(-mu, -mu);
           uint64_t l2[4] = {0, 0, 0, 0};
           // P goes over the columns of the upper half of S, so that the lower
           // half stays readable
@@ -653,29 +807,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&m.pfull[2 * wg + 1]);
           mbar_arrive(&m.pfull[2 * wg]);
         }
+        if (x == first && !(ok = write_out())) break;
       }
       if (!ok) break;
       // the partial of this CTA and warpgroup
-      if (!(ok = __all_sync(0xffffffffu, wait_bar(&m.olast[wg], jobs & 1, abort_flag, p.err)))) break;
-      if (busy) {
-        tc_fence_after();
-        float* orow = (q.own ? p.o_s : p.o_p) + prow * D;
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          float ov[32];
-          tmem_ld32(tO + c * 32, ov);
-          tc_wait_ld();
-          if (valid) {
-#pragma unroll
-            for (int y = 0; y < 32; y += 8) store8(orow + c * 32 + y, ov + y);
-          }
-        }
-        if (valid) (q.own ? p.ml_s : p.ml_p)[prow] = make_float2(mref, l);
-        tc_fence_before();
-      }
-      mbar_arrive(&m.ofree[wg]);
+      if (valid) *ml = make_float2(mref, l);
+      pend = true;
+      pend_busy = busy;
+      pend_valid = valid;
+      pend_o = (q.own ? p.o_s : p.o_p) + prow * D;
       ++jobs;
     }
+    if (ok) write_out();
   }
 
   tc_fence_before();
@@ -693,6 +836,7 @@ struct Parts {
   int c0, n, nb, w, id, row, rows;
   bool own, pair;
   int wg;       // of a pair: the warpgroup of the row's tile
+  int sub;      // partials of a warpgroup: 4 of a spread tile, else 1
 };
 
 __device__ __forceinline__ Parts parts_of(const PrefixParams& p, long long total, bool own, int b,
@@ -701,6 +845,7 @@ __device__ __forceinline__ Parts parts_of(const PrefixParams& p, long long total
   const int g = h / p.r, hr = h - g * p.r;
   s.own = own;
   s.pair = false;
+  s.sub = (own ? p.spread_s : p.spread_p) ? 4 : 1;
   s.wg = 0;
   s.w = kCostSingle;
   if (own) {
@@ -724,21 +869,22 @@ __device__ __forceinline__ Parts parts_of(const PrefixParams& p, long long total
   s.c0 = 0;
   if (s.nb > 0) {
     s.c0 = cta_of(s.start, total, p.grid);
-    s.n = 2 * (cta_of(s.start + static_cast<long long>(s.nb - 1) * s.w, total, p.grid) - s.c0 + 1);
+    s.n = 2 * s.sub * (cta_of(s.start + static_cast<long long>(s.nb - 1) * s.w, total, p.grid) - s.c0 + 1);
   }
   return s;
 }
 
-// Partial k of the list (two a CTA): its index, or -1 when that CTA had no
+// Partial k of the list (two warpgroups a CTA): its index, or -1 when that CTA had no
 // block of the segment, or of a pair when it is the other tile's.
 __device__ __forceinline__ long long part_at(const PrefixParams& p, const Parts& s, long long total,
                                              int k) {
-  const int c = s.c0 + (k >> 1), wg = k & 1;
+  const int sub = k & (s.sub - 1), k2 = s.sub == 4 ? k >> 2 : k;
+  const int c = s.c0 + (k2 >> 1), wg = k2 & 1;
   const int n = blocks_before(cta_begin(c + 1, total, p.grid), s.start, s.w, s.nb) -
                 blocks_before(cta_begin(c, total, p.grid), s.start, s.w, s.nb);
   if (n <= 0 || (s.pair && wg != s.wg)) return -1;
   const long long part = 2ll * ((s.own ? s.id - p.nsp : s.id) + c) + wg;
-  return part * s.rows + s.row;
+  return (part * s.sub + sub) * s.rows + s.row;
 }
 
 constexpr int kMergeWarps = 8;
@@ -862,6 +1008,10 @@ __global__ void __launch_bounds__(kScoreThreads) prefix_score_kernel(const Prefi
   }
 }
 
+// Most rows of a tile that is spread over the four warps: 32 lie in a warp's
+// TMEM lanes; own tiles need them twice, for the next segment's queries.
+constexpr size_t kSpreadPrefix = 32, kSpreadOwn = 16;
+
 // Workspace layout.
 struct PrefixWs {
   size_t starts, lse2, ml_p, o_p, ml_s, o_s, logits, bytes;
@@ -872,8 +1022,9 @@ PrefixWs ws_layout(const msa_shape& s, bool weights) {
   const size_t rows = static_cast<size_t>(s.batch) * s.seq_q * r;
   const size_t bg = static_cast<size_t>(s.batch) * s.n_kv_heads;
   const size_t nsp = static_cast<size_t>(ceil_div(ceil_div(rows, 128), 2)) * s.n_kv_heads;
-  const size_t pr = 2 * (nsp + kMaxGrid) * std::min<size_t>(rows, 128);
-  const size_t sr = 2 * (bg + kMaxGrid) * s.seq_q * r;
+  const size_t rp = std::min<size_t>(rows, 128), rs = s.seq_q * r;
+  const size_t pr = 2 * (nsp + kMaxGrid) * rp * (rp <= kSpreadPrefix ? 4 : 1);
+  const size_t sr = 2 * (bg + kMaxGrid) * rs * (rs <= kSpreadOwn ? 4 : 1);
   PrefixWs w{};
   size_t at = 0;
   auto take = [&](size_t n) {
@@ -895,11 +1046,11 @@ PrefixWs ws_layout(const msa_shape& s, bool weights) {
 template <int D>
 cudaError_t launch(const msa_shape& s, const PrefixDecodeArgs& a, const PrefixParams& p,
                    cudaStream_t st) {
-  CUtensorMap tqp, tqs, tkp, tvp, tk, tv;
+  PrefixMaps tm;
   const uint64_t D8 = D;
   const uint64_t dq[3] = {D8, static_cast<uint64_t>(p.H), static_cast<uint64_t>(p.B) * p.T};
   const uint64_t sq[2] = {D8 * 2, static_cast<uint64_t>(p.H) * D * 2};
-  const uint32_t bqp[3] = {64, static_cast<uint32_t>(p.r), static_cast<uint32_t>(128 / p.r)};
+  const uint32_t bqp[3] = {64, static_cast<uint32_t>(p.r), static_cast<uint32_t>(p.rows_p / p.r)};
   const uint32_t bqs[3] = {64, static_cast<uint32_t>(p.r), static_cast<uint32_t>(p.T)};
   // contiguous: [B*G][C][d]; paged: [num_pages*G][128][d]
   const bool paged = a.pages.table != nullptr;
@@ -907,7 +1058,7 @@ cudaError_t launch(const msa_shape& s, const PrefixDecodeArgs& a, const PrefixPa
   const uint64_t mats = static_cast<uint64_t>(paged ? p.num_pages : p.B) * p.G;
   const uint64_t dk[3] = {D8, rows, mats};
   const uint64_t sk[2] = {D8 * 2, rows * D * 2};
-  const uint32_t bk[3] = {64, 128, 1};
+  const uint32_t bk[3] = {64, 128, 1}, b16[3] = {64, 16, 1};
   const uint64_t dp[3] = {D8, static_cast<uint64_t>(std::max(a.prefix_cap, 1)),
                           static_cast<uint64_t>(p.G)};
   const uint64_t sp[2] = {D8 * 2, dp[1] * D * 2};
@@ -917,10 +1068,15 @@ cudaError_t launch(const msa_shape& s, const PrefixDecodeArgs& a, const PrefixPa
     return encode_tmap(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box,
                        CU_TENSOR_MAP_SWIZZLE_128B);
   };
-  if (!enc(&tqp, a.q, dq, sq, bqp) || !enc(&tqs, a.q, dq, sq, bqs) || !enc(&tk, a.k, dk, sk, bk) ||
-      !enc(&tv, a.v, dk, sk, bk) || !enc(&tkp, pre ? a.kp : a.k, pre ? dp : dk, pre ? sp : sk, bk) ||
-      !enc(&tvp, pre ? a.vp : a.v, pre ? dp : dk, pre ? sp : sk, bk))
-    return cudaErrorInvalidValue;
+  bool ok = enc(&tm.qp, a.q, dq, sq, bqp) && enc(&tm.qs, a.q, dq, sq, bqs) &&
+            enc(&tm.k, a.k, dk, sk, bk) && enc(&tm.v, a.v, dk, sk, bk) &&
+            enc(&tm.k16, a.k, dk, sk, b16) && enc(&tm.v16, a.v, dk, sk, b16);
+  if (pre)
+    ok = ok && enc(&tm.kp, a.kp, dp, sp, bk) && enc(&tm.vp, a.vp, dp, sp, bk) &&
+         enc(&tm.kp16, a.kp, dp, sp, b16) && enc(&tm.vp16, a.vp, dp, sp, b16);
+  else
+    tm.kp = tm.k, tm.vp = tm.v, tm.kp16 = tm.k16, tm.vp16 = tm.v16;
+  if (!ok) return cudaErrorInvalidValue;
   const size_t smem = PrefixSmem<D>::kBytes;
   cudaError_t e = cudaFuncSetAttribute(prefix_attn_kernel<D>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -929,7 +1085,7 @@ cudaError_t launch(const msa_shape& s, const PrefixDecodeArgs& a, const PrefixPa
   {
     ProfScope ps_("prefix_attn", st);
     e = launch_dependent(prefix_attn_kernel<D>, dim3(static_cast<unsigned>(p.grid)), dim3(kThreads),
-                         smem, st, tqp, tqs, tkp, tvp, tk, tv, p);
+                         smem, st, tm, p);
   }
   if (e != cudaSuccess) return e;
   {
@@ -993,6 +1149,10 @@ cudaError_t launch_prefix_decode(const msa_shape& s, const PrefixDecodeArgs& a, 
   p.nsp = p.Np > 0 ? p.npt * p.G : 0;
   p.rows_p = static_cast<int>(std::min<int64_t>(rows, 128));
   p.rows_s = p.T * p.r;
+  p.spread_p = rows <= static_cast<int64_t>(kSpreadPrefix);
+  p.spread_s = p.rows_s <= static_cast<int>(kSpreadOwn);
+  p.two_q = p.rows_s <= 64;
+  p.q_stage = p.spread_s ? 16 * 128 : 64 * 128;
   p.cost_pair = static_cast<long long>(p.nbp) * kCostPair + kCostSegment;
   const long long last = (p.ntile & 1) ? static_cast<long long>(p.nbp) * kCostSingle + kCostSegment
                                        : p.cost_pair;

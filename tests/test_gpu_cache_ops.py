@@ -184,6 +184,25 @@ def test_paged_caches_give_the_contiguous_result(i):
     c.check(op, lp, wp)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kw", [
+    dict(B=4, T=1, H=8, G=1, Np=200001, C=300, lens=[300, 0, 1, 177]),      # one tile, few rows
+    dict(B=20, T=1, H=8, G=1, Np=100000, C=300, lens=[15 * i for i in range(20)]),   # a pair
+    dict(B=11, T=1, H=8, G=1, Np=150000, C=130, lens=[13 * i for i in range(11)]),   # one full tile
+    dict(B=2, T=1, H=8, G=1, Np=0, C=90000, lens=[90000, 61111]),           # long own caches
+    dict(B=2, T=5, H=8, G=1, Np=300, C=50000, lens=[49999, 3]),
+])
+def test_many_blocks_per_cta(kw, d):
+    c = Case(d=d, seed=60, **kw)
+    got = c.run()
+    torch.cuda.synchronize()
+    assert M.device_status() == 0
+    c.check(*got)
+    for _ in range(5):
+        assert all(torch.equal(a, b) for a, b in zip(got, c.run()))
+    assert M.device_status() == 0
+
+
 def test_scores_in_place_and_from_zero():
     c = Case(seed=70, **CASES[3])
     _, _, w = c.run()
