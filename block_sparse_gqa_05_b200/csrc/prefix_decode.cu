@@ -12,7 +12,9 @@
 //           flight and splits the keys between two accumulators.
 // The blocks of all segments form one line, weighted by what a block of each
 // kind costs, which is cut evenly over a persistent grid of one CTA per SM
-// (the lengths are read on the device).  Every (CTA, segment, warpgroup) leaves
+// (the lengths are read on the device: a warp of each CTA walks its part of the
+// line and hands the others one descriptor a segment, as five copies of the
+// walk made the code too large for the instruction cache).  Every (CTA, segment, warpgroup) leaves
 // an unnormalised partial output with its running maximum and sum in fp32; a
 // second kernel merges them.  With scores wanted, the logits of own keys go to
 // the workspace (4 T r bytes per key against 4 d for its K and V) and a third
@@ -21,12 +23,12 @@
 //
 // In the CTA: warp 0 streams K and V through a ring of tiles by TMA; warps 1
 // and 2 load the queries and issue the MMAs of the two warpgroups' tiles (S = Q
-// K^T to TMEM, then O += P V with P read from TMEM over S); warp 3 zeroes the V
-// rows past a segment's length in its last 16-row step (their weight is zero,
-// but 0 * NaN is not; steps past it are neither loaded nor multiplied); warps
-// 4..7 and 8..11 are the two softmax warpgroups, one TMEM lane (row) per
-// thread.  O is rescaled only when a row's maximum grows by more than 2^8 over
-// the one it was accumulated with.
+// K^T to TMEM, then O += P V with P read from TMEM over S), and zero the V rows
+// past a segment's length in its last 16-row step (their weight is zero, but
+// 0 * NaN is not; steps past it are neither loaded nor multiplied); warp 3 walks
+// the line; warps 4..7 and 8..11 are the two softmax warpgroups, one TMEM lane
+// (row) per thread.  O is rescaled only when a row's maximum grows by more than
+// 2^8 over the one it was accumulated with.
 #include <math.h>
 
 #include <algorithm>
@@ -52,7 +54,7 @@ struct PrefixParams {
   float* w_out;
   const int32_t *lens, *prefix_pages, *table;
   uint32_t* err;
-  long long* starts;   // [B + 1] line cost of one group of sequences 0 .. b-1
+  int2* span;          // [nsp + B*G] first and last CTA with blocks of a segment
   float* lse2;         // [B*T*H] normalisers, log2
   float2* ml_p;        // [(nsp + grid) * 2, rows_p]  (maximum, sum) of prefix partials
   float* o_p;          // [(nsp + grid) * 2, rows_p, D]
@@ -66,7 +68,6 @@ struct PrefixParams {
   bool spread_p, spread_s;   // such a tile is there four times, a quarter of the keys each
   bool two_q;          // own queries have two stages, q_stage bytes apart
   int q_stage;
-  int grid;
   long long cost_pair, cost_group, cost_prefix;   // of a pair segment, a group's, all prefix segments
   float scale_log2;
 };
@@ -84,13 +85,10 @@ __device__ __forceinline__ int blocks_of(int rows) { return (rows + 127) >> 7; }
 // Line cost of one group's segment over a sequence's own cache.
 __device__ __forceinline__ int own_cost(int nb) { return nb ? nb * kCostSingle + kCostSegment : 0; }
 
-// Line range [cta_begin(c), cta_begin(c + 1)) of CTA c; a block belongs to the
-// CTA in whose range it starts.
-__device__ __forceinline__ long long cta_begin(long long c, long long total, int grid) {
-  return (c * total + grid - 1) / grid;
-}
-__device__ __forceinline__ int cta_of(long long pos, long long total, int grid) {
-  return static_cast<int>(pos * grid / total);
+// The line is cut into ``parts`` ranges [part_begin(c), part_begin(c + 1)); a
+// block belongs to the range it starts in.
+__device__ __forceinline__ long long part_begin(long long c, long long total, int parts) {
+  return (c * total + parts - 1) / parts;
 }
 
 // Blocks of a segment that start at ``start`` and cost ``w`` each, up to line
@@ -101,84 +99,90 @@ __device__ __forceinline__ int blocks_before(long long u, long long start, int w
   return d >= static_cast<long long>(nb) * w ? nb : (static_cast<int>(d) + w - 1) / w;
 }
 
-// One CTA's share of a segment.
-struct Seg {
-  int id;            // index of the segment: prefix segments, then b * G + g
-  int j0, n;         // first block and number of blocks
-  int nb, rows;      // blocks and valid keys of the whole segment
-  int b, g, tile;    // own: sequence and group; prefix: group and first row tile
-  bool own, pair;
+// One CTA's share of a segment, as the walk hands it on (n == 0: the end).
+struct __align__(16) Seg {
+  int id;          // index of the segment: prefix segments, then b * G + g
+  int j0, n;       // first block and number of blocks
+  int rows;        // valid keys of the whole segment
+  int b, g;        // own: sequence and group; prefix: group
+  int tile_kind;   // prefix: first row tile << 2; | kPair | kOwn
+  int n0;          // blocks of the CTA before
+  __device__ __forceinline__ bool own() const { return (tile_kind & 1) != 0; }
+  __device__ __forceinline__ bool pair() const { return (tile_kind & 2) != 0; }
+  __device__ __forceinline__ int tile() const { return tile_kind >> 2; }
+  // First of these blocks that warpgroup wg takes, and the step to its next
+  // one.  The blocks of single segments alternate along the whole walk, so that
+  // short segments share the warpgroups.
+  __device__ __forceinline__ int first(int wg) const { return pair() ? 0 : ((n0 ^ wg) & 1); }
+  __device__ __forceinline__ int step() const { return pair() ? 1 : 2; }
+  // Whether the share ends in a block with rows past the segment's length, and
+  // the 16-row steps of that block that hold valid rows.
+  __device__ __forceinline__ bool ragged() const {
+    return j0 + n == ((rows + 127) >> 7) && (rows & 127) != 0;
+  }
+  __device__ __forceinline__ int tail_steps() const { return ((rows & 127) + 15) >> 4; }
 };
 
-// Walks a CTA's segments along the line, the same way in every role.
+// Walks a CTA's segments along the line.
 struct Walk {
   long long u0, u1, pos;
-  int s, b, g, len;
+  int s, b, g, len, n0;
 
-  __device__ __forceinline__ bool next(const PrefixParams& p, Seg& q) {
+  __device__ __forceinline__ Seg next(const PrefixParams& p) {
+    Seg q;
     for (;;) {
-      int w;
+      int w, nb;
       const long long start = pos;
       if (s < p.nsp) {
-        q.own = false;
+        const int g_ = s / p.npt, tile = 2 * (s - g_ * p.npt);
+        const bool pair = tile + 1 < p.ntile;
         q.id = s;
-        q.g = s / p.npt;
-        q.tile = 2 * (s - q.g * p.npt);
-        q.pair = q.tile + 1 < p.ntile;
         q.b = 0;
-        q.nb = p.nbp;
+        q.g = g_;
+        q.tile_kind = tile << 2 | (pair ? 2 : 0);
         q.rows = p.Np;
-        w = q.pair ? kCostPair : kCostSingle;
-        pos += static_cast<long long>(p.nbp) * w + kCostSegment;
+        nb = p.nbp;
+        w = pair ? kCostPair : kCostSingle;
+        pos += static_cast<long long>(nb) * w + kCostSegment;
         ++s;
       } else {
-        if (b >= p.B) return false;
-        if (len < 0) len = own_len(p, b);
-        if (len == 0) {
+        if (b < p.B && len < 0) len = own_len(p, b);
+        if (b < p.B && len == 0) {
           ++b;
           g = 0;
           len = -1;
           continue;
         }
-        q.own = true;
-        q.pair = false;
         q.id = p.nsp + b * p.G + g;
         q.b = b;
         q.g = g;
-        q.tile = 0;
-        q.nb = blocks_of(len);
+        q.tile_kind = 1;
         q.rows = len;
+        nb = blocks_of(len);
         w = kCostSingle;
-        pos += own_cost(q.nb);
-        if (++g == p.G) {
+        if (b < p.B) pos += own_cost(nb);
+        if (++g >= p.G) {
           g = 0;
           ++b;
           len = -1;
         }
       }
-      if (start >= u1) return false;
-      q.j0 = blocks_before(u0, start, w, q.nb);
-      q.n = blocks_before(u1, start, w, q.nb) - q.j0;
-      if (q.n > 0) return true;
+      if (start >= u1) {
+        q.n = 0;
+        return q;
+      }
+      q.j0 = blocks_before(u0, start, w, nb);
+      q.n = blocks_before(u1, start, w, nb) - q.j0;
+      q.n0 = n0;
+      if (q.n > 0) {
+        n0 += q.n;
+        if (q.j0 == 0) p.span[q.id].x = blockIdx.x;
+        if (q.j0 + q.n == nb) p.span[q.id].y = blockIdx.x;
+        return q;
+      }
     }
   }
 };
-
-// First of the CTA's blocks of a segment that warpgroup ``wg`` takes, and the
-// step to its next one; n0 the number of blocks the CTA had before.  The
-// blocks of single segments alternate along the whole walk, so that short
-// segments share the warpgroups.
-__device__ __forceinline__ int first_block(const Seg& q, int wg, int n0) {
-  return q.pair ? 0 : ((n0 ^ wg) & 1);
-}
-__device__ __forceinline__ int block_step(const Seg& q) { return q.pair ? 1 : 2; }
-// Whether the CTA's share ends in a block with rows past the segment's length.
-__device__ __forceinline__ bool ragged_end(const Seg& q) {
-  return q.j0 + q.n == q.nb && (q.rows & 127) != 0;
-}
-
-// 16-row steps of a segment's last block that hold valid rows.
-__device__ __forceinline__ int tail_steps(const Seg& q) { return ((q.rows & 127) + 15) >> 4; }
 
 // TMA maps: queries of a prefix tile and of a sequence; K and V in blocks of
 // 128 rows and in steps of 16.
@@ -186,42 +190,57 @@ struct PrefixMaps {
   CUtensorMap qp, qs, kp, vp, k, v, kp16, vp16, k16, v16;
 };
 
+constexpr int kSegRing = 8;        // descriptors the walk is ahead at most
+
 template <int D>
 struct PrefixSmem {
   static constexpr uint32_t kTile = 128u * D * 2u;
   static constexpr int kRing = D == 128 ? 5 : 10;       // K or V tiles in the ring
   static constexpr uint32_t kOffRing = 2 * kTile;       // two query tiles first
   static constexpr uint32_t kOffBar = kOffRing + kRing * kTile;
-  static constexpr uint32_t kBytes = kOffBar + 512;
+  static constexpr uint32_t kOffSeg = kOffBar + 640;
+  static constexpr uint32_t kBytes = kOffSeg + kSegRing * 32;
 };
 
 struct Bars {
   uint64_t *full, *empty;   // [ring] K or V tile loaded / released by both warpgroups
+  uint64_t *dfull, *dempty; // [kSegRing] descriptor written / read by all
   uint64_t* qfull;          // [2][2] per warpgroup: queries loaded, alternating
   uint64_t* sfull;          // [2] S complete
   uint64_t* pfull;          // [2][2] per warpgroup and half of the keys: P written
   uint64_t *olast, *ofree;  // [2] a segment's O complete / read
   uint64_t* turn;           // [2] of a pair: the warpgroup's turn at the tensor cores
-  uint64_t* drain;          // [2] the MMA threads' last commits
+  uint64_t* drain;          // [2] the MMA warps' last commits
 };
+
+// mbar_wait out of line behind a probe: most waits here are complete, and the
+// bounded loop at each of them is most of their code.
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t phase, volatile int* abort,
+                                       uint32_t* err) {
+  return mbar_wait(bar, phase, abort, err);
+}
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t phase, volatile int* abort,
+                                         uint32_t* err) {
+  return mbar_test(bar, phase) || wait_slow(bar, phase, abort, err);
+}
 
 // Sets *word, after everything this thread (and its warp, before a
 // __syncwarp) wrote.
 __device__ __forceinline__ void publish_count(const uint32_t* word, uint32_t v) {
   asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(smem_u32(word)), "r"(v) : "memory");
 }
-
+__device__ __forceinline__ uint32_t read_count(const uint32_t* word) {
+  uint32_t v;
+  asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(v) : "r"(smem_u32(word)) : "memory");
+  return v;
+}
 // Bounded wait until *word >= want (a count another warp publishes).
-__device__ __forceinline__ bool wait_count(const uint32_t* word, uint32_t want, volatile int* abort,
-                                           uint32_t* err) {
-  const uint32_t a = smem_u32(word);
+__device__ __noinline__ bool count_slow(const uint32_t* word, uint32_t want, volatile int* abort,
+                                        uint32_t* err) {
   const uint64_t lim = g_wait_limit_ns;
-  uint64_t t0 = 0;
+  const uint64_t t0 = globaltimer();
   for (uint32_t it = 0;; ++it) {
-    uint32_t v;
-    asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-    if (static_cast<int32_t>(v - want) >= 0) return true;
-    if (it == 0) t0 = globaltimer();
+    if (static_cast<int32_t>(read_count(word) - want) >= 0) return true;
     if (*abort) return false;
     if (lim == 0 || ((it & 63u) == 63u && globaltimer() - t0 > lim)) {
       atomicOr(err, kErrTimeout);
@@ -229,6 +248,27 @@ __device__ __forceinline__ bool wait_count(const uint32_t* word, uint32_t want, 
       return false;
     }
   }
+}
+
+// Waits for K or V tile ``item`` of the ring.  The parity of a slot's phase
+// tells its present load from the one before, but not from the one before
+// that; a warp that skips tiles (another warpgroup's) may come that early, as
+// loads complete in any order.  So it first waits for the load to be issued,
+// which happens after the slot's previous tile was loaded and released.
+template <int R>
+__device__ __forceinline__ bool wait_tile(const Bars& m, const uint32_t* issued, int item,
+                                          volatile int* abort, uint32_t* err) {
+  const uint32_t want = static_cast<uint32_t>(item) + 1u;
+  if (static_cast<int32_t>(read_count(issued) - want) < 0 && !count_slow(issued, want, abort, err))
+    return false;
+  return wait_bar(&m.full[item % R], (item / R) & 1, abort, err);
+}
+
+__device__ __forceinline__ Seg read_seg(const Seg* at) {
+  Seg q;
+  reinterpret_cast<int4*>(&q)[0] = reinterpret_cast<const int4*>(at)[0];
+  reinterpret_cast<int4*>(&q)[1] = reinterpret_cast<const int4*>(at)[1];
+  return q;
 }
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -243,37 +283,26 @@ __device__ __forceinline__ void store8(float* dst, const float* v) {
                : "memory");
 }
 
-// Keys 64 hf .. 64 hf + 63 of this thread's row of S, those past lim at -inf.
-__device__ __forceinline__ void load_half(uint32_t tS, int hf, int lim, bool whole, float* sv) {
-  tmem_ld32(tS + hf * 64, sv);
-  tmem_ld32(tS + hf * 64 + 32, sv + 32);
-  tc_wait_ld();
-  if (!whole) {
+// Logits of keys past lim to -inf (of the first 32 only when half).
+__device__ __forceinline__ void mask_keys(float* sv, int lim, bool half) {
+  if (__all_sync(0xffffffffu, lim >= (half ? 31 : 63))) return;
 #pragma unroll
-    for (int y = 0; y < 64; ++y) sv[y] = hf * 64 + y <= lim ? sv[y] : -INFINITY;
+  for (int y = 0; y < 64; ++y) sv[y] = y <= lim ? sv[y] : -INFINITY;
+}
+
+// 32 weights 2^(s scale - m) as bf16 pairs, and their sums in fp32.
+__device__ __forceinline__ void exp_keys(const float* sv, uint64_t sc2, uint64_t mm2, uint32_t* pk,
+                                         uint64_t* l2) {
+#pragma unroll
+  for (int y = 0; y < 32; y += 2) {
+    const float2 e = f2_unpack(ffma2(f2_pack(sv[y], sv[y + 1]), sc2, mm2));
+    const float e0 = fast_exp2(e.x), e1 = fast_exp2(e.y);
+    pk[y >> 1] = pack2(e0, e1);
+    l2[(y >> 1) & 3] = fadd2(l2[(y >> 1) & 3], f2_pack(e0, e1));
   }
 }
 
-// mbar_wait with a probe before anything else: most waits here are complete.
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t phase, volatile int* abort,
-                                         uint32_t* err) {
-  return mbar_test(bar, phase) || mbar_wait(bar, phase, abort, err);
-}
-
-// Waits for K or V tile ``item`` of the ring.  The parity of a slot's phase
-// tells its present load from the one before, but not from the one before
-// that; a warp that skips tiles (another warpgroup's) may come that early, as
-// loads complete in any order.  So it first waits for the load to be issued,
-// which happens after the slot's previous tile was loaded and released.
-template <int R>
-__device__ __forceinline__ bool wait_tile(const Bars& m, const uint32_t* issued, int item,
-                                          volatile int* abort, uint32_t* err) {
-  return wait_count(issued, static_cast<uint32_t>(item) + 1u, abort, err) &&
-         wait_bar(&m.full[item % R], (item / R) & 1, abort, err);
-}
-
 // The CTA's range of the line and where its walk starts, by all threads.
-// CTA 0 also publishes the sequences' line starts for the merge kernel.
 __device__ __forceinline__ void plan(const PrefixParams& p, long long* scratch, Walk* out) {
   const int tid = threadIdx.x;
   const int per = (p.B + kThreads - 1) / kThreads;
@@ -296,16 +325,12 @@ __device__ __forceinline__ void plan(const PrefixParams& p, long long* scratch, 
     all += scratch[i];
   }
   const long long total = p.cost_prefix + all * p.G;
-  const long long u0 = cta_begin(blockIdx.x, total, p.grid);
-  const long long u1 = cta_begin(blockIdx.x + 1, total, p.grid);
-  if (blockIdx.x == 0) {
-    long long at = before;
-    for (int b = b0; b < b1; ++b) {
-      p.starts[b] = at;
-      at += own_cost(blocks_of(own_len(p, b)));
-    }
-    if (tid == 0) p.starts[p.B] = all;
-  }
+  // no more parts than blocks there are: every part between a segment's first
+  // and last one then holds a block of it
+  const int parts = static_cast<int>(
+      max(1ll, min(static_cast<long long>(gridDim.x), total / max(kCostPair, kCostSingle))));
+  const long long u0 = min(total, part_begin(blockIdx.x, total, parts));
+  const long long u1 = min(total, part_begin(blockIdx.x + 1, total, parts));
   if (u0 < p.cost_prefix) {
     if (tid == 0) {
       const int g = static_cast<int>(u0 / p.cost_group);
@@ -344,12 +369,13 @@ __device__ __forceinline__ void plan(const PrefixParams& p, long long* scratch, 
   if (tid == 0) {
     out->u0 = u0;
     out->u1 = u1;
+    out->n0 = 0;
   }
 }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    prefix_attn_kernel(const __grid_constant__ PrefixMaps tm, const PrefixParams p) {
+    prefix_attn_kernel(const __grid_constant__ PrefixMaps tm, const __grid_constant__ PrefixParams p) {
   using L = PrefixSmem<D>;
   constexpr int R = L::kRing;
   constexpr uint32_t kIdescS = idesc_bf16(128, 128, 0, 0);
@@ -365,7 +391,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   Bars m;
   m.full = bars;
   m.empty = bars + R;
-  m.qfull = bars + 2 * R;
+  m.dfull = bars + 2 * R;
+  m.dempty = m.dfull + kSegRing;
+  m.qfull = m.dempty + kSegRing;
   m.sfull = m.qfull + 4;
   m.pfull = m.qfull + 6;
   m.olast = m.qfull + 10;
@@ -374,14 +402,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   m.drain = m.qfull + 16;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(m.qfull + 18);
   uint32_t* issued = tmem_slot + 1;                  // K and V tiles whose loads were issued
-  uint32_t* fixed = tmem_slot + 2;                   // ragged V tiles zeroed past their length
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 3);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 2);
+  Seg* segs = reinterpret_cast<Seg*>(smem + L::kOffSeg);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < R; ++i) {
       mbar_init(&m.full[i], 1);
       mbar_init(&m.empty[i], 2);
+    }
+    for (int i = 0; i < kSegRing; ++i) {
+      mbar_init(&m.dfull[i], 1);
+      mbar_init(&m.dempty[i], 11);       // the TMA, MMA and softmax warps
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&m.qfull[2 * i], 1);
@@ -394,7 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&m.turn[i], 1);
       mbar_init(&m.drain[i], 1);
     }
-    *issued = *fixed = 0;
+    *issued = 0;
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tm.qp);
@@ -415,45 +447,63 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;   // S/P of the warpgroups at 0 and 128, O at 256 and 384
-  Walk walk = walk0;
-  Seg q;
 
   if (warp < 4) {
-    regs_dec<104>();
-    if (warp == 0) {
+    if (warp == 3) {
+      // ------------------------------------------------------------ the walk
+      if (lane == 0) {
+        Walk walk = walk0;
+        for (int k = 0;; ++k) {
+          const Seg q = walk.next(p);
+          const int slot = k % kSegRing;
+          if (!wait_bar(&m.dempty[slot], ((k / kSegRing) & 1) ^ 1, abort_flag, p.err)) break;
+          reinterpret_cast<int4*>(segs + slot)[0] = reinterpret_cast<const int4*>(&q)[0];
+          reinterpret_cast<int4*>(segs + slot)[1] = reinterpret_cast<const int4*>(&q)[1];
+          mbar_arrive(&m.dfull[slot]);
+          if (q.n == 0) break;
+        }
+      }
+      __syncwarp();
+    } else if (warp == 0) {
       // ------------------------------------------------------- K and V tiles
       if (lane == 0) {
         int item = 0;      // tiles issued: K of block n is 2n, V is 2n + 1
         bool ok = true;
-        while (ok && walk.next(p, q)) {
-          const bool own = q.own || p.prefix_pages;   // which maps
-          const bool rag = ragged_end(q);
+        for (int k = 0; ok; ++k) {
+          const int ds = k % kSegRing;
+          if (!wait_bar(&m.dfull[ds], (k / kSegRing) & 1, abort_flag, p.err)) break;
+          const Seg q = read_seg(segs + ds);
+          if (q.n == 0) break;
+          mbar_arrive(&m.dempty[ds]);
+          const bool own = q.own();
+          const int32_t* table = own ? p.table + static_cast<long long>(q.b) * p.nb : p.prefix_pages;
+          const bool paged = own ? p.table != nullptr : p.prefix_pages != nullptr;
+          const bool kv_own = own || paged;           // which maps
+          const bool rag = q.ragged();
           for (int j = q.j0; ok && j < q.j0 + q.n; ++j) {
-            int y = j * 128, z = q.own ? q.b * p.G + q.g : q.g;
-            if (q.own ? p.table != nullptr : p.prefix_pages != nullptr) {
+            int y = j * 128, z = own ? q.b * p.G + q.g : q.g;
+            if (paged) {
               y = 0;
-              z = (q.own ? page_of(p.table, p.nb, p.num_pages, q.b, j, p.err)
-                         : page_of(p.prefix_pages, 0, p.num_pages, 0, j, p.err)) *
-                      p.G + q.g;
+              z = page_of(table, 0, p.num_pages, 0, j, p.err) * p.G + q.g;
             }
             // of a block with rows past the length only the 16-row steps with valid ones
-            const int part = rag && j == q.nb - 1 ? tail_steps(q) : 0;
-#pragma unroll
+            const int part = rag && j == q.j0 + q.n - 1 ? q.tail_steps() : 0;
+#pragma unroll 1
             for (int kv = 0; kv < 2; ++kv, ++item) {
               const int st = item % R;
               if (!(ok = wait_bar(&m.empty[st], ((item / R) & 1) ^ 1, abort_flag, p.err))) break;
-              if (!q.pair) mbar_arrive(&m.empty[st]);   // only one warpgroup will release it
+              if (!q.pair()) mbar_arrive(&m.empty[st]);   // only one warpgroup will release it
               uint8_t* dst = smem + L::kOffRing + st * L::kTile;
+              const CUtensorMap* map = kv_own ? (kv ? &tm.v : &tm.k) : (kv ? &tm.vp : &tm.kp);
               if (part == 0) {
-                const CUtensorMap* map = kv ? (own ? &tm.v : &tm.vp) : (own ? &tm.k : &tm.kp);
                 mbar_arrive_expect_tx(&m.full[st], L::kTile);
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c)
                   tma_load_3d(dst + c * 16384, map, &m.full[st], c * 64, y, z);
               } else {
-                const CUtensorMap* map =
-                    kv ? (own ? &tm.v16 : &tm.vp16) : (own ? &tm.k16 : &tm.kp16);
+                map += &tm.k16 - &tm.k;               // the same in 16-row steps
                 mbar_arrive_expect_tx(&m.full[st], static_cast<uint32_t>(part * 16 * D * 2));
+#pragma unroll 1
                 for (int u = 0; u < part; ++u)
 #pragma unroll
                   for (int c = 0; c < D / 64; ++c)
@@ -467,147 +517,155 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int x = max(0, item - R); x < item; ++x) mbar_drain(&m.full[x % R], (x / R) & 1);
       }
       __syncwarp();
-    } else if (warp == 3) {
-      // ------------------------- V rows past a length, within its last 16 rows
-      int n0 = 0;                  // blocks of the segments before
-      uint32_t ragged = 0;
-      while (walk.next(p, q)) {
-        n0 += q.n;
-        if (!ragged_end(q)) continue;
-        const int item = 2 * n0 - 1;
-        const int st = item % R;
-        if (!__all_sync(0xffffffffu, wait_tile<R>(m, issued, item, abort_flag, p.err))) break;
-        ++ragged;
-        const int tail = q.rows & 127, rows = tail_steps(q) * 16 - tail;
-        uint8_t* v = smem + L::kOffRing + st * L::kTile + tail * 128;
-        for (int x = lane; x < rows * 8; x += 32)
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c)
-            *reinterpret_cast<uint4*>(v + c * 16384 + x * 16) = make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) publish_count(fixed, ragged);
-      }
     } else {
       // ------------------------- queries and MMAs of one warpgroup's tiles
       const int wg = warp - 1;
-      if (lane == 0) {
-        const uint32_t tS = tmem + wg * 128, tO = tmem + 256 + wg * 128;
-        uint8_t* qbuf = smem + wg * L::kTile;
-        const uint32_t ring = smem_u32(smem + L::kOffRing);
-        // Queries are loaded one segment ahead.  Own segments use two stages
-        // when their rows fit twice; otherwise the tile is free once the
-        // softmax has read the segment's last S.
-        Walk ahead = walk;
-        Seg nq;
-        int n0 = 0, n0a = 0, i = 0, jobs = 0, loads = 0, pairs = 0, stage = 0;
-        uint32_t ragged = 0;
-        auto load_next = [&]() {
-          while (ahead.next(p, nq)) {
-            const int first = first_block(nq, wg, n0a);
-            n0a += nq.n;
-            if (first >= nq.n) continue;
-            const int sg = nq.own && p.two_q ? loads & 1 : 0;
+      const uint32_t tS = tmem + wg * 128, tO = tmem + 256 + wg * 128;
+      uint8_t* qbuf = smem + wg * L::kTile;
+      const uint32_t ring = smem_u32(smem + L::kOffRing);
+      int ka = 0, i = 0, jobs = 0, loads = 0, pairs = 0;
+      // Loads the queries of the warpgroup's next segment, if its descriptor is
+      // there (descriptors ka.. were not looked at).  Own segments use two
+      // stages when their rows fit twice and are loaded one ahead; otherwise
+      // the tile is free once the softmax has read the segment's last S.
+      auto load_next = [&](int k) {
+        for (; ka < k + kSegRing; ++ka) {
+          const int ds = ka % kSegRing;
+          if (!mbar_test(&m.dfull[ds], (ka / kSegRing) & 1)) return;
+          const Seg a = read_seg(segs + ds);
+          if (a.n == 0) return;
+          if (a.first(wg) >= a.n) continue;
+          if (lane == 0) {
+            const bool own = a.own();
             uint64_t* bar = &m.qfull[2 * wg + (loads & 1)];
-            ++loads;
-            const CUtensorMap* map = nq.own ? &tm.qs : &tm.qp;
-            const int rows = nq.own ? p.rows_s : p.rows_p;
-            const int tok = nq.own ? nq.b * p.T : (nq.tile + (nq.pair ? wg : 0)) * (128 / p.r);
-            const int copies = (nq.own ? p.spread_s : p.spread_p) ? 4 : 1;
+            uint8_t* dst = qbuf + (own && p.two_q ? (loads & 1) * p.q_stage : 0);
+            const CUtensorMap* map = own ? &tm.qs : &tm.qp;
+            const int rows = own ? p.rows_s : p.rows_p;
+            const int tok = own ? a.b * p.T : (a.tile() + (a.pair() ? wg : 0)) * (128 / p.r);
+            const int copies = (own ? p.spread_s : p.spread_p) ? 4 : 1;
             mbar_arrive_expect_tx(bar, static_cast<uint32_t>(copies * rows * D * 2));
+#pragma unroll 1
             for (int u = 0; u < copies; ++u)
 #pragma unroll
               for (int c = 0; c < D / 64; ++c)
-                tma_load_3d(qbuf + sg * p.q_stage + c * 16384 + u * 4096, map, bar, c * 64,
-                            nq.g * p.r, tok);
-            return;
+                tma_load_3d(dst + c * 16384 + u * 4096, map, bar, c * 64, a.g * p.r, tok);
           }
-        };
-        load_next();
-        bool ok = true;
-        while (ok && walk.next(p, q)) {
-          const bool rag = ragged_end(q);
-          ragged += rag ? 1u : 0u;
-          const int first = first_block(q, wg, n0), step = block_step(q);
-          if (first < q.n) {
-            stage = q.own && p.two_q ? jobs & 1 : 0;
-            const uint32_t qa = smem_u32(qbuf + stage * p.q_stage);
-            if (!(ok = wait_bar(&m.qfull[2 * wg + (jobs & 1)], (jobs >> 1) & 1, abort_flag, p.err)))
-              break;
-            const bool early = q.own && p.two_q;
-            if (early) load_next();
-            // S = Q K^T, over the P that the product before this one has read
-            auto issue_s = [&](int x) -> bool {
-              const int ki = 2 * (n0 + x), ks_ = ki % R;
-              if (!wait_tile<R>(m, issued, ki, abort_flag, p.err)) return false;
-              tc_fence_after();
-              const uint32_t ka = ring + ks_ * L::kTile;
-#pragma unroll
-              for (int ks = 0; ks < D / 16; ++ks) {
-                const uint32_t off = (ks >> 2) * 16384 + (ks & 3) * 32;
-                tc_mma_ss(tS, smem_desc(qa + off, 16, 1024, 2), smem_desc(ka + off, 16, 1024, 2),
-                          kIdescS, ks > 0 ? 1u : 0u);
-              }
-              tc_commit(&m.sfull[wg]);
-              tc_commit(&m.empty[ks_]);
-              return true;
-            };
-            if (!(ok = issue_s(first))) break;
-            for (int x = first; x < q.n; x += step, ++i) {
-              const bool last = x + step >= q.n;
-              const int vi = 2 * (n0 + x) + 1, vs_ = vi % R;
-              // O += P V, the upper half of the keys first; past a length only
-              // the 16-key steps that hold valid rows
-              if (x == first && jobs > 0 &&
-                  !(ok = wait_bar(&m.ofree[wg], (jobs - 1) & 1, abort_flag, p.err)))
-                break;
-              if (!(ok = wait_tile<R>(m, issued, vi, abort_flag, p.err))) break;
-              int steps = 8;
-              if (rag && x == q.n - 1) {
-                steps = tail_steps(q);
-                if (!(ok = wait_count(fixed, ragged, abort_flag, p.err))) break;
-              }
-              // Of a pair the two warpgroups take turns at the tensor cores,
-              // O += P V and the next S together, so that one is in its
-              // softmax while the other's products run
-              if (q.pair) {
-                if (wg == 0) {
-                  if (pairs > 0 &&
-                      !(ok = wait_bar(&m.turn[0], (pairs - 1) & 1, abort_flag, p.err)))
-                    break;
-                } else if (!(ok = wait_bar(&m.turn[1], pairs & 1, abort_flag, p.err))) {
-                  break;
-                }
-                ++pairs;
-              }
-              const uint32_t va = ring + vs_ * L::kTile;
-              uint32_t acc = x > first ? 1u : 0u;
-#pragma unroll
-              for (int hf = 1; hf >= 0; --hf) {
-                if (!(ok = wait_bar(&m.pfull[2 * wg + hf], i & 1, abort_flag, p.err))) break;
-                tc_fence_after();
-#pragma unroll
-                for (int ks = 4 * hf; ks < 4 * hf + 4; ++ks) {
-                  if (ks >= steps) break;
-                  tc_mma_ts(tO, tS + 64 + ks * 8, smem_desc(va + ks * 16 * 128, 16384, 1024, 2),
-                            kIdescO, acc);
-                  acc = 1u;
-                }
-              }
-              if (!ok) break;
-              tc_commit(&m.empty[vs_]);
-              if (last)
-                tc_commit(&m.olast[wg]);
-              else if (!(ok = issue_s(x + step)))
-                break;
-              if (q.pair) mbar_arrive(&m.turn[1 - wg]);
-            }
-            ++jobs;
-            if (ok && !early) load_next();
-          }
-          n0 += q.n;
+          __syncwarp();
+          ++loads;
+          ++ka;
+          return;
         }
-        // every load and MMA issued completes before TMEM is released
+      };
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        const int ds = k % kSegRing;
+        if (!(ok = __all_sync(0xffffffffu, wait_bar(&m.dfull[ds], (k / kSegRing) & 1, abort_flag, p.err))))
+          break;
+        const Seg q = read_seg(segs + ds);
+        if (q.n == 0) break;
+        const int first = q.first(wg), step = q.step();
+        if (first < q.n) {
+          const bool early = q.own() && p.two_q;
+          if (loads == jobs) {
+            ka = k;
+            load_next(k);
+          }
+          ka = max(ka, k + 1);
+          if (!(ok = __all_sync(0xffffffffu, wait_bar(&m.qfull[2 * wg + (jobs & 1)], (jobs >> 1) & 1,
+                                                      abort_flag, p.err))))
+            break;
+          if (early) load_next(k);
+          const uint32_t qa = smem_u32(qbuf) + (early ? (jobs & 1) * p.q_stage : 0);
+          const bool rag = q.ragged(), pair = q.pair();
+          for (int x = first; x < q.n; x += step, ++i) {
+            const bool last = x + step >= q.n;
+            // S = Q K^T, over the P that the product before this one has read
+            {
+              const int item = 2 * (q.n0 + x), st = item % R;
+              if (!(ok = __all_sync(0xffffffffu, wait_tile<R>(m, issued, item, abort_flag, p.err))))
+                break;
+              tc_fence_after();
+              const uint32_t ka_ = ring + st * L::kTile;
+              if (lane == 0) {
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                  const uint32_t off = (ks >> 2) * 16384 + (ks & 3) * 32;
+                  tc_mma_ss(tS, smem_desc(qa + off, 16, 1024, 2), smem_desc(ka_ + off, 16, 1024, 2),
+                            kIdescS, ks > 0 ? 1u : 0u);
+                }
+                tc_commit(&m.sfull[wg]);
+                tc_commit(&m.empty[st]);
+                if (pair && x > first) mbar_arrive(&m.turn[1 - wg]);
+              }
+              __syncwarp();
+            }
+            // O += P V, the upper half of the keys first; past a length only
+            // the 16-key steps that hold valid rows
+            if (x == first && jobs > 0 &&
+                !(ok = __all_sync(0xffffffffu,
+                                  wait_bar(&m.ofree[wg], (jobs - 1) & 1, abort_flag, p.err))))
+              break;
+            const int item = 2 * (q.n0 + x) + 1, st = item % R;
+            if (!(ok = __all_sync(0xffffffffu, wait_tile<R>(m, issued, item, abort_flag, p.err))))
+              break;
+            uint8_t* v = smem + L::kOffRing + st * L::kTile;
+            int steps = 8;
+            if (rag && x == q.n - 1) {
+              steps = q.tail_steps();
+              const int tail = q.rows & 127, units = (steps * 16 - tail) * 8;
+              for (int y = lane; y < units; y += 32)
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c)
+                  *reinterpret_cast<uint4*>(v + c * 16384 + tail * 128 + y * 16) =
+                      make_uint4(0, 0, 0, 0);
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
+            // Of a pair the two warpgroups take turns at the tensor cores, O +=
+            // P V and the next S together, so that one is in its softmax while
+            // the other's products run
+            if (pair) {
+              if ((wg == 1 || pairs > 0) &&
+                  !(ok = __all_sync(0xffffffffu, wait_bar(&m.turn[wg], (pairs - 1 + wg) & 1,
+                                                          abort_flag, p.err))))
+                break;
+              ++pairs;
+            }
+            const uint32_t va = smem_u32(v);
+            uint32_t acc = x > first ? 1u : 0u;
+#pragma unroll 1
+            for (int hf = 1; hf >= 0; --hf) {
+              if (!(ok = __all_sync(0xffffffffu, wait_bar(&m.pfull[2 * wg + hf], i & 1, abort_flag,
+                                                          p.err))))
+                break;
+              tc_fence_after();
+              const int todo = min(4, steps - 4 * hf);
+              if (lane == 0) {
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                  if (ks < todo)
+                    tc_mma_ts(tO, tS + 64 + (4 * hf + ks) * 8,
+                              smem_desc(va + (4 * hf + ks) * 16 * 128, 16384, 1024, 2), kIdescO,
+                              ks > 0 ? 1u : acc);
+              }
+              __syncwarp();
+              if (todo > 0) acc = 1u;
+            }
+            if (!ok) break;
+            if (lane == 0) {
+              tc_commit(&m.empty[st]);
+              if (last) tc_commit(&m.olast[wg]);
+              if (last && pair) mbar_arrive(&m.turn[1 - wg]);
+            }
+            __syncwarp();
+          }
+          ++jobs;
+          if (ok && loads == jobs) load_next(k);
+        }
+        if (lane == 0) mbar_arrive(&m.dempty[ds]);
+      }
+      // every load and MMA issued completes before TMEM is released
+      if (lane == 0) {
         for (int x = max(0, loads - 2); x < loads; ++x)
           mbar_drain(&m.qfull[2 * wg + (x & 1)], (x >> 1) & 1);
         tc_drain(&m.drain[wg], 0);
@@ -615,12 +673,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     }
   } else {
-    regs_inc<192>();
     // ------------------------------------------------------ softmax, one row a thread
     const int wg = (warp >> 2) - 1, quarter = warp & 3;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t tS = tmem + wg * 128 + lane_off, tO = tmem + 256 + wg * 128 + lane_off;
-    int n0 = 0, i = 0, jobs = 0;
+    const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
+    int i = 0, jobs = 0;
     bool ok = true;
     // The output of a segment is written after the softmax of the next one's
     // first block, so that its last product runs meanwhile.
@@ -633,15 +691,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         return false;
       if (pend_busy) {
         tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          float ov[64];
-          tmem_ld32(tO + c * 64, ov);
-          tmem_ld32(tO + c * 64 + 32, ov + 32);
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          float ov[32];
+          tmem_ld32(tO + c * 32, ov);
           tc_wait_ld();
           if (pend_valid) {
 #pragma unroll
-            for (int y = 0; y < 64; y += 8) store8(pend_o + c * 64 + y, ov + y);
+            for (int y = 0; y < 32; y += 8) store8(pend_o + c * 32 + y, ov + y);
           }
         }
         tc_fence_before();
@@ -649,157 +706,138 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(&m.ofree[wg]);
       return true;
     };
-    while (ok && walk.next(p, q)) {
-      const int first = first_block(q, wg, n0), step = block_step(q);
-      n0 += q.n;
+    for (int k = 0; ok; ++k) {
+      const int ds = k % kSegRing;
+      if (!(ok = __all_sync(0xffffffffu, wait_bar(&m.dfull[ds], (k / kSegRing) & 1, abort_flag, p.err))))
+        break;
+      const Seg q = read_seg(segs + ds);
+      __syncwarp();
+      if (q.n == 0) break;
+      if (lane == 0) mbar_arrive(&m.dempty[ds]);
+      const int first = q.first(wg), step = q.step();
+      const bool own = q.own();
       // Rows of the tile that exist, this thread's row and its last key.  A tile
       // of few rows is there four times, once per warp, and each warp takes a
       // quarter of every block's keys: four partials.
-      const bool spread = q.own ? p.spread_s : p.spread_p;
-      const int tile = q.tile + (q.pair ? wg : 0);
-      const int nrow = q.own ? p.rows_s : min(128, p.B * p.T * p.r - tile * 128);
+      const bool spread = own ? p.spread_s : p.spread_p;
+      const int tile = q.tile() + (q.pair() ? wg : 0);
+      const int nrow = own ? p.rows_s : min(128, p.B * p.T * p.r - tile * 128);
       const int row = spread ? lane : quarter * 32 + lane;
       const bool busy = spread || quarter * 32 < nrow;   // a warp without a row only keeps the pace
       const bool valid = row < nrow;
-      const int last_key = q.own ? q.rows - p.T + row / p.r : q.rows - 1;
-      const long long part =
-          2ll * (static_cast<long long>(q.own ? q.id - p.nsp : q.id) + blockIdx.x) + wg;
-      const int rows = q.own ? p.rows_s : p.rows_p;
+      const int last_key = own ? q.rows - p.T + row / p.r : q.rows - 1;
+      const long long part = 2ll * (static_cast<long long>(own ? q.id - p.nsp : q.id) + blockIdx.x) + wg;
+      const int rows = own ? p.rows_s : p.rows_p;
       const long long prow = spread ? (part * 4 + quarter) * rows + row : part * rows + row;
-      float2* ml = (q.own ? p.ml_s : p.ml_p) + prow;
+      float2* ml = (own ? p.ml_s : p.ml_p) + prow;
       if (first >= q.n) {              // the one block of a short share is the other warpgroup's
         if (valid) *ml = make_float2(-INFINITY, 0.f);
         continue;
       }
       float* logit = nullptr;
-      if (q.own && p.logits && valid)
+      if (own && p.logits && valid)
         logit = p.logits + (static_cast<long long>(q.b * p.G + q.g) * p.rows_s + row) * p.nb * 128;
       float mref = -INFINITY, l = 0.f;
-      // O of the rows whose maximum outgrew its reference is rescaled; S of a
-      // block is issued after the product of the block before, so that one is
-      // complete
-      auto new_max = [&](float mblk, bool later) {
-        const bool grow = valid && mblk > mref + kRescaleLog2;
-        if (__any_sync(0xffffffffu, grow && later)) {
-          const float a = grow ? fast_exp2(mref - mblk) : 1.f;
-#pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            float ov[32];
-            tmem_ld32(tO + c * 32, ov);
-            tc_wait_ld();
-#pragma unroll
-            for (int y = 0; y < 32; ++y) ov[y] *= a;
-            tmem_st32(tO + c * 32, ov);
-          }
-          l *= a;
-        }
-        if (grow) mref = mblk;
-        return mref == -INFINITY ? 0.f : mref;   // a row that has seen no key yet
-      };
       for (int x = first; x < q.n; x += step, ++i) {
         if (!(ok = __all_sync(0xffffffffu, wait_bar(&m.sfull[wg], i & 1, abort_flag, p.err)))) break;
         const int j = q.j0 + x;
         const int lim = last_key - j * 128;        // keys past lim are not seen
-        const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
-        if (spread) {
+        if (busy) {
           tc_fence_after();
-          const int k0 = quarter * 32;
-          float sv[32];
-          tmem_ld32(tS + k0, sv);
-          tc_wait_ld();
-          if (!__all_sync(0xffffffffu, lim >= k0 + 31)) {
-#pragma unroll
-            for (int y = 0; y < 32; ++y) sv[y] = k0 + y <= lim ? sv[y] : -INFINITY;
-          }
-          if (logit) {
-#pragma unroll
-            for (int y = 0; y < 32; y += 8) {
-              float t8[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) t8[e] = sv[y + e] * p.scale_log2;
-              store8(logit + j * 128 + k0 + y, t8);
-            }
-          }
-          float m4[4] = {sv[0], sv[1], sv[2], sv[3]};
-#pragma unroll
-          for (int y = 4; y < 32; y += 2)
-            m4[(y >> 1) & 3] = fmax3(m4[(y >> 1) & 3], sv[y], sv[y + 1]);
-          const float mu = new_max(fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * p.scale_log2,
-                                   x > first);
-          const uint64_t mm2 = f2_pack(-mu, -mu);
-          uint64_t l2[2] = {0, 0};
-          uint32_t pk[16], zero[16];
-#pragma unroll
-          for (int y = 0; y < 32; y += 2) {
-            const float2 e = f2_unpack(ffma2(f2_pack(sv[y], sv[y + 1]), sc2, mm2));
-            const float e0 = fast_exp2(e.x), e1 = fast_exp2(e.y);
-            pk[y >> 1] = pack2(e0, e1);
-            zero[y >> 1] = 0u;
-            l2[(y >> 1) & 1] = fadd2(l2[(y >> 1) & 1], f2_pack(e0, e1));
-          }
-          // this copy's weights of the other warps' keys are zero
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (c == quarter)
-              tmem_st16(tS + 64 + c * 16, pk);
-            else
-              tmem_st16(tS + 64 + c * 16, zero);
-          }
-          const float2 la = f2_unpack(fadd2(l2[0], l2[1]));
-          l += la.x + la.y;
-          tc_wait_st();
-          tc_fence_before();
-          mbar_arrive(&m.pfull[2 * wg + 1]);
-          mbar_arrive(&m.pfull[2 * wg]);
-        } else if (busy) {
-          tc_fence_after();
-          const bool whole = __all_sync(0xffffffffu, lim >= 127);
-          // Half of the row's 128 logits is in registers at a time: keys 0..63
-          // for the maximum alone, then 64..127 for both, then 0..63 again
-          // (TMEM is read at 4 times the rate at which the rest goes).
+          // Maximum of the keys this thread sees.  Of a full tile, half of the
+          // row's 128 logits is in registers at a time: keys 0..63 for the
+          // maximum alone, then 64..127 for both, then 0..63 again (TMEM is
+          // read at 4 times the rate at which the rest goes).  A warp of a
+          // spread tile holds its 32 keys in the lower half of sv.
           float sv[64];
           float mraw = -INFINITY;
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            load_half(tS, hf, lim, whole, sv);
+          const int k0 = spread ? quarter * 32 : 0, parts = spread ? 1 : 2;
+#pragma unroll 1
+          for (int hf = 0; hf < parts; ++hf) {
+            const int at = k0 + hf * 64;
+            tmem_ld32(tS + at, sv);
+            if (!spread) tmem_ld32(tS + at + 32, sv + 32);
+            tc_wait_ld();
+            mask_keys(sv, lim - at, spread);
             if (logit) {
+              float* dst = logit + j * 128 + at;
 #pragma unroll
               for (int y = 0; y < 64; y += 8) {
+                if (y >= 32 && spread) break;
                 float t8[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) t8[e] = sv[y + e] * p.scale_log2;
-                store8(logit + j * 128 + hf * 64 + y, t8);
+                store8(dst + y, t8);
               }
             }
             float m4[4] = {mraw, sv[0], sv[1], sv[2]};
 #pragma unroll
-            for (int y = 3; y + 1 < 64; y += 2)
+            for (int y = 3; y + 1 < 32; y += 2)
               m4[(y >> 1) & 3] = fmax3(m4[(y >> 1) & 3], sv[y], sv[y + 1]);
-            mraw = fmax3(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]), sv[63]);
+            m4[0] = fmaxf(m4[0], sv[31]);
+            if (!spread) {
+#pragma unroll
+              for (int y = 32; y < 64; y += 2)
+                m4[(y >> 1) & 3] = fmax3(m4[(y >> 1) & 3], sv[y], sv[y + 1]);
+            }
+            mraw = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
           }
-          const float mu = new_max(mraw * p.scale_log2, x > first);
+          const float mblk = mraw * p.scale_log2;
+          // O of the rows whose maximum outgrew its reference is rescaled; S of a
+          // block is issued after the product of the block before, so that one is
+          // complete
+          const bool grow = valid && mblk > mref + kRescaleLog2;
+          if (__any_sync(0xffffffffu, grow && x > first)) {
+            const float a = grow ? fast_exp2(mref - mblk) : 1.f;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              float ov[32];
+              tmem_ld32(tO + c * 32, ov);
+              tc_wait_ld();
+#pragma unroll
+              for (int y = 0; y < 32; ++y) ov[y] *= a;
+              tmem_st32(tO + c * 32, ov);
+            }
+            l *= a;
+          }
+          if (grow) mref = mblk;
+          const float mu = mref == -INFINITY ? 0.f : mref;   // a row that has seen no key yet
           const uint64_t mm2 = f2_pack(-mu, -mu);
           uint64_t l2[4] = {0, 0, 0, 0};
-          // P goes over the columns of the upper half of S, so that the lower
-          // half stays readable
+          if (spread) {
+            uint32_t pk[16];
+            exp_keys(sv, sc2, mm2, pk, l2);
+            // this copy's weights of the other warps' keys are zero
+            uint32_t zero[16];
 #pragma unroll
-          for (int hf = 1; hf >= 0; --hf) {
-            if (hf == 0) load_half(tS, 0, lim, whole, sv);
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              uint32_t pk[16];
-#pragma unroll
-              for (int y = 0; y < 32; y += 2) {
-                const float2 e = f2_unpack(ffma2(f2_pack(sv[c * 32 + y], sv[c * 32 + y + 1]), sc2, mm2));
-                const float e0 = fast_exp2(e.x), e1 = fast_exp2(e.y);
-                pk[y >> 1] = pack2(e0, e1);
-                l2[(y >> 1) & 3] = fadd2(l2[(y >> 1) & 3], f2_pack(e0, e1));
-              }
-              tmem_st16(tS + 64 + hf * 32 + c * 16, pk);
-            }
+            for (int y = 0; y < 16; ++y) zero[y] = 0u;
+#pragma unroll 1
+            for (int c = 1; c < 4; ++c) tmem_st16(tS + 64 + ((quarter + c) & 3) * 16, zero);
+            tmem_st16(tS + 64 + quarter * 16, pk);
             tc_wait_st();
             tc_fence_before();
-            mbar_arrive(&m.pfull[2 * wg + hf]);
+            mbar_arrive(&m.pfull[2 * wg + 1]);
+            mbar_arrive(&m.pfull[2 * wg]);
+          } else {
+            // P goes over the columns of the upper half of S, so that the lower
+            // half stays readable
+#pragma unroll 1
+            for (int hf = 1; hf >= 0; --hf) {
+              if (hf == 0) {
+                tmem_ld32(tS, sv);
+                tmem_ld32(tS + 32, sv + 32);
+                tc_wait_ld();
+                mask_keys(sv, lim, false);
+              }
+              uint32_t pk[16];
+              exp_keys(sv, sc2, mm2, pk, l2);
+              tmem_st16(tS + 64 + hf * 32, pk);
+              exp_keys(sv + 32, sc2, mm2, pk, l2);
+              tmem_st16(tS + 64 + hf * 32 + 16, pk);
+              tc_wait_st();
+              tc_fence_before();
+              mbar_arrive(&m.pfull[2 * wg + hf]);
+            }
           }
           const float2 la = f2_unpack(fadd2(fadd2(l2[0], l2[1]), fadd2(l2[2], l2[3])));
           l += la.x + la.y;
@@ -815,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       pend = true;
       pend_busy = busy;
       pend_valid = valid;
-      pend_o = (q.own ? p.o_s : p.o_p) + prow * D;
+      pend_o = (own ? p.o_s : p.o_p) + prow * D;
       ++jobs;
     }
     if (ok) write_out();
@@ -827,64 +865,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-}
-
-// Where one row's partials of a segment lie: of CTAs c0 .. c1, at index
-// (id + c) * 2 + warpgroup.
-struct Parts {
-  long long start;
-  int c0, n, nb, w, id, row, rows;
-  bool own, pair;
-  int wg;       // of a pair: the warpgroup of the row's tile
-  int sub;      // partials of a warpgroup: 4 of a spread tile, else 1
-};
-
-__device__ __forceinline__ Parts parts_of(const PrefixParams& p, long long total, bool own, int b,
-                                          int t, int h) {
-  Parts s;
-  const int g = h / p.r, hr = h - g * p.r;
-  s.own = own;
-  s.pair = false;
-  s.sub = (own ? p.spread_s : p.spread_p) ? 4 : 1;
-  s.wg = 0;
-  s.w = kCostSingle;
-  if (own) {
-    s.id = p.nsp + b * p.G + g;
-    s.nb = blocks_of(own_len(p, b));
-    s.start = p.cost_prefix + p.starts[b] * p.G + static_cast<long long>(g) * own_cost(s.nb);
-    s.row = t * p.r + hr;
-    s.rows = p.rows_s;
-  } else {
-    const int at = (b * p.T + t) * p.r + hr, tile = at >> 7, pt = tile >> 1;
-    s.id = g * p.npt + pt;
-    s.pair = 2 * pt + 1 < p.ntile;
-    s.wg = tile & 1;
-    s.nb = p.nbp;
-    if (s.pair) s.w = kCostPair;
-    s.start = g * p.cost_group + pt * p.cost_pair;
-    s.row = at & 127;
-    s.rows = p.rows_p;
-  }
-  s.n = 0;
-  s.c0 = 0;
-  if (s.nb > 0) {
-    s.c0 = cta_of(s.start, total, p.grid);
-    s.n = 2 * s.sub * (cta_of(s.start + static_cast<long long>(s.nb - 1) * s.w, total, p.grid) - s.c0 + 1);
-  }
-  return s;
-}
-
-// Partial k of the list (two warpgroups a CTA): its index, or -1 when that CTA had no
-// block of the segment, or of a pair when it is the other tile's.
-__device__ __forceinline__ long long part_at(const PrefixParams& p, const Parts& s, long long total,
-                                             int k) {
-  const int sub = k & (s.sub - 1), k2 = s.sub == 4 ? k >> 2 : k;
-  const int c = s.c0 + (k2 >> 1), wg = k2 & 1;
-  const int n = blocks_before(cta_begin(c + 1, total, p.grid), s.start, s.w, s.nb) -
-                blocks_before(cta_begin(c, total, p.grid), s.start, s.w, s.nb);
-  if (n <= 0 || (s.pair && wg != s.wg)) return -1;
-  const long long part = 2ll * ((s.own ? s.id - p.nsp : s.id) + c) + wg;
-  return (part * s.sub + sub) * s.rows + s.row;
 }
 
 constexpr int kMergeWarps = 8;
@@ -899,9 +879,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const Pr
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long row = static_cast<long long>(blockIdx.x) * kMergeWarps + warp;
   if (row >= static_cast<long long>(p.B) * p.T * p.H) return;
-  const int h = static_cast<int>(row % p.H);
-  const int t = static_cast<int>(row / p.H % p.T), b = static_cast<int>(row / p.H / p.T);
-  const long long total = p.cost_prefix + p.starts[p.B] * p.G;
+  const int H = p.H, tok = static_cast<int>(row / H), h = static_cast<int>(row - static_cast<long long>(tok) * H);
+  const int b = tok / p.T, t = tok - b * p.T, g = h / p.r, hr = h - g * p.r;
   float M = -INFINITY, den = 0.f;
   bool poison = false;
   constexpr int V = D / 32;
@@ -910,11 +889,37 @@ __global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const Pr
   for (int y = 0; y < V; ++y) acc[y] = 0.f;
 #pragma unroll 1
   for (int own = 0; own < 2; ++own) {
-    const Parts s = parts_of(p, total, own != 0, b, t, h);
+    // The segment's partials: of the CTAs of its span, of both warpgroups (of a
+    // pair: the row's tile's), of the four quarters of a spread tile.
+    int id, at_row, rows, wgs = 2, wg0 = 0;
+    bool spread;
+    if (own) {
+      if (own_len(p, b) == 0) continue;
+      id = b * p.G + g;
+      at_row = t * p.r + hr;
+      rows = p.rows_s;
+      spread = p.spread_s;
+    } else {
+      if (p.nsp == 0) continue;
+      const int at = tok * p.r + hr, tile = at >> 7;
+      id = g * p.npt + (tile >> 1);
+      at_row = at & 127;
+      rows = p.rows_p;
+      spread = p.spread_p;
+      if ((tile | 1) < p.ntile) {
+        wgs = 1;
+        wg0 = tile & 1;
+      }
+    }
+    const int2 span = __ldcg(p.span + (own ? p.nsp + id : id));
+    const int per = wgs * (spread ? 4 : 1), n = (span.y - span.x + 1) * per;
     const float2* ml = own ? p.ml_s : p.ml_p;
     const float* po = own ? p.o_s : p.o_p;
-    for (int k0 = 0; k0 < s.n; k0 += 32) {
-      const long long at = k0 + lane < s.n ? part_at(p, s, total, k0 + lane) : -1;
+    for (int k0 = 0; k0 < n; k0 += 32) {
+      const int k = k0 + lane, c = k / per, in = k - c * per;
+      const long long part = 2ll * (id + span.x + c) + wg0 + (spread ? in >> 2 : in);
+      const long long at =
+          k < n ? (spread ? (part * 4 + (in & 3)) * rows : part * rows) + at_row : -1;
       const float2 v = at >= 0 ? __ldcg(ml + at) : make_float2(-INFINITY, 0.f);
       // fmaxf drops a NaN: a row with a NaN or +inf logit is NaN throughout
       poison |= __any_sync(0xffffffffu, v.x != v.x || v.y != v.y);
@@ -1014,7 +1019,7 @@ constexpr size_t kSpreadPrefix = 32, kSpreadOwn = 16;
 
 // Workspace layout.
 struct PrefixWs {
-  size_t starts, lse2, ml_p, o_p, ml_s, o_s, logits, bytes;
+  size_t span, lse2, ml_p, o_p, ml_s, o_s, logits, bytes;
 };
 
 PrefixWs ws_layout(const msa_shape& s, bool weights) {
@@ -1032,7 +1037,7 @@ PrefixWs ws_layout(const msa_shape& s, bool weights) {
     at += align_up(n, 256);
     return x;
   };
-  w.starts = take((static_cast<size_t>(s.batch) + 1) * sizeof(long long));
+  w.span = take((nsp + bg) * sizeof(int2));
   w.lse2 = take(rows * s.n_kv_heads * sizeof(float));
   w.ml_p = take(pr * sizeof(float2));
   w.o_p = take(pr * d * sizeof(float));
@@ -1044,7 +1049,7 @@ PrefixWs ws_layout(const msa_shape& s, bool weights) {
 }
 
 template <int D>
-cudaError_t launch(const msa_shape& s, const PrefixDecodeArgs& a, const PrefixParams& p,
+cudaError_t launch(const msa_shape& s, const PrefixDecodeArgs& a, const PrefixParams& p, int grid,
                    cudaStream_t st) {
   PrefixMaps tm;
   const uint64_t D8 = D;
@@ -1084,7 +1089,7 @@ cudaError_t launch(const msa_shape& s, const PrefixDecodeArgs& a, const PrefixPa
   if (e != cudaSuccess) return e;
   {
     ProfScope ps_("prefix_attn", st);
-    e = launch_dependent(prefix_attn_kernel<D>, dim3(static_cast<unsigned>(p.grid)), dim3(kThreads),
+    e = launch_dependent(prefix_attn_kernel<D>, dim3(static_cast<unsigned>(grid)), dim3(kThreads),
                          smem, st, tm, p);
   }
   if (e != cudaSuccess) return e;
@@ -1127,7 +1132,7 @@ cudaError_t launch_prefix_decode(const msa_shape& s, const PrefixDecodeArgs& a, 
   p.table = a.pages.table;
   p.num_pages = a.pages.num_pages;
   p.err = ctx->err;
-  p.starts = reinterpret_cast<long long*>(base + w.starts);
+  p.span = reinterpret_cast<int2*>(base + w.span);
   p.lse2 = reinterpret_cast<float*>(base + w.lse2);
   p.ml_p = reinterpret_cast<float2*>(base + w.ml_p);
   p.o_p = reinterpret_cast<float*>(base + w.o_p);
@@ -1161,8 +1166,9 @@ cudaError_t launch_prefix_decode(const msa_shape& s, const PrefixDecodeArgs& a, 
   p.scale_log2 = kLog2e / sqrtf(static_cast<float>(s.head_dim));
   // no more CTAs than blocks there can be
   const int64_t most = static_cast<int64_t>(p.nsp) * p.nbp + static_cast<int64_t>(p.B) * p.G * p.nb;
-  p.grid = static_cast<int>(std::min<int64_t>(most, std::min(std::max(ctx->num_sms, 1), kMaxGrid)));
-  return s.head_dim == 128 ? launch<128>(s, a, p, st) : launch<64>(s, a, p, st);
+  const int grid =
+      static_cast<int>(std::min<int64_t>(most, std::min(std::max(ctx->num_sms, 1), kMaxGrid)));
+  return s.head_dim == 128 ? launch<128>(s, a, p, grid, st) : launch<64>(s, a, p, grid, st);
 }
 
 cudaError_t set_wait_limit_prefix(uint64_t ns) { return set_wait_limit_here(ns); }
