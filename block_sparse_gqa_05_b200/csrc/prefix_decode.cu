@@ -17,9 +17,9 @@
 // walk made the code too large for the instruction cache).  Every (CTA, segment, warpgroup) leaves
 // an unnormalised partial output with its running maximum and sum in fp32; a
 // second kernel merges them.  With scores wanted, the logits of own keys go to
-// the workspace (4 T r bytes per key against 4 d for its K and V) and a third
-// kernel turns them into weights once the normalisers are known, which is
-// cheaper than reading K again.
+// the workspace (4 T r bytes per key against 4 d for its K and V) and other
+// CTAs of that kernel turn them into weights, which is cheaper than reading K
+// again.
 //
 // In the CTA: warp 0 streams K and V through a ring of tiles by TMA; warps 1
 // and 2 load the queries and issue the MMAs of the two warpgroups' tiles (S = Q
@@ -42,7 +42,9 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kMaxGrid = 256;      // bound of the persistent grid, for the workspace size
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kRescaleLog2 = 8.f;
+// A row's reference follows its maximum when that is 2^8 above it, and at once
+// within a block when it is 2^64 above.
+constexpr float kRescaleLog2 = 8.f, kJumpLog2 = 64.f;
 
 // Cost of a block on the line, by the kind of its segment, and of a segment.
 constexpr int kCostPair = 5, kCostSingle = 4, kCostSegment = 2;
@@ -55,7 +57,6 @@ struct PrefixParams {
   const int32_t *lens, *prefix_pages, *table;
   uint32_t* err;
   int2* span;          // [nsp + B*G] first and last CTA with blocks of a segment
-  float* lse2;         // [B*T*H] normalisers, log2
   float2* ml_p;        // [(nsp + grid) * 2, rows_p]  (maximum, sum) of prefix partials
   float* o_p;          // [(nsp + grid) * 2, rows_p, D]
   float2* ml_s;        // [(B*G + grid) * 2, T*r]     of own-cache partials
@@ -207,7 +208,7 @@ struct Bars {
   uint64_t *dfull, *dempty; // [kSegRing] descriptor written / read by all
   uint64_t* qfull;          // [2][2] per warpgroup: queries loaded, alternating
   uint64_t* sfull;          // [2] S complete
-  uint64_t* pfull;          // [2][2] per warpgroup and half of the keys: P written
+  uint64_t* pfull;          // [2] P written
   uint64_t *olast, *ofree;  // [2] a segment's O complete / read
   uint64_t* turn;           // [2] of a pair: the warpgroup's turn at the tensor cores
   uint64_t* drain;          // [2] the MMA warps' last commits
@@ -283,11 +284,52 @@ __device__ __forceinline__ void store8(float* dst, const float* v) {
                : "memory");
 }
 
-// Logits of keys past lim to -inf (of the first 32 only when half).
-__device__ __forceinline__ void mask_keys(float* sv, int lim, bool half) {
-  if (__all_sync(0xffffffffu, lim >= (half ? 31 : 63))) return;
+// Logits of keys past lim to -inf.
+template <int N>
+__device__ __forceinline__ void mask_keys(float* sv, int lim) {
+  if (__all_sync(0xffffffffu, lim >= N - 1)) return;
 #pragma unroll
-  for (int y = 0; y < 64; ++y) sv[y] = y <= lim ? sv[y] : -INFINITY;
+  for (int y = 0; y < N; ++y) sv[y] = y <= lim ? sv[y] : -INFINITY;
+}
+
+template <int N>
+__device__ __forceinline__ float max_keys(const float* sv) {
+  float m4[4] = {sv[0], sv[1], sv[2], sv[3]};
+#pragma unroll
+  for (int y = 4; y < N; y += 2) m4[(y >> 1) & 3] = fmax3(m4[(y >> 1) & 3], sv[y], sv[y + 1]);
+  return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+}
+
+// N logits in units of log2 to the workspace.
+template <int N>
+__device__ __forceinline__ void store_logits(float* dst, const float* sv, float scale_log2) {
+#pragma unroll
+  for (int y = 0; y < N; y += 8) {
+    float t8[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t8[e] = sv[y + e] * scale_log2;
+    store8(dst + y, t8);
+  }
+}
+
+// Scales 64 weights of this row (32 columns of bf16 pairs) by a.
+__device__ __forceinline__ void scale_p(uint32_t taddr, float a) {
+#pragma unroll 1
+  for (int c = 0; c < 32; c += 4) {
+    uint32_t r[4];
+    asm volatile("tcgen05.wait::st.sync.aligned;\n\t"
+                 "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];\n\t"
+                 "tcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(taddr + c)
+                 : "memory");
+#pragma unroll
+    for (int y = 0; y < 4; ++y)
+      r[y] = pack2(__uint_as_float(r[y] << 16) * a, __uint_as_float(r[y] & 0xFFFF0000u) * a);
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr + c),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
+  }
 }
 
 // 32 weights 2^(s scale - m) as bf16 pairs, and their sums in fp32.
@@ -396,11 +438,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   m.qfull = m.dempty + kSegRing;
   m.sfull = m.qfull + 4;
   m.pfull = m.qfull + 6;
-  m.olast = m.qfull + 10;
-  m.ofree = m.qfull + 12;
-  m.turn = m.qfull + 14;
-  m.drain = m.qfull + 16;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(m.qfull + 18);
+  m.olast = m.qfull + 8;
+  m.ofree = m.qfull + 10;
+  m.turn = m.qfull + 12;
+  m.drain = m.qfull + 14;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(m.qfull + 16);
   uint32_t* issued = tmem_slot + 1;                  // K and V tiles whose loads were issued
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 2);
   Seg* segs = reinterpret_cast<Seg*>(smem + L::kOffSeg);
@@ -419,8 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&m.qfull[2 * i], 1);
       mbar_init(&m.qfull[2 * i + 1], 1);
       mbar_init(&m.sfull[i], 1);
-      mbar_init(&m.pfull[2 * i], 128);
-      mbar_init(&m.pfull[2 * i + 1], 128);
+      mbar_init(&m.pfull[i], 128);
       mbar_init(&m.olast[i], 1);
       mbar_init(&m.ofree[i], 128);
       mbar_init(&m.turn[i], 1);
@@ -575,32 +616,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                       abort_flag, p.err))))
             break;
           if (early) load_next(k);
-          const uint32_t qa = smem_u32(qbuf) + (early ? (jobs & 1) * p.q_stage : 0);
+          const uint64_t qd = smem_desc(smem_u32(qbuf) + (early ? (jobs & 1) * p.q_stage : 0), 16, 1024, 2);
           const bool rag = q.ragged(), pair = q.pair();
+          // S = Q K^T of block x, over the P that the product before has read
+          auto wait_k = [&](int x) {
+            return __all_sync(0xffffffffu, wait_tile<R>(m, issued, 2 * (q.n0 + x), abort_flag, p.err)) != 0;
+          };
+          auto issue_s = [&](int x) {
+            const int st = 2 * (q.n0 + x) % R;
+            const uint64_t kd = smem_desc(ring + st * L::kTile, 16, 1024, 2);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+              const uint32_t off = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
+              tc_mma_ss(tS, qd + off, kd + off, kIdescS, ks > 0 ? 1u : 0u);
+            }
+            tc_commit(&m.sfull[wg]);
+            tc_commit(&m.empty[st]);
+          };
+          if (!(ok = wait_k(first))) break;
+          tc_fence_after();
+          if (lane == 0) issue_s(first);
+          __syncwarp();
           for (int x = first; x < q.n; x += step, ++i) {
             const bool last = x + step >= q.n;
-            // S = Q K^T, over the P that the product before this one has read
-            {
-              const int item = 2 * (q.n0 + x), st = item % R;
-              if (!(ok = __all_sync(0xffffffffu, wait_tile<R>(m, issued, item, abort_flag, p.err))))
-                break;
-              tc_fence_after();
-              const uint32_t ka_ = ring + st * L::kTile;
-              if (lane == 0) {
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                  const uint32_t off = (ks >> 2) * 16384 + (ks & 3) * 32;
-                  tc_mma_ss(tS, smem_desc(qa + off, 16, 1024, 2), smem_desc(ka_ + off, 16, 1024, 2),
-                            kIdescS, ks > 0 ? 1u : 0u);
-                }
-                tc_commit(&m.sfull[wg]);
-                tc_commit(&m.empty[st]);
-                if (pair && x > first) mbar_arrive(&m.turn[1 - wg]);
-              }
-              __syncwarp();
-            }
-            // O += P V, the upper half of the keys first; past a length only
-            // the 16-key steps that hold valid rows
+            // O += P V; past a length only the 16-key steps that hold valid rows
             if (x == first && jobs > 0 &&
                 !(ok = __all_sync(0xffffffffu,
                                   wait_bar(&m.ofree[wg], (jobs - 1) & 1, abort_flag, p.err))))
@@ -621,42 +660,37 @@ __global__ void __launch_bounds__(kThreads, 1)
               fence_proxy_async_smem();
               __syncwarp();
             }
+            if (!(ok = __all_sync(0xffffffffu, wait_bar(&m.pfull[wg], i & 1, abort_flag, p.err))))
+              break;
             // Of a pair the two warpgroups take turns at the tensor cores, O +=
-            // P V and the next S together, so that one is in its softmax while
-            // the other's products run
+            // P V and the next S together and with nothing left to wait for, so
+            // that one is in its softmax while the other's products run
             if (pair) {
+              if (!last && !(ok = wait_k(x + step))) break;
               if ((wg == 1 || pairs > 0) &&
                   !(ok = __all_sync(0xffffffffu, wait_bar(&m.turn[wg], (pairs - 1 + wg) & 1,
                                                           abort_flag, p.err))))
                 break;
               ++pairs;
             }
-            const uint32_t va = smem_u32(v);
-            uint32_t acc = x > first ? 1u : 0u;
-#pragma unroll 1
-            for (int hf = 1; hf >= 0; --hf) {
-              if (!(ok = __all_sync(0xffffffffu, wait_bar(&m.pfull[2 * wg + hf], i & 1, abort_flag,
-                                                          p.err))))
-                break;
-              tc_fence_after();
-              const int todo = min(4, steps - 4 * hf);
-              if (lane == 0) {
-#pragma unroll
-                for (int ks = 0; ks < 4; ++ks)
-                  if (ks < todo)
-                    tc_mma_ts(tO, tS + 64 + (4 * hf + ks) * 8,
-                              smem_desc(va + (4 * hf + ks) * 16 * 128, 16384, 1024, 2), kIdescO,
-                              ks > 0 ? 1u : acc);
-              }
-              __syncwarp();
-              if (todo > 0) acc = 1u;
-            }
-            if (!ok) break;
+            tc_fence_after();
+            const uint64_t vd = smem_desc(smem_u32(v), 16384, 1024, 2);
             if (lane == 0) {
+#pragma unroll
+              for (int ks = 0; ks < 8; ++ks)
+                if (ks < steps)
+                  tc_mma_ts(tO, tS + 64 + ks * 8, vd + ks * 128, kIdescO,
+                            x > first || ks > 0 ? 1u : 0u);
               tc_commit(&m.empty[st]);
               if (last) tc_commit(&m.olast[wg]);
-              if (last && pair) mbar_arrive(&m.turn[1 - wg]);
             }
+            __syncwarp();
+            if (!last) {
+              if (!pair && !(ok = wait_k(x + step))) break;
+              tc_fence_after();
+              if (lane == 0) issue_s(x + step);
+            }
+            if (pair && lane == 0) mbar_arrive(&m.turn[1 - wg]);
             __syncwarp();
           }
           ++jobs;
@@ -737,76 +771,50 @@ __global__ void __launch_bounds__(kThreads, 1)
       float* logit = nullptr;
       if (own && p.logits && valid)
         logit = p.logits + (static_cast<long long>(q.b * p.G + q.g) * p.rows_s + row) * p.nb * 128;
-      float mref = -INFINITY, l = 0.f;
+      float mref = -INFINITY, mtop = -INFINITY, l = 0.f;   // reference, maximum seen, sum
       for (int x = first; x < q.n; x += step, ++i) {
         if (!(ok = __all_sync(0xffffffffu, wait_bar(&m.sfull[wg], i & 1, abort_flag, p.err)))) break;
         const int j = q.j0 + x;
         const int lim = last_key - j * 128;        // keys past lim are not seen
         if (busy) {
           tc_fence_after();
-          // Maximum of the keys this thread sees.  Of a full tile, half of the
-          // row's 128 logits is in registers at a time: keys 0..63 for the
-          // maximum alone, then 64..127 for both, then 0..63 again (TMEM is
-          // read at 4 times the rate at which the rest goes).  A warp of a
-          // spread tile holds its 32 keys in the lower half of sv.
-          float sv[64];
-          float mraw = -INFINITY;
-          const int k0 = spread ? quarter * 32 : 0, parts = spread ? 1 : 2;
+          // O of the rows whose maximum is above the reference by more than
+          // 2^slack gets a new one; S of a block is issued after the product of
+          // the block before, so that one is complete.  P and the sums hold
+          // any power of two up to 2^100 with the same relative precision.
+          auto new_reference = [&](float slack) {
+            const bool grow = valid && mtop > mref + slack;
+            if (!__any_sync(0xffffffffu, grow)) return 1.f;
+            const float a = grow ? fast_exp2(mref - mtop) : 1.f;
+            if (x > first) {
 #pragma unroll 1
-          for (int hf = 0; hf < parts; ++hf) {
-            const int at = k0 + hf * 64;
-            tmem_ld32(tS + at, sv);
-            if (!spread) tmem_ld32(tS + at + 32, sv + 32);
-            tc_wait_ld();
-            mask_keys(sv, lim - at, spread);
-            if (logit) {
-              float* dst = logit + j * 128 + at;
+              for (int c = 0; c < D / 32; ++c) {
+                float ov[32];
+                tmem_ld32(tO + c * 32, ov);
+                tc_wait_ld();
 #pragma unroll
-              for (int y = 0; y < 64; y += 8) {
-                if (y >= 32 && spread) break;
-                float t8[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) t8[e] = sv[y + e] * p.scale_log2;
-                store8(dst + y, t8);
+                for (int y = 0; y < 32; ++y) ov[y] *= a;
+                tmem_st32(tO + c * 32, ov);
               }
-            }
-            float m4[4] = {mraw, sv[0], sv[1], sv[2]};
-#pragma unroll
-            for (int y = 3; y + 1 < 32; y += 2)
-              m4[(y >> 1) & 3] = fmax3(m4[(y >> 1) & 3], sv[y], sv[y + 1]);
-            m4[0] = fmaxf(m4[0], sv[31]);
-            if (!spread) {
-#pragma unroll
-              for (int y = 32; y < 64; y += 2)
-                m4[(y >> 1) & 3] = fmax3(m4[(y >> 1) & 3], sv[y], sv[y + 1]);
-            }
-            mraw = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
-          }
-          const float mblk = mraw * p.scale_log2;
-          // O of the rows whose maximum outgrew its reference is rescaled; S of a
-          // block is issued after the product of the block before, so that one is
-          // complete
-          const bool grow = valid && mblk > mref + kRescaleLog2;
-          if (__any_sync(0xffffffffu, grow && x > first)) {
-            const float a = grow ? fast_exp2(mref - mblk) : 1.f;
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              float ov[32];
-              tmem_ld32(tO + c * 32, ov);
-              tc_wait_ld();
-#pragma unroll
-              for (int y = 0; y < 32; ++y) ov[y] *= a;
-              tmem_st32(tO + c * 32, ov);
+              tc_wait_st();
             }
             l *= a;
-          }
-          if (grow) mref = mblk;
-          const float mu = mref == -INFINITY ? 0.f : mref;   // a row that has seen no key yet
-          const uint64_t mm2 = f2_pack(-mu, -mu);
+            if (grow) mref = mtop;
+            return a;
+          };
+          float sv[64];
           uint64_t l2[4] = {0, 0, 0, 0};
+          uint32_t pk[16];
           if (spread) {
-            uint32_t pk[16];
-            exp_keys(sv, sc2, mm2, pk, l2);
+            const int k0 = quarter * 32;
+            tmem_ld32(tS + k0, sv);
+            tc_wait_ld();
+            mask_keys<32>(sv, lim - k0);
+            if (logit) store_logits<32>(logit + j * 128 + k0, sv, p.scale_log2);
+            mtop = fmaxf(mtop, max_keys<32>(sv) * p.scale_log2);
+            new_reference(kRescaleLog2);
+            const float mu = mref == -INFINITY ? 0.f : mref;   // a row that has seen no key yet
+            exp_keys(sv, sc2, f2_pack(-mu, -mu), pk, l2);
             // this copy's weights of the other warps' keys are zero
             uint32_t zero[16];
 #pragma unroll
@@ -814,37 +822,52 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int c = 1; c < 4; ++c) tmem_st16(tS + 64 + ((quarter + c) & 3) * 16, zero);
             tmem_st16(tS + 64 + quarter * 16, pk);
-            tc_wait_st();
-            tc_fence_before();
-            mbar_arrive(&m.pfull[2 * wg + 1]);
-            mbar_arrive(&m.pfull[2 * wg]);
           } else {
-            // P goes over the columns of the upper half of S, so that the lower
-            // half stays readable
+            // The reference is the maximum of the blocks before, so that the
+            // exponentials need not wait for this block's: it is looked at
+            // half by half (64 logits in registers) and only a jump of 2^64
+            // makes a new one at once.  Rows without a reference look ahead.
+            if (__any_sync(0xffffffffu, valid && mref == -INFINITY)) {
+#pragma unroll 1
+              for (int hf = 0; hf < 2; ++hf) {
+                tmem_ld32(tS + hf * 64, sv);
+                tmem_ld32(tS + hf * 64 + 32, sv + 32);
+                tc_wait_ld();
+                mask_keys<64>(sv, lim - hf * 64);
+                mtop = fmaxf(mtop, max_keys<64>(sv) * p.scale_log2);
+              }
+            }
+            new_reference(kRescaleLog2);
+            // P goes over the columns of the upper half of S, which is read
+            // first, so that the lower half stays readable
 #pragma unroll 1
             for (int hf = 1; hf >= 0; --hf) {
-              if (hf == 0) {
-                tmem_ld32(tS, sv);
-                tmem_ld32(tS + 32, sv + 32);
-                tc_wait_ld();
-                mask_keys(sv, lim, false);
+              tmem_ld32(tS + hf * 64, sv);
+              tmem_ld32(tS + hf * 64 + 32, sv + 32);
+              tc_wait_ld();
+              mask_keys<64>(sv, lim - hf * 64);
+              if (logit) store_logits<64>(logit + j * 128 + hf * 64, sv, p.scale_log2);
+              mtop = fmaxf(mtop, max_keys<64>(sv) * p.scale_log2);
+              if (__any_sync(0xffffffffu, valid && mtop > mref + kJumpLog2)) {
+                const float a = new_reference(kJumpLog2);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) l2[y] = fmul2(l2[y], f2_pack(a, a));
+                if (hf == 0) scale_p(tS + 96, a);      // the upper half's weights
               }
-              uint32_t pk[16];
+              const float mu = mref == -INFINITY ? 0.f : mref;
+              const uint64_t mm2 = f2_pack(-mu, -mu);
               exp_keys(sv, sc2, mm2, pk, l2);
               tmem_st16(tS + 64 + hf * 32, pk);
               exp_keys(sv + 32, sc2, mm2, pk, l2);
               tmem_st16(tS + 64 + hf * 32 + 16, pk);
-              tc_wait_st();
-              tc_fence_before();
-              mbar_arrive(&m.pfull[2 * wg + hf]);
             }
           }
           const float2 la = f2_unpack(fadd2(fadd2(l2[0], l2[1]), fadd2(l2[2], l2[3])));
           l += la.x + la.y;
-        } else {
-          mbar_arrive(&m.pfull[2 * wg + 1]);
-          mbar_arrive(&m.pfull[2 * wg]);
+          tc_wait_st();
+          tc_fence_before();
         }
+        mbar_arrive(&m.pfull[wg]);
         if (x == first && !(ok = write_out())) break;
       }
       if (!ok) break;
@@ -868,149 +891,201 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 constexpr int kMergeWarps = 8;
+constexpr int kScoreKeys = 4 * kMergeWarps * 32;   // keys of a CTA: four a thread
 
-// One warp per row (b, t, h): merges its partials.  With m and l the running
-// maximum and sum of a partial and O its unnormalised output,
-// o = sum 2^(m - M) O / sum 2^(m - M) l, lse = M + log2 of the denominator.
-template <int D>
-__global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const PrefixParams p) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long row = static_cast<long long>(blockIdx.x) * kMergeWarps + warp;
-  if (row >= static_cast<long long>(p.B) * p.T * p.H) return;
-  const int H = p.H, tok = static_cast<int>(row / H), h = static_cast<int>(row - static_cast<long long>(tok) * H);
+// The partials of one row (token tok, head h): of the prefix segment of its
+// tile and of its own segment, of the CTAs of their spans, of both warpgroups
+// (of a pair: the tile's), of the four quarters of a spread tile.
+struct RowParts {
+  int n[2];              // partials of the prefix and of the own segment
+  int per[2], wg0[2], wgs[2];
+  long long first[2];    // index of CTA span.x's first partial
+  int rows[2], at[2];    // rows of a partial, and this row's place
+};
+
+__device__ __forceinline__ RowParts row_parts(const PrefixParams& p, int tok, int h) {
+  RowParts s;
   const int b = tok / p.T, t = tok - b * p.T, g = h / p.r, hr = h - g * p.r;
-  float M = -INFINITY, den = 0.f;
-  bool poison = false;
-  constexpr int V = D / 32;
-  float acc[V];
-#pragma unroll
-  for (int y = 0; y < V; ++y) acc[y] = 0.f;
-#pragma unroll 1
-  for (int own = 0; own < 2; ++own) {
-    // The segment's partials: of the CTAs of its span, of both warpgroups (of a
-    // pair: the row's tile's), of the four quarters of a spread tile.
-    int id, at_row, rows, wgs = 2, wg0 = 0;
-    bool spread;
-    if (own) {
-      if (own_len(p, b) == 0) continue;
-      id = b * p.G + g;
-      at_row = t * p.r + hr;
-      rows = p.rows_s;
-      spread = p.spread_s;
-    } else {
-      if (p.nsp == 0) continue;
-      const int at = tok * p.r + hr, tile = at >> 7;
-      id = g * p.npt + (tile >> 1);
-      at_row = at & 127;
-      rows = p.rows_p;
-      spread = p.spread_p;
-      if ((tile | 1) < p.ntile) {
-        wgs = 1;
-        wg0 = tile & 1;
-      }
-    }
-    const int2 span = __ldcg(p.span + (own ? p.nsp + id : id));
-    const int per = wgs * (spread ? 4 : 1), n = (span.y - span.x + 1) * per;
-    const float2* ml = own ? p.ml_s : p.ml_p;
-    const float* po = own ? p.o_s : p.o_p;
-    for (int k0 = 0; k0 < n; k0 += 32) {
-      const int k = k0 + lane, c = k / per, in = k - c * per;
-      const long long part = 2ll * (id + span.x + c) + wg0 + (spread ? in >> 2 : in);
-      const long long at =
-          k < n ? (spread ? (part * 4 + (in & 3)) * rows : part * rows) + at_row : -1;
-      const float2 v = at >= 0 ? __ldcg(ml + at) : make_float2(-INFINITY, 0.f);
-      // fmaxf drops a NaN: a row with a NaN or +inf logit is NaN throughout
-      poison |= __any_sync(0xffffffffu, v.x != v.x || v.y != v.y);
-      float mx = v.x;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      const float Mn = fmaxf(M, mx);
-      if (Mn == -INFINITY) continue;
-      const float keep = fast_exp2(M - Mn), wgt = at >= 0 ? fast_exp2(v.x - Mn) : 0.f;
-      float ls = wgt * v.y;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
-      den = den * keep + ls;
-#pragma unroll
-      for (int y = 0; y < V; ++y) acc[y] *= keep;
-      M = Mn;
-      unsigned todo = __ballot_sync(0xffffffffu, wgt > 0.f);
-      while (todo) {
-        // up to four partial rows in flight
-        float x[4][V], wk[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int src = todo ? __ffs(todo) - 1 : 0;
-          wk[u] = todo ? __shfl_sync(0xffffffffu, wgt, src) : 0.f;
-          const long long a = __shfl_sync(0xffffffffu, at, src);
-          if (todo) {
-            const float* f = po + a * D + lane * V;
-            if constexpr (V == 4) {
-              const float4 q4 = __ldcg(reinterpret_cast<const float4*>(f));
-              x[u][0] = q4.x;
-              x[u][1] = q4.y;
-              x[u][2] = q4.z;
-              x[u][3] = q4.w;
-            } else {
-              const float2 q2 = __ldcg(reinterpret_cast<const float2*>(f));
-              x[u][0] = q2.x;
-              x[u][1] = q2.y;
-            }
-          } else {
-#pragma unroll
-            for (int y = 0; y < V; ++y) x[u][y] = 0.f;
-          }
-          todo &= todo - 1;
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-          for (int y = 0; y < V; ++y) acc[y] = fmaf(wk[u], x[u][y], acc[y]);
-      }
-    }
+  s.n[0] = s.n[1] = 0;
+  if (p.nsp > 0) {
+    const int at = tok * p.r + hr, tile = at >> 7, id = g * p.npt + (tile >> 1);
+    const bool pair = (tile | 1) < p.ntile;
+    const int2 span = __ldcg(p.span + id);
+    s.wgs[0] = pair ? 1 : 2;
+    s.wg0[0] = pair ? tile & 1 : 0;
+    s.per[0] = s.wgs[0] * (p.spread_p ? 4 : 1);
+    s.n[0] = (span.y - span.x + 1) * s.per[0];
+    s.first[0] = 2ll * (id + span.x);
+    s.rows[0] = p.rows_p;
+    s.at[0] = at & 127;
   }
-  if (poison) M = den = __int_as_float(0x7fffffff);
-  const float inv = M == -INFINITY ? 0.f : 1.f / den;
-  uint16_t* out = p.o + row * D + lane * V;
-  if constexpr (V == 4)
-    *reinterpret_cast<uint2*>(out) =
-        make_uint2(pack2(acc[0] * inv, acc[1] * inv), pack2(acc[2] * inv, acc[3] * inv));
-  else
-    *reinterpret_cast<uint32_t*>(out) = pack2(acc[0] * inv, acc[1] * inv);
-  if (lane == 0) {
-    const float lse2 = M == -INFINITY ? -INFINITY : M + log2f(den);
-    p.lse2[row] = lse2;
-    if (p.lse) p.lse[row] = lse2 / kLog2e;
+  if (own_len(p, b) > 0) {
+    const int id = b * p.G + g;
+    const int2 span = __ldcg(p.span + p.nsp + id);
+    s.wgs[1] = 2;
+    s.wg0[1] = 0;
+    s.per[1] = p.spread_s ? 8 : 2;
+    s.n[1] = (span.y - span.x + 1) * s.per[1];
+    s.first[1] = 2ll * (id + span.x);
+    s.rows[1] = p.rows_s;
+    s.at[1] = t * p.r + hr;
   }
+  return s;
 }
 
-constexpr int kScoreThreads = 256;
+// Index of the row in partial k of segment kind own.
+__device__ __forceinline__ long long part_row(const PrefixParams& p, const RowParts& s, int own, int k) {
+  const bool spread = own ? p.spread_s : p.spread_p;
+  const int c = s.wgs[own] == 2 ? k >> (spread ? 3 : 1) : k >> (spread ? 2 : 0);
+  const int in = k - c * s.per[own];
+  const long long part = s.first[own] + 2 * c + s.wg0[own] + (spread ? in >> 2 : in);
+  return (spread ? part * 4 + (in & 3) : part) * s.rows[own] + s.at[own];
+}
 
-// One thread per own key: the weights its rows gave it, from their logits.
-__global__ void __launch_bounds__(kScoreThreads) prefix_score_kernel(const PrefixParams p) {
+// With m and l the running maximum and sum of a partial, M = max m and
+// *den = sum 2^(m - M) l, by a warp.  *den is NaN when a logit was NaN or +inf
+// (fmaxf drops a NaN, the sums do not).
+__device__ __forceinline__ float row_norm(const PrefixParams& p, const RowParts& s, float* den) {
+  const int lane = threadIdx.x & 31;
+  float m = -INFINITY, l = 0.f;
+  bool bad = false;
+#pragma unroll
+  for (int own = 0; own < 2; ++own) {
+    const float2* ml = own ? p.ml_s : p.ml_p;
+#pragma unroll 2
+    for (int k = lane; k < s.n[own]; k += 32) {
+      const float2 v = __ldcg(ml + part_row(p, s, own, k));
+      bad |= v.x != v.x || v.y != v.y;
+      const float mn = fmaxf(m, v.x);
+      if (mn != -INFINITY) l = l * fast_exp2(m - mn) + v.y * fast_exp2(v.x - mn);
+      m = mn;
+    }
+  }
+  float M = m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  l = m == -INFINITY ? 0.f : l * fast_exp2(m - M);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if (__any_sync(0xffffffffu, bad)) {
+    M = fmaxf(M, 0.f);
+    l = __int_as_float(0x7fffffff);
+  }
+  *den = l;
+  return M;
+}
+
+// The first CTAs merge the partials: o = sum 2^(m - M) O / sum 2^(m - M) l and
+// lse = M + log2 of the denominator, kMergeWarps / split rows a CTA, split
+// warps sharing a row's partials (few rows have many).  The others add the
+// weights of kScoreKeys own keys of a (sequence, group), from their logits and
+// the normalisers of the rows, which each finds for itself: that is a few
+// hundred cached loads, against a launch more and its wait.
+template <int D>
+__global__ void __launch_bounds__(kMergeWarps * 32)
+    prefix_finish_kernel(const __grid_constant__ PrefixParams p, int merge_ctas, int split) {
+  constexpr int V = D / 32;
+  __shared__ float part[kMergeWarps][D];
   __shared__ float norm[128];
   griddep_wait();
   griddep_launch_dependents();
-  const int bg = blockIdx.x, b = bg / p.G, g = bg - b * p.G;
-  const int len = own_len(p, b);
-  if (blockIdx.y * kScoreThreads >= len) return;
-  for (int i = threadIdx.x; i < p.rows_s; i += kScoreThreads) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (static_cast<int>(blockIdx.x) < merge_ctas) {
+    const int sub = warp % split;
+    const long long row = (static_cast<long long>(blockIdx.x) * kMergeWarps + warp) / split;
+    const bool in = row < static_cast<long long>(p.B) * p.T * p.H;
+    float acc[V];
+#pragma unroll
+    for (int y = 0; y < V; ++y) acc[y] = 0.f;
+    float M = -INFINITY, den = 0.f;
+    if (in) {
+      const int tok = static_cast<int>(row / p.H), h = static_cast<int>(row - static_cast<long long>(tok) * p.H);
+      const RowParts s = row_parts(p, tok, h);
+      M = row_norm(p, s, &den);
+#pragma unroll 1
+      for (int own = 0; own < 2; ++own) {
+        const float* po = own ? p.o_s : p.o_p;
+        const float2* ml = own ? p.ml_s : p.ml_p;
+        constexpr int U = 8;         // partial rows in flight
+#pragma unroll 1
+        for (int k0 = sub; k0 < s.n[own]; k0 += U * split) {
+          float w[U], x[U][V];
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int k = k0 + u * split;
+            w[u] = 0.f;
+#pragma unroll
+            for (int y = 0; y < V; ++y) x[u][y] = 0.f;
+            if (k < s.n[own]) {
+              const long long at = part_row(p, s, own, k);
+              const float mk = __ldcg(&ml[at].x);
+              if (mk != -INFINITY) {     // else its output was never written
+                const float* f = po + at * D + lane * V;
+                if constexpr (V == 4)
+                  *reinterpret_cast<float4*>(x[u]) = __ldcg(reinterpret_cast<const float4*>(f));
+                else
+                  *reinterpret_cast<float2*>(x[u]) = __ldcg(reinterpret_cast<const float2*>(f));
+                w[u] = fast_exp2(mk - M);
+              }
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int y = 0; y < V; ++y) acc[y] = fmaf(w[u], x[u][y], acc[y]);
+        }
+      }
+    }
+    if (split > 1) {
+#pragma unroll
+      for (int y = 0; y < V; ++y) part[warp][lane * V + y] = acc[y];
+      __syncthreads();
+      if (sub != 0) return;
+      for (int u = 1; u < split; ++u)
+#pragma unroll
+        for (int y = 0; y < V; ++y) acc[y] += part[warp + u][lane * V + y];
+    }
+    if (!in) return;
+    const float inv = M == -INFINITY ? 0.f : 1.f / den;
+    uint16_t* out = p.o + row * D + lane * V;
+    if constexpr (V == 4)
+      *reinterpret_cast<uint2*>(out) =
+          make_uint2(pack2(acc[0] * inv, acc[1] * inv), pack2(acc[2] * inv, acc[3] * inv));
+    else
+      *reinterpret_cast<uint32_t*>(out) = pack2(acc[0] * inv, acc[1] * inv);
+    if (lane == 0 && p.lse) p.lse[row] = M == -INFINITY ? -INFINITY : (M + log2f(den)) / kLog2e;
+    return;
+  }
+  const int id = static_cast<int>(blockIdx.x) - merge_ctas;
+  const int chunks = (p.C + kScoreKeys - 1) / kScoreKeys;
+  const int bg = id / chunks, b = bg / p.G, g = bg - b * p.G;
+  const int len = own_len(p, b), x0 = (id - bg * chunks) * kScoreKeys;
+  if (x0 >= len) return;
+  for (int i = warp; i < p.rows_s; i += kMergeWarps) {
     const int t = i / p.r;
-    const float n = __ldcg(p.lse2 + (static_cast<long long>(b) * p.T + t) * p.H + g * p.r + (i - t * p.r));
-    norm[i] = n == -INFINITY ? 0.f : n;     // a row that sees no key has logits of -inf alone
+    float den;
+    const float M = row_norm(p, row_parts(p, b * p.T + t, g * p.r + i - t * p.r), &den);
+    // a row that sees no key has logits of -inf alone
+    if (lane == 0) norm[i] = M == -INFINITY ? 0.f : M + log2f(den);
   }
   __syncthreads();
   const long long stride = static_cast<long long>(p.nb) * 128;
-  for (int x = blockIdx.y * kScoreThreads + threadIdx.x; x < len; x += gridDim.y * kScoreThreads) {
-    const float* s = p.logits + static_cast<long long>(bg) * p.rows_s * stride + x;
-    const long long at = static_cast<long long>(bg) * p.C + x;
-    float w = 0.f;
+  const int x = x0 + 4 * static_cast<int>(threadIdx.x);
+  if (x >= len) return;
+  const float* s = p.logits + static_cast<long long>(bg) * p.rows_s * stride + x;
+  float w[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 8
-    for (int i = 0; i < p.rows_s; ++i) w += fast_exp2(__ldcg(s + i * stride) - norm[i]);
-    p.w_out[at] = (p.w_in ? p.w_in[at] : 0.f) + w;
+  for (int i = 0; i < p.rows_s; ++i) {
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(s + i * stride));
+    w[0] += fast_exp2(v.x - norm[i]);
+    w[1] += fast_exp2(v.y - norm[i]);
+    w[2] += fast_exp2(v.z - norm[i]);
+    w[3] += fast_exp2(v.w - norm[i]);
   }
+  const long long at = static_cast<long long>(bg) * p.C + x;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)      // rows of C elements need not be 16-byte aligned
+    if (x + e < len) p.w_out[at + e] = (p.w_in ? p.w_in[at + e] : 0.f) + w[e];
 }
 
 // Most rows of a tile that is spread over the four warps: 32 lie in a warp's
@@ -1019,7 +1094,7 @@ constexpr size_t kSpreadPrefix = 32, kSpreadOwn = 16;
 
 // Workspace layout.
 struct PrefixWs {
-  size_t span, lse2, ml_p, o_p, ml_s, o_s, logits, bytes;
+  size_t span, ml_p, o_p, ml_s, o_s, logits, bytes;
 };
 
 PrefixWs ws_layout(const msa_shape& s, bool weights) {
@@ -1038,7 +1113,6 @@ PrefixWs ws_layout(const msa_shape& s, bool weights) {
     return x;
   };
   w.span = take((nsp + bg) * sizeof(int2));
-  w.lse2 = take(rows * s.n_kv_heads * sizeof(float));
   w.ml_p = take(pr * sizeof(float2));
   w.o_p = take(pr * d * sizeof(float));
   w.ml_s = take(sr * sizeof(float2));
@@ -1093,21 +1167,16 @@ cudaError_t launch(const msa_shape& s, const PrefixDecodeArgs& a, const PrefixPa
                          smem, st, tm, p);
   }
   if (e != cudaSuccess) return e;
-  {
-    ProfScope ps_("prefix_merge", st);
-    const long long all = static_cast<long long>(p.B) * p.T * p.H;
-    e = launch_dependent(prefix_merge_kernel<D>, dim3(static_cast<unsigned>(ceil_div(all, kMergeWarps))),
-                         dim3(kMergeWarps * 32), 0, st, p);
-  }
-  if (e != cudaSuccess || !p.w_out) return e;
-  {
-    ProfScope ps_("prefix_score", st);
-    const int64_t slices = std::min<int64_t>(ceil_div(p.C, kScoreThreads), 65535);   // grid limit
-    e = launch_dependent(prefix_score_kernel,
-                         dim3(static_cast<unsigned>(p.B) * p.G, static_cast<unsigned>(slices)),
-                         dim3(kScoreThreads), 0, st, p);
-  }
-  return e;
+  // warps a row: enough to have some 16 warps on every SM
+  const int64_t all = static_cast<int64_t>(p.B) * p.T * p.H;
+  int split = 1;
+  while (split < kMergeWarps && all * split < 16ll * grid) split *= 2;
+  const int64_t merge = ceil_div(all * split, kMergeWarps);
+  const int64_t score = p.w_out ? static_cast<int64_t>(p.B) * p.G * ceil_div(p.C, kScoreKeys) : 0;
+  if (merge + score >= (1ll << 31)) return cudaErrorInvalidValue;
+  ProfScope ps_("prefix_finish", st);
+  return launch_dependent(prefix_finish_kernel<D>, dim3(static_cast<unsigned>(merge + score)),
+                          dim3(kMergeWarps * 32), 0, st, p, static_cast<int>(merge), split);
 }
 
 }  // namespace
@@ -1133,7 +1202,6 @@ cudaError_t launch_prefix_decode(const msa_shape& s, const PrefixDecodeArgs& a, 
   p.num_pages = a.pages.num_pages;
   p.err = ctx->err;
   p.span = reinterpret_cast<int2*>(base + w.span);
-  p.lse2 = reinterpret_cast<float*>(base + w.lse2);
   p.ml_p = reinterpret_cast<float2*>(base + w.ml_p);
   p.o_p = reinterpret_cast<float*>(base + w.o_p);
   p.ml_s = reinterpret_cast<float2*>(base + w.ml_s);
