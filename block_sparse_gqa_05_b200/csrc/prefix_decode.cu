@@ -40,6 +40,12 @@ namespace msa {
 namespace {
 
 constexpr int kThreads = 384;
+// Most rows of a tile that is spread over the four warps: 32 lie in a warp's
+// TMEM lanes; own tiles need them twice, for the next segment's queries.  And
+// the blocks a segment needs to be spread: its softmax is then twice as fast,
+// but it leaves four partials instead of one.
+constexpr size_t kSpreadPrefix = 32, kSpreadOwn = 16;
+constexpr int kSpreadBlocks = 4;
 constexpr int kMaxGrid = 256;      // bound of the persistent grid, for the workspace size
 constexpr float kLog2e = 1.4426950408889634f;
 // A row's reference follows its maximum when that is 2^8 above it, and at once
@@ -66,7 +72,7 @@ struct PrefixParams {
   int Np, nbp;         // prefix rows and blocks
   int ntile, npt, nsp; // prefix row tiles and tile pairs of a group; prefix segments
   int rows_p, rows_s;  // rows of a prefix / own tile: min(128, B*T*r), T*r
-  bool spread_p, spread_s;   // such a tile is there four times, a quarter of the keys each
+  bool spread_p, spread_s;   // rows few enough for the tile to be there four times, a quarter of the keys each
   bool two_q;          // own queries have two stages, q_stage bytes apart
   int q_stage;
   long long cost_pair, cost_group, cost_prefix;   // of a pair segment, a group's, all prefix segments
@@ -98,6 +104,11 @@ __device__ __forceinline__ int blocks_before(long long u, long long start, int w
   if (u <= start) return 0;
   const long long d = u - start;
   return d >= static_cast<long long>(nb) * w ? nb : (static_cast<int>(d) + w - 1) / w;
+}
+
+// Whether a segment of nb blocks is spread over the four warps.
+__device__ __forceinline__ bool spreads(const PrefixParams& p, bool own, int nb) {
+  return (own ? p.spread_s : p.spread_p) && nb >= kSpreadBlocks;
 }
 
 // One CTA's share of a segment, as the walk hands it on (n == 0: the end).
@@ -199,8 +210,9 @@ struct PrefixSmem {
   static constexpr int kRing = D == 128 ? 5 : 10;       // K or V tiles in the ring
   static constexpr uint32_t kOffRing = 2 * kTile;       // two query tiles first
   static constexpr uint32_t kOffBar = kOffRing + kRing * kTile;
-  static constexpr uint32_t kOffSeg = kOffBar + 640;
-  static constexpr uint32_t kBytes = kOffSeg + kSegRing * 32;
+  static constexpr uint32_t kOffSeg = kOffBar + (2 * kRing + 2 * kSegRing + 16) * 8 + 16;
+  static constexpr uint32_t kOffPlan = kOffSeg + kSegRing * 32;      // scan scratch, first segment
+  static constexpr uint32_t kBytes = kOffPlan + kThreads / 32 * 8 + 64;
 };
 
 struct Bars {
@@ -214,15 +226,38 @@ struct Bars {
   uint64_t* drain;          // [2] the MMA warps' last commits
 };
 
-// mbar_wait out of line behind a probe: most waits here are complete, and the
-// bounded loop at each of them is most of their code.
-__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t phase, volatile int* abort,
-                                       uint32_t* err) {
-  return mbar_wait(bar, phase, abort, err);
+// What the waits need; ``now``: the limit is 0, so that a wait that is not
+// complete at its first probe expires.
+struct Waits {
+  volatile int* abort;
+  uint32_t* err;
+  bool now;
+};
+
+// The loop of a bounded wait, out of line behind a first probe.  The timer is
+// looked at every 256 probes only: reading it takes longer than most waits here.
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t phase, Waits w) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 1;; ++it) {
+    if (!w.now && mbar_try_wait(bar, phase)) return true;
+    if (*w.abort) return false;
+    if (!w.now && (it & 255u) != 0) continue;
+    const uint64_t t = globaltimer();
+    if (t0 == 0) t0 = t;
+    if (w.now || t - t0 > g_wait_limit_ns) {
+      atomicOr(w.err, kErrTimeout);
+      *w.abort = 1;
+      return false;
+    }
+  }
 }
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t phase, volatile int* abort,
-                                         uint32_t* err) {
-  return mbar_test(bar, phase) || wait_slow(bar, phase, abort, err);
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t phase, const Waits& w) {
+  return (w.now ? mbar_test(bar, phase) : mbar_try_wait(bar, phase)) || wait_slow(bar, phase, w);
+}
+// The same for a whole warp.  All lanes probe: measured, a hand-over between two
+// warps takes 100 clocks so, 190 through one lane and a shuffle.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t phase, const Waits& w) {
+  return __all_sync(0xffffffffu, wait_bar(bar, phase, w)) != 0;
 }
 
 // Sets *word, after everything this thread (and its warp, before a
@@ -236,16 +271,17 @@ __device__ __forceinline__ uint32_t read_count(const uint32_t* word) {
   return v;
 }
 // Bounded wait until *word >= want (a count another warp publishes).
-__device__ __noinline__ bool count_slow(const uint32_t* word, uint32_t want, volatile int* abort,
-                                        uint32_t* err) {
-  const uint64_t lim = g_wait_limit_ns;
-  const uint64_t t0 = globaltimer();
-  for (uint32_t it = 0;; ++it) {
+__device__ __noinline__ bool count_slow(const uint32_t* word, uint32_t want, Waits w) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 1;; ++it) {
     if (static_cast<int32_t>(read_count(word) - want) >= 0) return true;
-    if (*abort) return false;
-    if (lim == 0 || ((it & 63u) == 63u && globaltimer() - t0 > lim)) {
-      atomicOr(err, kErrTimeout);
-      *abort = 1;
+    if (*w.abort) return false;
+    if (!w.now && (it & 255u) != 0) continue;
+    const uint64_t t = globaltimer();
+    if (t0 == 0) t0 = t;
+    if (w.now || t - t0 > g_wait_limit_ns) {
+      atomicOr(w.err, kErrTimeout);
+      *w.abort = 1;
       return false;
     }
   }
@@ -257,12 +293,12 @@ __device__ __noinline__ bool count_slow(const uint32_t* word, uint32_t want, vol
 // loads complete in any order.  So it first waits for the load to be issued,
 // which happens after the slot's previous tile was loaded and released.
 template <int R>
-__device__ __forceinline__ bool wait_tile(const Bars& m, const uint32_t* issued, int item,
-                                          volatile int* abort, uint32_t* err) {
+__device__ __forceinline__ bool warp_wait_tile(const Bars& m, const uint32_t* issued, int item,
+                                               const Waits& w) {
   const uint32_t want = static_cast<uint32_t>(item) + 1u;
-  if (static_cast<int32_t>(read_count(issued) - want) < 0 && !count_slow(issued, want, abort, err))
-    return false;
-  return wait_bar(&m.full[item % R], (item / R) & 1, abort, err);
+  bool ok = true;
+  if (static_cast<int32_t>(read_count(issued) - want) < 0) ok = count_slow(issued, want, w);
+  return __all_sync(0xffffffffu, ok && wait_bar(&m.full[item % R], (item / R) & 1, w)) != 0;
 }
 
 __device__ __forceinline__ Seg read_seg(const Seg* at) {
@@ -344,6 +380,40 @@ __device__ __forceinline__ void exp_keys(const float* sv, uint64_t sc2, uint64_t
   }
 }
 
+// A value all lanes of the warp hold, in the form the compiler knows as such.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+
+// MMAs and commits by one elected lane (always the same one) of a whole warp,
+// without a branch: descriptors then stay in uniform registers, which the
+// instructions read; under a branch on the lane each of them was moved there
+// first (8 MMAs of S: 690 clocks against 512 of execution).
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+      ::"r"(smem_u32(bar))
+      : "memory");
+}
+
 // The CTA's range of the line and where its walk starts, by all threads.
 __device__ __forceinline__ void plan(const PrefixParams& p, long long* scratch, Walk* out) {
   const int tid = threadIdx.x;
@@ -423,8 +493,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint32_t kIdescS = idesc_bf16(128, 128, 0, 0);
   constexpr uint32_t kIdescO = idesc_bf16(128, D, 0, 1);
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ long long scratch[kThreads / 32];
-  __shared__ Walk walk0;
   if ((smem_u32(smem) & 1023u) != 0u) {
     if (threadIdx.x == 0) atomicOr(p.err, kErrTimeout);
     return;
@@ -446,6 +514,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* issued = tmem_slot + 1;                  // K and V tiles whose loads were issued
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 2);
   Seg* segs = reinterpret_cast<Seg*>(smem + L::kOffSeg);
+  long long* scratch = reinterpret_cast<long long*>(smem + L::kOffPlan);
+  Walk* walk0 = reinterpret_cast<Walk*>(scratch + kThreads / 32);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -461,9 +531,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&m.qfull[2 * i], 1);
       mbar_init(&m.qfull[2 * i + 1], 1);
       mbar_init(&m.sfull[i], 1);
-      mbar_init(&m.pfull[i], 128);
+      mbar_init(&m.pfull[i], 4);         // a tile's softmax warps
       mbar_init(&m.olast[i], 1);
-      mbar_init(&m.ofree[i], 128);
+      mbar_init(&m.ofree[i], 4);
       mbar_init(&m.turn[i], 1);
       mbar_init(&m.drain[i], 1);
     }
@@ -484,20 +554,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_wait();
   griddep_launch_dependents();
   __syncthreads();
-  plan(p, scratch, &walk0);
+  plan(p, scratch, walk0);
   __syncthreads();
   tc_fence_after();
+  const Waits w{abort_flag, p.err, g_wait_limit_ns == 0};
   const uint32_t tmem = *tmem_slot;   // S/P of the warpgroups at 0 and 128, O at 256 and 384
 
   if (warp < 4) {
     if (warp == 3) {
       // ------------------------------------------------------------ the walk
       if (lane == 0) {
-        Walk walk = walk0;
+        Walk walk = *walk0;
         for (int k = 0;; ++k) {
           const Seg q = walk.next(p);
           const int slot = k % kSegRing;
-          if (!wait_bar(&m.dempty[slot], ((k / kSegRing) & 1) ^ 1, abort_flag, p.err)) break;
+          if (!wait_bar(&m.dempty[slot], ((k / kSegRing) & 1) ^ 1, w)) break;
           reinterpret_cast<int4*>(segs + slot)[0] = reinterpret_cast<const int4*>(&q)[0];
           reinterpret_cast<int4*>(segs + slot)[1] = reinterpret_cast<const int4*>(&q)[1];
           mbar_arrive(&m.dfull[slot]);
@@ -512,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         for (int k = 0; ok; ++k) {
           const int ds = k % kSegRing;
-          if (!wait_bar(&m.dfull[ds], (k / kSegRing) & 1, abort_flag, p.err)) break;
+          if (!wait_bar(&m.dfull[ds], (k / kSegRing) & 1, w)) break;
           const Seg q = read_seg(segs + ds);
           if (q.n == 0) break;
           mbar_arrive(&m.dempty[ds]);
@@ -532,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int kv = 0; kv < 2; ++kv, ++item) {
               const int st = item % R;
-              if (!(ok = wait_bar(&m.empty[st], ((item / R) & 1) ^ 1, abort_flag, p.err))) break;
+              if (!(ok = wait_bar(&m.empty[st], ((item / R) & 1) ^ 1, w))) break;
               if (!q.pair()) mbar_arrive(&m.empty[st]);   // only one warpgroup will release it
               uint8_t* dst = smem + L::kOffRing + st * L::kTile;
               const CUtensorMap* map = kv_own ? (kv ? &tm.v : &tm.k) : (kv ? &tm.vp : &tm.kp);
@@ -560,8 +631,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     } else {
       // ------------------------- queries and MMAs of one warpgroup's tiles
-      const int wg = warp - 1;
-      const uint32_t tS = tmem + wg * 128, tO = tmem + 256 + wg * 128;
+      const int wg = static_cast<int>(uniform(warp - 1));
+      const uint32_t tS = uniform(tmem) + wg * 128, tO = tS + 256;
       uint8_t* qbuf = smem + wg * L::kTile;
       const uint32_t ring = smem_u32(smem + L::kOffRing);
       int ka = 0, i = 0, jobs = 0, loads = 0, pairs = 0;
@@ -572,7 +643,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto load_next = [&](int k) {
         for (; ka < k + kSegRing; ++ka) {
           const int ds = ka % kSegRing;
-          if (!mbar_test(&m.dfull[ds], (ka / kSegRing) & 1)) return;
+          bool there = false;
+          if (lane == 0) there = mbar_test(&m.dfull[ds], (ka / kSegRing) & 1);
+          __syncwarp();
+          if (!__shfl_sync(0xffffffffu, there, 0)) return;
           const Seg a = read_seg(segs + ds);
           if (a.n == 0) return;
           if (a.first(wg) >= a.n) continue;
@@ -583,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const CUtensorMap* map = own ? &tm.qs : &tm.qp;
             const int rows = own ? p.rows_s : p.rows_p;
             const int tok = own ? a.b * p.T : (a.tile() + (a.pair() ? wg : 0)) * (128 / p.r);
-            const int copies = (own ? p.spread_s : p.spread_p) ? 4 : 1;
+            const int copies = spreads(p, own, blocks_of(a.rows)) ? 4 : 1;
             mbar_arrive_expect_tx(bar, static_cast<uint32_t>(copies * rows * D * 2));
 #pragma unroll 1
             for (int u = 0; u < copies; ++u)
@@ -600,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       for (int k = 0; ok; ++k) {
         const int ds = k % kSegRing;
-        if (!(ok = __all_sync(0xffffffffu, wait_bar(&m.dfull[ds], (k / kSegRing) & 1, abort_flag, p.err))))
+        if (!(ok = warp_wait(&m.dfull[ds], (k / kSegRing) & 1, w)))
           break;
         const Seg q = read_seg(segs + ds);
         if (q.n == 0) break;
@@ -612,40 +686,38 @@ __global__ void __launch_bounds__(kThreads, 1)
             load_next(k);
           }
           ka = max(ka, k + 1);
-          if (!(ok = __all_sync(0xffffffffu, wait_bar(&m.qfull[2 * wg + (jobs & 1)], (jobs >> 1) & 1,
-                                                      abort_flag, p.err))))
+          if (!(ok = warp_wait(&m.qfull[2 * wg + (jobs & 1)], (jobs >> 1) & 1, w)))
             break;
           if (early) load_next(k);
-          const uint64_t qd = smem_desc(smem_u32(qbuf) + (early ? (jobs & 1) * p.q_stage : 0), 16, 1024, 2);
+          const uint64_t qd =
+              smem_desc(uniform(smem_u32(qbuf) + (early ? (jobs & 1) * p.q_stage : 0)), 16, 1024, 2);
           const bool rag = q.ragged(), pair = q.pair();
           // S = Q K^T of block x, over the P that the product before has read
           auto wait_k = [&](int x) {
-            return __all_sync(0xffffffffu, wait_tile<R>(m, issued, 2 * (q.n0 + x), abort_flag, p.err)) != 0;
+            return warp_wait_tile<R>(m, issued, 2 * (q.n0 + x), w);
           };
           auto issue_s = [&](int x) {
             const int st = 2 * (q.n0 + x) % R;
-            const uint64_t kd = smem_desc(ring + st * L::kTile, 16, 1024, 2);
+            const uint64_t kd = smem_desc(uniform(ring + st * L::kTile), 16, 1024, 2);
+            tc_fence_after();
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
               const uint32_t off = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
-              tc_mma_ss(tS, qd + off, kd + off, kIdescS, ks > 0 ? 1u : 0u);
+              mma_ss(tS, qd + off, kd + off, kIdescS, ks > 0 ? 1u : 0u);
             }
-            tc_commit(&m.sfull[wg]);
-            tc_commit(&m.empty[st]);
+            mma_commit(&m.sfull[wg]);
+            mma_commit(&m.empty[st]);
           };
           if (!(ok = wait_k(first))) break;
-          tc_fence_after();
-          if (lane == 0) issue_s(first);
-          __syncwarp();
+          issue_s(first);
           for (int x = first; x < q.n; x += step, ++i) {
             const bool last = x + step >= q.n;
             // O += P V; past a length only the 16-key steps that hold valid rows
             if (x == first && jobs > 0 &&
-                !(ok = __all_sync(0xffffffffu,
-                                  wait_bar(&m.ofree[wg], (jobs - 1) & 1, abort_flag, p.err))))
+                !(ok = warp_wait(&m.ofree[wg], (jobs - 1) & 1, w)))
               break;
             const int item = 2 * (q.n0 + x) + 1, st = item % R;
-            if (!(ok = __all_sync(0xffffffffu, wait_tile<R>(m, issued, item, abort_flag, p.err))))
+            if (!(ok = warp_wait_tile<R>(m, issued, item, w)))
               break;
             uint8_t* v = smem + L::kOffRing + st * L::kTile;
             int steps = 8;
@@ -660,35 +732,34 @@ __global__ void __launch_bounds__(kThreads, 1)
               fence_proxy_async_smem();
               __syncwarp();
             }
-            if (!(ok = __all_sync(0xffffffffu, wait_bar(&m.pfull[wg], i & 1, abort_flag, p.err))))
-              break;
             // Of a pair the two warpgroups take turns at the tensor cores, O +=
-            // P V and the next S together and with nothing left to wait for, so
-            // that one is in its softmax while the other's products run
+            // P V and the next S together, so that one is in its softmax while
+            // the other's products run; the weights are waited for last
             if (pair) {
               if (!last && !(ok = wait_k(x + step))) break;
               if ((wg == 1 || pairs > 0) &&
-                  !(ok = __all_sync(0xffffffffu, wait_bar(&m.turn[wg], (pairs - 1 + wg) & 1,
-                                                          abort_flag, p.err))))
+                  !(ok = warp_wait(&m.turn[wg], (pairs - 1 + wg) & 1, w)))
                 break;
               ++pairs;
             }
+            const uint64_t vd = smem_desc(uniform(smem_u32(v)), 16384, 1024, 2);
+            if (!(ok = warp_wait(&m.pfull[wg], i & 1, w))) break;
             tc_fence_after();
-            const uint64_t vd = smem_desc(smem_u32(v), 16384, 1024, 2);
-            if (lane == 0) {
+            if (steps == 8) {
 #pragma unroll
               for (int ks = 0; ks < 8; ++ks)
-                if (ks < steps)
-                  tc_mma_ts(tO, tS + 64 + ks * 8, vd + ks * 128, kIdescO,
-                            x > first || ks > 0 ? 1u : 0u);
-              tc_commit(&m.empty[st]);
-              if (last) tc_commit(&m.olast[wg]);
+                mma_ts(tO, tS + 64 + ks * 8, vd + ks * 128, kIdescO, x > first || ks > 0 ? 1u : 0u);
+            } else {
+#pragma unroll 1
+              for (int ks = 0; ks < steps; ++ks)
+                mma_ts(tO, tS + 64 + ks * 8, vd + ks * 128, kIdescO, x > first || ks > 0 ? 1u : 0u);
             }
-            __syncwarp();
-            if (!last) {
+            mma_commit(&m.empty[st]);
+            if (last) {
+              mma_commit(&m.olast[wg]);
+            } else {
               if (!pair && !(ok = wait_k(x + step))) break;
-              tc_fence_after();
-              if (lane == 0) issue_s(x + step);
+              issue_s(x + step);
             }
             if (pair && lane == 0) mbar_arrive(&m.turn[1 - wg]);
             __syncwarp();
@@ -699,12 +770,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&m.dempty[ds]);
       }
       // every load and MMA issued completes before TMEM is released
-      if (lane == 0) {
-        for (int x = max(0, loads - 2); x < loads; ++x)
-          mbar_drain(&m.qfull[2 * wg + (x & 1)], (x >> 1) & 1);
-        tc_drain(&m.drain[wg], 0);
-      }
-      __syncwarp();
+      mma_commit(&m.drain[wg]);
+      for (int x = max(0, loads - 2); x < loads; ++x)
+        mbar_drain(&m.qfull[2 * wg + (x & 1)], (x >> 1) & 1);
+      mbar_drain(&m.drain[wg], 0);
     }
   } else {
     // ------------------------------------------------------ softmax, one row a thread
@@ -721,7 +790,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto write_out = [&]() -> bool {
       if (!pend) return true;
       pend = false;
-      if (!__all_sync(0xffffffffu, wait_bar(&m.olast[wg], (jobs - 1) & 1, abort_flag, p.err)))
+      if (!warp_wait(&m.olast[wg], (jobs - 1) & 1, w))
         return false;
       if (pend_busy) {
         tc_fence_after();
@@ -737,12 +806,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
       }
-      mbar_arrive(&m.ofree[wg]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&m.ofree[wg]);
       return true;
     };
     for (int k = 0; ok; ++k) {
       const int ds = k % kSegRing;
-      if (!(ok = __all_sync(0xffffffffu, wait_bar(&m.dfull[ds], (k / kSegRing) & 1, abort_flag, p.err))))
+      if (!(ok = warp_wait(&m.dfull[ds], (k / kSegRing) & 1, w)))
         break;
       const Seg q = read_seg(segs + ds);
       __syncwarp();
@@ -753,7 +823,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Rows of the tile that exist, this thread's row and its last key.  A tile
       // of few rows is there four times, once per warp, and each warp takes a
       // quarter of every block's keys: four partials.
-      const bool spread = own ? p.spread_s : p.spread_p;
+      const bool spread = spreads(p, own, blocks_of(q.rows));
       const int tile = q.tile() + (q.pair() ? wg : 0);
       const int nrow = own ? p.rows_s : min(128, p.B * p.T * p.r - tile * 128);
       const int row = spread ? lane : quarter * 32 + lane;
@@ -762,7 +832,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int last_key = own ? q.rows - p.T + row / p.r : q.rows - 1;
       const long long part = 2ll * (static_cast<long long>(own ? q.id - p.nsp : q.id) + blockIdx.x) + wg;
       const int rows = own ? p.rows_s : p.rows_p;
-      const long long prow = spread ? (part * 4 + quarter) * rows + row : part * rows + row;
+      const bool room = own ? p.spread_s : p.spread_p;     // partials lie four times as far apart
+      const long long prow = (room ? part * 4 + (spread ? quarter : 0) : part) * rows + row;
       float2* ml = (own ? p.ml_s : p.ml_p) + prow;
       if (first >= q.n) {              // the one block of a short share is the other warpgroup's
         if (valid) *ml = make_float2(-INFINITY, 0.f);
@@ -773,7 +844,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         logit = p.logits + (static_cast<long long>(q.b * p.G + q.g) * p.rows_s + row) * p.nb * 128;
       float mref = -INFINITY, mtop = -INFINITY, l = 0.f;   // reference, maximum seen, sum
       for (int x = first; x < q.n; x += step, ++i) {
-        if (!(ok = __all_sync(0xffffffffu, wait_bar(&m.sfull[wg], i & 1, abort_flag, p.err)))) break;
+        if (!(ok = warp_wait(&m.sfull[wg], i & 1, w))) break;
         const int j = q.j0 + x;
         const int lim = last_key - j * 128;        // keys past lim are not seen
         if (busy) {
@@ -867,7 +938,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_wait_st();
           tc_fence_before();
         }
-        mbar_arrive(&m.pfull[wg]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&m.pfull[wg]);
         if (x == first && !(ok = write_out())) break;
       }
       if (!ok) break;
@@ -901,6 +973,7 @@ struct RowParts {
   int per[2], wg0[2], wgs[2];
   long long first[2];    // index of CTA span.x's first partial
   int rows[2], at[2];    // rows of a partial, and this row's place
+  bool spread[2];
 };
 
 __device__ __forceinline__ RowParts row_parts(const PrefixParams& p, int tok, int h) {
@@ -913,18 +986,21 @@ __device__ __forceinline__ RowParts row_parts(const PrefixParams& p, int tok, in
     const int2 span = __ldcg(p.span + id);
     s.wgs[0] = pair ? 1 : 2;
     s.wg0[0] = pair ? tile & 1 : 0;
-    s.per[0] = s.wgs[0] * (p.spread_p ? 4 : 1);
+    s.spread[0] = spreads(p, false, p.nbp);
+    s.per[0] = s.wgs[0] * (s.spread[0] ? 4 : 1);
     s.n[0] = (span.y - span.x + 1) * s.per[0];
     s.first[0] = 2ll * (id + span.x);
     s.rows[0] = p.rows_p;
     s.at[0] = at & 127;
   }
-  if (own_len(p, b) > 0) {
+  const int len = own_len(p, b);
+  if (len > 0) {
     const int id = b * p.G + g;
     const int2 span = __ldcg(p.span + p.nsp + id);
     s.wgs[1] = 2;
     s.wg0[1] = 0;
-    s.per[1] = p.spread_s ? 8 : 2;
+    s.spread[1] = spreads(p, true, blocks_of(len));
+    s.per[1] = s.spread[1] ? 8 : 2;
     s.n[1] = (span.y - span.x + 1) * s.per[1];
     s.first[1] = 2ll * (id + span.x);
     s.rows[1] = p.rows_s;
@@ -935,11 +1011,11 @@ __device__ __forceinline__ RowParts row_parts(const PrefixParams& p, int tok, in
 
 // Index of the row in partial k of segment kind own.
 __device__ __forceinline__ long long part_row(const PrefixParams& p, const RowParts& s, int own, int k) {
-  const bool spread = own ? p.spread_s : p.spread_p;
+  const bool spread = s.spread[own], room = own ? p.spread_s : p.spread_p;
   const int c = s.wgs[own] == 2 ? k >> (spread ? 3 : 1) : k >> (spread ? 2 : 0);
   const int in = k - c * s.per[own];
   const long long part = s.first[own] + 2 * c + s.wg0[own] + (spread ? in >> 2 : in);
-  return (spread ? part * 4 + (in & 3) : part) * s.rows[own] + s.at[own];
+  return (room ? part * 4 + (spread ? in & 3 : 0) : part) * s.rows[own] + s.at[own];
 }
 
 // With m and l the running maximum and sum of a partial, M = max m and
@@ -1087,10 +1163,6 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   for (int e = 0; e < 4; ++e)      // rows of C elements need not be 16-byte aligned
     if (x + e < len) p.w_out[at + e] = (p.w_in ? p.w_in[at + e] : 0.f) + w[e];
 }
-
-// Most rows of a tile that is spread over the four warps: 32 lie in a warp's
-// TMEM lanes; own tiles need them twice, for the next segment's queries.
-constexpr size_t kSpreadPrefix = 32, kSpreadOwn = 16;
 
 // Workspace layout.
 struct PrefixWs {
