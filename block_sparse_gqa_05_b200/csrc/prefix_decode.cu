@@ -48,9 +48,7 @@ constexpr size_t kSpreadPrefix = 32, kSpreadOwn = 16;
 constexpr int kSpreadBlocks = 4;
 constexpr int kMaxGrid = 256;      // bound of the persistent grid, for the workspace size
 constexpr float kLog2e = 1.4426950408889634f;
-// A row's reference follows its maximum when that is 2^8 above it, and at once
-// within a block when it is 2^64 above.
-constexpr float kRescaleLog2 = 8.f, kJumpLog2 = 64.f;
+constexpr float kRescaleLog2 = 8.f;   // a row's reference follows its maximum when that is 2^8 above it
 
 // Cost of a block on the line, by the kind of its segment, and of a segment.
 constexpr int kCostPair = 5, kCostSingle = 4, kCostSegment = 2;
@@ -109,6 +107,11 @@ __device__ __forceinline__ int blocks_before(long long u, long long start, int w
 // Whether a segment of nb blocks is spread over the four warps.
 __device__ __forceinline__ bool spreads(const PrefixParams& p, bool own, int nb) {
   return (own ? p.spread_s : p.spread_p) && nb >= kSpreadBlocks;
+}
+
+// Whether the tiles of a kind have 32 rows or fewer.
+__device__ __forceinline__ bool few_rows(const PrefixParams& p, bool own) {
+  return (own ? p.rows_s : p.rows_p) <= 32;
 }
 
 // One CTA's share of a segment, as the walk hands it on (n == 0: the end).
@@ -226,33 +229,36 @@ struct Bars {
   uint64_t* drain;          // [2] the MMA warps' last commits
 };
 
-// What the waits need; ``now``: the limit is 0, so that a wait that is not
-// complete at its first probe expires.
+// What the waits need; limit: in clocks; 0 makes a wait that is not complete at
+// its first probe expire.
 struct Waits {
   volatile int* abort;
   uint32_t* err;
-  bool now;
+  long long limit;
 };
 
-// The loop of a bounded wait, out of line behind a first probe.  The timer is
-// looked at every 256 probes only: reading it takes longer than most waits here.
-__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t phase, Waits w) {
-  uint64_t t0 = 0;
-  for (uint32_t it = 1;; ++it) {
-    if (!w.now && mbar_try_wait(bar, phase)) return true;
-    if (*w.abort) return false;
-    if (!w.now && (it & 255u) != 0) continue;
-    const uint64_t t = globaltimer();
-    if (t0 == 0) t0 = t;
-    if (w.now || t - t0 > g_wait_limit_ns) {
-      atomicOr(w.err, kErrTimeout);
-      *w.abort = 1;
-      return false;
-    }
-  }
+// The waits' limit in clocks, at 2 GHz, just above what the SM runs at.
+__device__ __forceinline__ long long wait_clocks() {
+  const uint64_t ns = g_wait_limit_ns;
+  return static_cast<long long>(ns > (1ull << 61) ? 1ull << 62 : 2 * ns);
 }
+
+__device__ __forceinline__ bool give_up(const Waits& w) {
+  atomicOr(w.err, kErrTimeout);
+  *w.abort = 1;
+  return false;
+}
+
+// Bounded wait for the completion of phase ``phase`` (parity), as mbar_wait, with
+// the SM clock for the bound: reading the timer takes longer than most waits.
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t phase, const Waits& w) {
-  return (w.now ? mbar_test(bar, phase) : mbar_try_wait(bar, phase)) || wait_slow(bar, phase, w);
+  if (w.limit == 0 ? mbar_test(bar, phase) : mbar_try_wait(bar, phase)) return true;
+  const long long t0 = clock64();
+  do {
+    if (w.limit != 0 && mbar_try_wait(bar, phase)) return true;
+    if (*w.abort) return false;
+  } while (clock64() - t0 < w.limit);
+  return give_up(w);
 }
 // The same for a whole warp.  All lanes probe: measured, a hand-over between two
 // warps takes 100 clocks so, 190 through one lane and a shuffle.
@@ -271,20 +277,14 @@ __device__ __forceinline__ uint32_t read_count(const uint32_t* word) {
   return v;
 }
 // Bounded wait until *word >= want (a count another warp publishes).
-__device__ __noinline__ bool count_slow(const uint32_t* word, uint32_t want, Waits w) {
-  uint64_t t0 = 0;
-  for (uint32_t it = 1;; ++it) {
-    if (static_cast<int32_t>(read_count(word) - want) >= 0) return true;
+__device__ __forceinline__ bool wait_count(const uint32_t* word, uint32_t want, const Waits& w) {
+  if (static_cast<int32_t>(read_count(word) - want) >= 0) return true;
+  const long long t0 = clock64();
+  do {
+    if (w.limit != 0 && static_cast<int32_t>(read_count(word) - want) >= 0) return true;
     if (*w.abort) return false;
-    if (!w.now && (it & 255u) != 0) continue;
-    const uint64_t t = globaltimer();
-    if (t0 == 0) t0 = t;
-    if (w.now || t - t0 > g_wait_limit_ns) {
-      atomicOr(w.err, kErrTimeout);
-      *w.abort = 1;
-      return false;
-    }
-  }
+  } while (clock64() - t0 < w.limit);
+  return give_up(w);
 }
 
 // Waits for K or V tile ``item`` of the ring.  The parity of a slot's phase
@@ -295,10 +295,9 @@ __device__ __noinline__ bool count_slow(const uint32_t* word, uint32_t want, Wai
 template <int R>
 __device__ __forceinline__ bool warp_wait_tile(const Bars& m, const uint32_t* issued, int item,
                                                const Waits& w) {
-  const uint32_t want = static_cast<uint32_t>(item) + 1u;
-  bool ok = true;
-  if (static_cast<int32_t>(read_count(issued) - want) < 0) ok = count_slow(issued, want, w);
-  return __all_sync(0xffffffffu, ok && wait_bar(&m.full[item % R], (item / R) & 1, w)) != 0;
+  const bool ok = wait_count(issued, static_cast<uint32_t>(item) + 1u, w) &&
+                  wait_bar(&m.full[item % R], (item / R) & 1, w);
+  return __all_sync(0xffffffffu, ok) != 0;
 }
 
 __device__ __forceinline__ Seg read_seg(const Seg* at) {
@@ -345,26 +344,6 @@ __device__ __forceinline__ void store_logits(float* dst, const float* sv, float 
 #pragma unroll
     for (int e = 0; e < 8; ++e) t8[e] = sv[y + e] * scale_log2;
     store8(dst + y, t8);
-  }
-}
-
-// Scales 64 weights of this row (32 columns of bf16 pairs) by a.
-__device__ __forceinline__ void scale_p(uint32_t taddr, float a) {
-#pragma unroll 1
-  for (int c = 0; c < 32; c += 4) {
-    uint32_t r[4];
-    asm volatile("tcgen05.wait::st.sync.aligned;\n\t"
-                 "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];\n\t"
-                 "tcgen05.wait::ld.sync.aligned;"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(taddr + c)
-                 : "memory");
-#pragma unroll
-    for (int y = 0; y < 4; ++y)
-      r[y] = pack2(__uint_as_float(r[y] << 16) * a, __uint_as_float(r[y] & 0xFFFF0000u) * a);
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr + c),
-                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
-                 : "memory");
   }
 }
 
@@ -557,10 +536,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   plan(p, scratch, walk0);
   __syncthreads();
   tc_fence_after();
-  const Waits w{abort_flag, p.err, g_wait_limit_ns == 0};
+  const Waits w{abort_flag, p.err, wait_clocks()};
   const uint32_t tmem = *tmem_slot;   // S/P of the warpgroups at 0 and 128, O at 256 and 384
 
   if (warp < 4) {
+    regs_dec<80>();
     if (warp == 3) {
       // ------------------------------------------------------------ the walk
       if (lane == 0) {
@@ -658,6 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int rows = own ? p.rows_s : p.rows_p;
             const int tok = own ? a.b * p.T : (a.tile() + (a.pair() ? wg : 0)) * (128 / p.r);
             const int copies = spreads(p, own, blocks_of(a.rows)) ? 4 : 1;
+            if (copies == 1 && few_rows(p, own)) dst += wg * 64 * 128;   // rows 64.. of the tile
             mbar_arrive_expect_tx(bar, static_cast<uint32_t>(copies * rows * D * 2));
 #pragma unroll 1
             for (int u = 0; u < copies; ++u)
@@ -748,11 +729,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (steps == 8) {
 #pragma unroll
               for (int ks = 0; ks < 8; ++ks)
-                mma_ts(tO, tS + 64 + ks * 8, vd + ks * 128, kIdescO, x > first || ks > 0 ? 1u : 0u);
+                mma_ts(tO, tS + ks * 8, vd + ks * 128, kIdescO, x > first || ks > 0 ? 1u : 0u);
             } else {
 #pragma unroll 1
               for (int ks = 0; ks < steps; ++ks)
-                mma_ts(tO, tS + 64 + ks * 8, vd + ks * 128, kIdescO, x > first || ks > 0 ? 1u : 0u);
+                mma_ts(tO, tS + ks * 8, vd + ks * 128, kIdescO, x > first || ks > 0 ? 1u : 0u);
             }
             mma_commit(&m.empty[st]);
             if (last) {
@@ -776,6 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_drain(&m.drain[wg], 0);
     }
   } else {
+    regs_inc<208>();
     // ------------------------------------------------------ softmax, one row a thread
     const int wg = (warp >> 2) - 1, quarter = warp & 3;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
@@ -826,9 +808,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool spread = spreads(p, own, blocks_of(q.rows));
       const int tile = q.tile() + (q.pair() ? wg : 0);
       const int nrow = own ? p.rows_s : min(128, p.B * p.T * p.r - tile * 128);
-      const int row = spread ? lane : quarter * 32 + lane;
-      const bool busy = spread || quarter * 32 < nrow;   // a warp without a row only keeps the pace
-      const bool valid = row < nrow;
+      // (a tile of up to 32 rows has them in the third quarter for the second
+      // warpgroup: the working warps of the two then run on different schedulers)
+      const int q0 = few_rows(p, own) ? 2 * wg : 0;
+      const int row = spread ? lane : (quarter - q0) * 32 + lane;
+      const bool valid = row >= 0 && row < nrow;
+      const bool busy = spread || (quarter >= q0 && (quarter - q0) * 32 < nrow);   // others keep the pace
       const int last_key = own ? q.rows - p.T + row / p.r : q.rows - 1;
       const long long part = 2ll * (static_cast<long long>(own ? q.id - p.nsp : q.id) + blockIdx.x) + wg;
       const int rows = own ? p.rows_s : p.rows_p;
@@ -842,21 +827,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       float* logit = nullptr;
       if (own && p.logits && valid)
         logit = p.logits + (static_cast<long long>(q.b * p.G + q.g) * p.rows_s + row) * p.nb * 128;
-      float mref = -INFINITY, mtop = -INFINITY, l = 0.f;   // reference, maximum seen, sum
+      float mref = -INFINITY, l = 0.f;   // reference of the accumulated O, sum of the weights
       for (int x = first; x < q.n; x += step, ++i) {
         if (!(ok = warp_wait(&m.sfull[wg], i & 1, w))) break;
         const int j = q.j0 + x;
         const int lim = last_key - j * 128;        // keys past lim are not seen
         if (busy) {
           tc_fence_after();
-          // O of the rows whose maximum is above the reference by more than
-          // 2^slack gets a new one; S of a block is issued after the product of
-          // the block before, so that one is complete.  P and the sums hold
-          // any power of two up to 2^100 with the same relative precision.
-          auto new_reference = [&](float slack) {
-            const bool grow = valid && mtop > mref + slack;
-            if (!__any_sync(0xffffffffu, grow)) return 1.f;
-            const float a = grow ? fast_exp2(mref - mtop) : 1.f;
+          // O of the rows whose maximum is above their reference by more than
+          // 2^8 is rescaled to a new one; S of a block is issued after the
+          // product of the block before, so that one is complete
+          auto new_reference = [&](float top) {
+            const bool grow = valid && top > mref + kRescaleLog2;
+            if (!__any_sync(0xffffffffu, grow)) return;
+            const float a = grow ? fast_exp2(mref - top) : 1.f;
             if (x > first) {
 #pragma unroll 1
               for (int c = 0; c < D / 32; ++c) {
@@ -867,23 +851,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int y = 0; y < 32; ++y) ov[y] *= a;
                 tmem_st32(tO + c * 32, ov);
               }
-              tc_wait_st();
             }
             l *= a;
-            if (grow) mref = mtop;
-            return a;
+            if (grow) mref = top;
           };
-          float sv[64];
           uint64_t l2[4] = {0, 0, 0, 0};
           uint32_t pk[16];
           if (spread) {
             const int k0 = quarter * 32;
+            float sv[32];
             tmem_ld32(tS + k0, sv);
             tc_wait_ld();
             mask_keys<32>(sv, lim - k0);
             if (logit) store_logits<32>(logit + j * 128 + k0, sv, p.scale_log2);
-            mtop = fmaxf(mtop, max_keys<32>(sv) * p.scale_log2);
-            new_reference(kRescaleLog2);
+            new_reference(max_keys<32>(sv) * p.scale_log2);
             const float mu = mref == -INFINITY ? 0.f : mref;   // a row that has seen no key yet
             exp_keys(sv, sc2, f2_pack(-mu, -mu), pk, l2);
             // this copy's weights of the other warps' keys are zero
@@ -891,46 +872,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int y = 0; y < 16; ++y) zero[y] = 0u;
 #pragma unroll 1
-            for (int c = 1; c < 4; ++c) tmem_st16(tS + 64 + ((quarter + c) & 3) * 16, zero);
-            tmem_st16(tS + 64 + quarter * 16, pk);
+            for (int c = 1; c < 4; ++c) tmem_st16(tS + ((quarter + c) & 3) * 16, zero);
+            tmem_st16(tS + quarter * 16, pk);
           } else {
-            // The reference is the maximum of the blocks before, so that the
-            // exponentials need not wait for this block's: it is looked at
-            // half by half (64 logits in registers) and only a jump of 2^64
-            // makes a new one at once.  Rows without a reference look ahead.
-            if (__any_sync(0xffffffffu, valid && mref == -INFINITY)) {
-#pragma unroll 1
-              for (int hf = 0; hf < 2; ++hf) {
-                tmem_ld32(tS + hf * 64, sv);
-                tmem_ld32(tS + hf * 64 + 32, sv + 32);
-                tc_wait_ld();
-                mask_keys<64>(sv, lim - hf * 64);
-                mtop = fmaxf(mtop, max_keys<64>(sv) * p.scale_log2);
-              }
-            }
-            new_reference(kRescaleLog2);
-            // P goes over the columns of the upper half of S, which is read
-            // first, so that the lower half stays readable
-#pragma unroll 1
-            for (int hf = 1; hf >= 0; --hf) {
-              tmem_ld32(tS + hf * 64, sv);
-              tmem_ld32(tS + hf * 64 + 32, sv + 32);
-              tc_wait_ld();
-              mask_keys<64>(sv, lim - hf * 64);
-              if (logit) store_logits<64>(logit + j * 128 + hf * 64, sv, p.scale_log2);
-              mtop = fmaxf(mtop, max_keys<64>(sv) * p.scale_log2);
-              if (__any_sync(0xffffffffu, valid && mtop > mref + kJumpLog2)) {
-                const float a = new_reference(kJumpLog2);
+            // The whole row in registers: one wait for TMEM, and nothing between
+            // the exponentials, whose unit is what bounds a block (1,024 clocks)
+            float sv[128];
 #pragma unroll
-                for (int y = 0; y < 4; ++y) l2[y] = fmul2(l2[y], f2_pack(a, a));
-                if (hf == 0) scale_p(tS + 96, a);      // the upper half's weights
-              }
-              const float mu = mref == -INFINITY ? 0.f : mref;
-              const uint64_t mm2 = f2_pack(-mu, -mu);
-              exp_keys(sv, sc2, mm2, pk, l2);
-              tmem_st16(tS + 64 + hf * 32, pk);
-              exp_keys(sv + 32, sc2, mm2, pk, l2);
-              tmem_st16(tS + 64 + hf * 32 + 16, pk);
+            for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, sv + c * 32);
+            tc_wait_ld();
+            mask_keys<128>(sv, lim);
+            if (logit) store_logits<128>(logit + j * 128, sv, p.scale_log2);
+            new_reference(max_keys<128>(sv) * p.scale_log2);
+            const float mu = mref == -INFINITY ? 0.f : mref;
+            const uint64_t mm2 = f2_pack(-mu, -mu);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              exp_keys(sv + c * 32, sc2, mm2, pk, l2);
+              tmem_st16(tS + c * 16, pk);
             }
           }
           const float2 la = f2_unpack(fadd2(fadd2(l2[0], l2[1]), fadd2(l2[2], l2[3])));
@@ -1297,7 +1256,7 @@ cudaError_t launch_prefix_decode(const msa_shape& s, const PrefixDecodeArgs& a, 
   p.spread_p = rows <= static_cast<int64_t>(kSpreadPrefix);
   p.spread_s = p.rows_s <= static_cast<int>(kSpreadOwn);
   p.two_q = p.rows_s <= 64;
-  p.q_stage = p.spread_s ? 16 * 128 : 64 * 128;
+  p.q_stage = (p.spread_s ? 16 : p.rows_s <= 32 ? 32 : 64) * 128;
   p.cost_pair = static_cast<long long>(p.nbp) * kCostPair + kCostSegment;
   const long long last = (p.ntile & 1) ? static_cast<long long>(p.nbp) * kCostSingle + kCostSegment
                                        : p.cost_pair;
