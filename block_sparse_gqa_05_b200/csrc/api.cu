@@ -68,7 +68,7 @@ msa_status check_prefix_decode(const msa_shape* s) {
   const msa_status st = check_shape(&c, true, false);
   if (st != MSA_OK) return st;
   const int64_t rows = static_cast<int64_t>(s->seq_q) * (s->n_q_heads / s->n_kv_heads);
-  return rows > 128 ? MSA_ERR_UNSUPPORTED : MSA_OK;
+  return rows > 128 || !prefix_decode_supported(*s, 0) ? MSA_ERR_UNSUPPORTED : MSA_OK;
 }
 
 msa_status check_evict(const msa_shape* s) {
@@ -583,6 +583,7 @@ msa_status msa_forward_prefill_paged(const msa_shape* s, int num_pages,
 // The checks and the launch shared by the contiguous and the paged call.
 static msa_status prefix_decode(const msa_shape* s, const PrefixDecodeArgs& a, void* ws,
                                 size_t ws_bytes, void* stream) {
+  if (!prefix_decode_supported(*s, a.prefix_len)) return MSA_ERR_UNSUPPORTED;
   if (!a.q || !a.k || !a.v || !a.o || !a.lens || (a.w_in && !a.w_out)) return MSA_ERR_NULL_PTR;
   if (!aligned16(a.q) || !aligned16(a.k) || !aligned16(a.v) || !aligned16(a.o) ||
       !aligned4(a.lens) || !aligned4(a.lse) || !aligned4(a.w_in) || !aligned4(a.w_out))

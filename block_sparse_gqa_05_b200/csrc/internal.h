@@ -140,6 +140,7 @@ struct PrefixDecodeArgs {
   const int32_t* prefix_pages = nullptr;
   PageTable pages;
 };
+bool prefix_decode_supported(const msa_shape& s, int prefix_len);
 size_t prefix_decode_workspace_bytes(const msa_shape& s, bool weights);
 cudaError_t launch_prefix_decode(const msa_shape& s, const PrefixDecodeArgs& a, void* ws,
                                  cudaStream_t st);

@@ -50,8 +50,10 @@ constexpr int kMaxGrid = 256;      // bound of the persistent grid, for the work
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleLog2 = 8.f;   // a row's reference follows its maximum when that is 2^8 above it
 
-// Cost of a block on the line, by the kind of its segment, and of a segment.
-constexpr int kCostPair = 5, kCostSingle = 4, kCostSegment = 2;
+// Cost of a block on the line, in some 500 clocks: of a pair, of a spread tile, of
+// another single tile; and of a segment.
+constexpr int kCostPair = 7, kCostSpread = 5, kCostSingle = 8, kCostSegment = 2;
+constexpr int kCostMost = 8;
 
 struct PrefixParams {
   uint16_t* o;
@@ -73,7 +75,7 @@ struct PrefixParams {
   bool spread_p, spread_s;   // rows few enough for the tile to be there four times, a quarter of the keys each
   bool two_q;          // own queries have two stages, q_stage bytes apart
   int q_stage;
-  long long cost_pair, cost_group, cost_prefix;   // of a pair segment, a group's, all prefix segments
+  int cost_pair, cost_group, cost_prefix;   // line cost of a pair segment, a group's, all prefix segments
   float scale_log2;
 };
 
@@ -87,26 +89,30 @@ __device__ __forceinline__ int own_len(const PrefixParams& p, int b) {
 
 __device__ __forceinline__ int blocks_of(int rows) { return (rows + 127) >> 7; }
 
-// Line cost of one group's segment over a sequence's own cache.
-__device__ __forceinline__ int own_cost(int nb) { return nb ? nb * kCostSingle + kCostSegment : 0; }
-
 // The line is cut into ``parts`` ranges [part_begin(c), part_begin(c + 1)); a
 // block belongs to the range it starts in.
-__device__ __forceinline__ long long part_begin(long long c, long long total, int parts) {
-  return (c * total + parts - 1) / parts;
+__device__ __forceinline__ int part_begin(int c, int total, int parts) {
+  const int q = total / parts;
+  return c * q + min(c, total - q * parts);
 }
 
 // Blocks of a segment that start at ``start`` and cost ``w`` each, up to line
 // position ``u``.
-__device__ __forceinline__ int blocks_before(long long u, long long start, int w, int nb) {
-  if (u <= start) return 0;
-  const long long d = u - start;
-  return d >= static_cast<long long>(nb) * w ? nb : (static_cast<int>(d) + w - 1) / w;
+__device__ __forceinline__ int blocks_before(int u, int start, int w, int nb) {
+  return u <= start ? 0 : min(nb, (u - start + w - 1) / w);
 }
 
 // Whether a segment of nb blocks is spread over the four warps.
 __device__ __forceinline__ bool spreads(const PrefixParams& p, bool own, int nb) {
   return (own ? p.spread_s : p.spread_p) && nb >= kSpreadBlocks;
+}
+
+// Line cost of a block of a single segment, and of one group's own segment.
+__device__ __forceinline__ int single_cost(const PrefixParams& p, bool own, int nb) {
+  return spreads(p, own, nb) ? kCostSpread : kCostSingle;
+}
+__device__ __forceinline__ int own_cost(const PrefixParams& p, int nb) {
+  return nb ? nb * single_cost(p, true, nb) + kCostSegment : 0;
 }
 
 // Whether the tiles of a kind have 32 rows or fewer.
@@ -140,14 +146,14 @@ struct __align__(16) Seg {
 
 // Walks a CTA's segments along the line.
 struct Walk {
-  long long u0, u1, pos;
+  int u0, u1, pos;
   int s, b, g, len, n0;
 
   __device__ __forceinline__ Seg next(const PrefixParams& p) {
     Seg q;
     for (;;) {
       int w, nb;
-      const long long start = pos;
+      const int start = pos;
       if (s < p.nsp) {
         const int g_ = s / p.npt, tile = 2 * (s - g_ * p.npt);
         const bool pair = tile + 1 < p.ntile;
@@ -157,8 +163,8 @@ struct Walk {
         q.tile_kind = tile << 2 | (pair ? 2 : 0);
         q.rows = p.Np;
         nb = p.nbp;
-        w = pair ? kCostPair : kCostSingle;
-        pos += static_cast<long long>(nb) * w + kCostSegment;
+        w = pair ? kCostPair : single_cost(p, false, nb);
+        pos += nb * w + kCostSegment;
         ++s;
       } else {
         if (b < p.B && len < 0) len = own_len(p, b);
@@ -174,8 +180,8 @@ struct Walk {
         q.tile_kind = 1;
         q.rows = len;
         nb = blocks_of(len);
-        w = kCostSingle;
-        if (b < p.B) pos += own_cost(nb);
+        w = single_cost(p, true, nb);
+        if (b < p.B) pos += own_cost(p, nb);
         if (++g >= p.G) {
           g = 0;
           ++b;
@@ -215,7 +221,7 @@ struct PrefixSmem {
   static constexpr uint32_t kOffBar = kOffRing + kRing * kTile;
   static constexpr uint32_t kOffSeg = kOffBar + (2 * kRing + 2 * kSegRing + 16) * 8 + 16;
   static constexpr uint32_t kOffPlan = kOffSeg + kSegRing * 32;      // scan scratch, first segment
-  static constexpr uint32_t kBytes = kOffPlan + kThreads / 32 * 8 + 64;
+  static constexpr uint32_t kBytes = kOffPlan + kThreads / 32 * 4 + 64;
 };
 
 struct Bars {
@@ -394,73 +400,69 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
 }
 
 // The CTA's range of the line and where its walk starts, by all threads.
-__device__ __forceinline__ void plan(const PrefixParams& p, long long* scratch, Walk* out) {
-  const int tid = threadIdx.x;
+__device__ __forceinline__ void plan(const PrefixParams& p, int* scratch, Walk* out) {
+  constexpr int kWarps = kThreads / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.B + kThreads - 1) / kThreads;
   const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-  long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += own_cost(blocks_of(own_len(p, b)));
-  // exclusive scan of the threads' sums
-  const int lane = tid & 31, warp = tid >> 5;
-  long long inc = mine;
+  int mine = 0;
+#pragma unroll 1
+  for (int b = b0; b < b1; ++b) mine += own_cost(p, blocks_of(own_len(p, b)));
+  // exclusive scan of the threads' sums: in the warps, then over their totals
+  int inc = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+    const int v = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += v;
   }
   if (lane == 31) scratch[warp] = inc;
   __syncthreads();
-  long long before = inc - mine, all = 0;
-  for (int i = 0; i < kThreads / 32; ++i) {
-    if (i < warp) before += scratch[i];
-    all += scratch[i];
+  int sums = lane < kWarps ? scratch[lane] : 0;
+  const int own_total = sums;
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, sums, o);
+    if (lane >= o) sums += v;
   }
-  const long long total = p.cost_prefix + all * p.G;
+  const int before = inc - mine + __shfl_sync(0xffffffffu, sums - own_total, warp);
+  const int all = __shfl_sync(0xffffffffu, sums, kWarps - 1);
+  const int total = p.cost_prefix + all * p.G;
   // no more parts than blocks there are: every part between a segment's first
   // and last one then holds a block of it
-  const int parts = static_cast<int>(
-      max(1ll, min(static_cast<long long>(gridDim.x), total / max(kCostPair, kCostSingle))));
-  const long long u0 = min(total, part_begin(blockIdx.x, total, parts));
-  const long long u1 = min(total, part_begin(blockIdx.x + 1, total, parts));
-  if (u0 < p.cost_prefix) {
-    if (tid == 0) {
-      const int g = static_cast<int>(u0 / p.cost_group);
-      const long long rest = u0 - g * p.cost_group;
-      const int pt = min(static_cast<int>(rest / p.cost_pair), p.npt - 1);
-      out->s = g * p.npt + pt;
-      out->pos = g * p.cost_group + pt * p.cost_pair;
-      out->b = out->g = 0;
-      out->len = -1;
-    }
-  } else {
-    if (tid == 0) {            // past every block, unless a thread below finds its place
-      out->s = p.nsp;
-      out->b = p.B;
-      out->g = 0;
-      out->len = -1;
-      out->pos = total;
-    }
-    __syncthreads();
-    const long long at = u0 - p.cost_prefix;   // < all * G when there is anything left
-    if (at >= before * p.G && at < (before + mine) * p.G) {
-      long long st = before;
-      for (int b = b0; b < b1; ++b) {
-        const int c = own_cost(blocks_of(own_len(p, b)));
-        if (at < (st + c) * p.G) {
-          const int g = static_cast<int>((at - st * p.G) / c);
-          out->b = b;
-          out->g = g;
-          out->pos = p.cost_prefix + st * p.G + static_cast<long long>(g) * c;
-          break;
-        }
-        st += c;
-      }
-    }
-  }
+  const int parts = max(1, min(static_cast<int>(gridDim.x), total / kCostMost));
+  const int u0 = min(total, part_begin(blockIdx.x, total, parts));
+  const int u1 = min(total, part_begin(blockIdx.x + 1, total, parts));
   if (tid == 0) {
     out->u0 = u0;
     out->u1 = u1;
-    out->n0 = 0;
+    out->n0 = out->b = out->g = 0;
+    out->len = -1;
+    if (u0 < p.cost_prefix) {
+      const int g = u0 / p.cost_group, pt = min((u0 - g * p.cost_group) / p.cost_pair, p.npt - 1);
+      out->s = g * p.npt + pt;
+      out->pos = g * p.cost_group + pt * p.cost_pair;
+    } else {                   // past every block, unless a thread below finds its place
+      out->s = p.nsp;
+      out->b = p.B;
+      out->pos = total;
+    }
+  }
+  __syncthreads();
+  const int at = u0 - p.cost_prefix;   // < all * G when there is anything left
+  if (at >= 0 && at >= before * p.G && at < (before + mine) * p.G) {
+    int st = before;
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+      const int c = own_cost(p, blocks_of(own_len(p, b)));
+      if (at < (st + c) * p.G) {
+        const int g = (at - st * p.G) / c;
+        out->b = b;
+        out->g = g;
+        out->pos = p.cost_prefix + st * p.G + g * c;
+        break;
+      }
+      st += c;
+    }
   }
 }
 
@@ -493,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* issued = tmem_slot + 1;                  // K and V tiles whose loads were issued
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 2);
   Seg* segs = reinterpret_cast<Seg*>(smem + L::kOffSeg);
-  long long* scratch = reinterpret_cast<long long*>(smem + L::kOffPlan);
+  int* scratch = reinterpret_cast<int*>(smem + L::kOffPlan);
   Walk* walk0 = reinterpret_cast<Walk*>(scratch + kThreads / 32);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -532,7 +534,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   // nothing of that one's is read or overwritten before this
   griddep_wait();
   griddep_launch_dependents();
-  __syncthreads();
   plan(p, scratch, walk0);
   __syncthreads();
   tc_fence_after();
@@ -765,33 +766,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
     int i = 0, jobs = 0;
     bool ok = true;
-    // The output of a segment is written after the softmax of the next one's
-    // first block, so that its last product runs meanwhile.
-    bool pend = false, pend_busy = false, pend_valid = false;
-    float* pend_o = nullptr;
-    auto write_out = [&]() -> bool {
-      if (!pend) return true;
-      pend = false;
-      if (!warp_wait(&m.olast[wg], (jobs - 1) & 1, w))
-        return false;
-      if (pend_busy) {
-        tc_fence_after();
-#pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          float ov[32];
-          tmem_ld32(tO + c * 32, ov);
-          tc_wait_ld();
-          if (pend_valid) {
-#pragma unroll
-            for (int y = 0; y < 32; y += 8) store8(pend_o + c * 32 + y, ov + y);
-          }
-        }
-        tc_fence_before();
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&m.ofree[wg]);
-      return true;
-    };
     for (int k = 0; ok; ++k) {
       const int ds = k % kSegRing;
       if (!(ok = warp_wait(&m.dfull[ds], (k / kSegRing) & 1, w)))
@@ -899,18 +873,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&m.pfull[wg]);
-        if (x == first && !(ok = write_out())) break;
       }
       if (!ok) break;
-      // the partial of this CTA and warpgroup
-      if (valid) *ml = make_float2(mref, l);
-      pend = true;
-      pend_busy = busy;
-      pend_valid = valid;
-      pend_o = (own ? p.o_s : p.o_p) + prow * D;
-      ++jobs;
+      // the partial of this CTA and warpgroup; the S of the next segment's first
+      // block is on its way meanwhile
+      if (!(ok = warp_wait(&m.olast[wg], jobs++ & 1, w))) break;
+      if (busy) {
+        tc_fence_after();
+        float ov[D];
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) tmem_ld32(tO + c * 32, ov + c * 32);
+        tc_wait_ld();
+        tc_fence_before();
+        if (valid) {
+          float* orow = (own ? p.o_s : p.o_p) + prow * D;
+#pragma unroll
+          for (int y = 0; y < D; y += 8) store8(orow + y, ov + y);
+          *ml = make_float2(mref, l);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&m.ofree[wg]);
     }
-    if (ok) write_out();
   }
 
   tc_fence_before();
@@ -1212,6 +1196,17 @@ cudaError_t launch(const msa_shape& s, const PrefixDecodeArgs& a, const PrefixPa
 
 }  // namespace
 
+// The line's positions and the partials' row indices are 32-bit.
+bool prefix_decode_supported(const msa_shape& s, int prefix_len) {
+  const int64_t r = s.n_q_heads / s.n_kv_heads, rows = static_cast<int64_t>(s.batch) * s.seq_q * r;
+  const int64_t bg = static_cast<int64_t>(s.batch) * s.n_kv_heads;
+  const int64_t nsp = ceil_div(ceil_div(rows, 128), 2) * s.n_kv_heads;
+  const int64_t line = nsp * (ceil_div(prefix_len, 128) * kCostMost + kCostSegment) +
+                       bg * (ceil_div(s.seq_kv, 128) * kCostMost + kCostSegment);
+  const int64_t parts = std::max(2 * (nsp + kMaxGrid) * 128, 2 * (bg + kMaxGrid) * std::max<int64_t>(s.seq_q * r, 64));
+  return line < (1ll << 31) && parts < (1ll << 31);
+}
+
 size_t prefix_decode_workspace_bytes(const msa_shape& s, bool weights) {
   return ws_layout(s, weights).bytes;
 }
@@ -1257,10 +1252,9 @@ cudaError_t launch_prefix_decode(const msa_shape& s, const PrefixDecodeArgs& a, 
   p.spread_s = p.rows_s <= static_cast<int>(kSpreadOwn);
   p.two_q = p.rows_s <= 64;
   p.q_stage = (p.spread_s ? 16 : p.rows_s <= 32 ? 32 : 64) * 128;
-  p.cost_pair = static_cast<long long>(p.nbp) * kCostPair + kCostSegment;
-  const long long last = (p.ntile & 1) ? static_cast<long long>(p.nbp) * kCostSingle + kCostSegment
-                                       : p.cost_pair;
-  p.cost_group = (p.npt - 1) * p.cost_pair + last;
+  p.cost_pair = p.nbp * kCostPair + kCostSegment;
+  const int single = p.spread_p && p.nbp >= kSpreadBlocks ? kCostSpread : kCostSingle;
+  p.cost_group = (p.npt - 1) * p.cost_pair + ((p.ntile & 1) ? p.nbp * single + kCostSegment : p.cost_pair);
   p.cost_prefix = p.Np > 0 ? p.cost_group * p.G : 0;
   p.scale_log2 = kLog2e / sqrtf(static_cast<float>(s.head_dim));
   // no more CTAs than blocks there can be
