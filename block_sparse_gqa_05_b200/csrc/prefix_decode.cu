@@ -906,205 +906,226 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 constexpr int kMergeWarps = 8;
-constexpr int kScoreKeys = 4 * kMergeWarps * 32;   // keys of a CTA: four a thread
 
-// The partials of one row (token tok, head h): of the prefix segment of its
-// tile and of its own segment, of the CTAs of their spans, of both warpgroups
-// (of a pair: the tile's), of the four quarters of a spread tile.
-struct RowParts {
-  int n[2];              // partials of the prefix and of the own segment
-  int per[2], wg0[2], wgs[2];
-  long long first[2];    // index of CTA span.x's first partial
-  int rows[2], at[2];    // rows of a partial, and this row's place
-  bool spread[2];
+// The partials of one row of a segment: n of them, of the CTAs of its span, of
+// both warpgroups (of a pair: the tile's), of the four quarters of a spread tile.
+struct Parts {
+  int n, per, first;     // per CTA; index of the first CTA's first (CTA, warpgroup)
+  int rows, at;          // rows of a partial, and this row's place
+  bool spread, room;     // room: partials lie four times as far apart
 };
 
-__device__ __forceinline__ RowParts row_parts(const PrefixParams& p, int tok, int h) {
-  RowParts s;
-  const int b = tok / p.T, t = tok - b * p.T, g = h / p.r, hr = h - g * p.r;
-  s.n[0] = s.n[1] = 0;
-  if (p.nsp > 0) {
-    const int at = tok * p.r + hr, tile = at >> 7, id = g * p.npt + (tile >> 1);
-    const bool pair = (tile | 1) < p.ntile;
-    const int2 span = __ldcg(p.span + id);
-    s.wgs[0] = pair ? 1 : 2;
-    s.wg0[0] = pair ? tile & 1 : 0;
-    s.spread[0] = spreads(p, false, p.nbp);
-    s.per[0] = s.wgs[0] * (s.spread[0] ? 4 : 1);
-    s.n[0] = (span.y - span.x + 1) * s.per[0];
-    s.first[0] = 2ll * (id + span.x);
-    s.rows[0] = p.rows_p;
-    s.at[0] = at & 127;
+__device__ __forceinline__ Parts parts_of(const PrefixParams& p, bool own, int tok, int b, int h, int len) {
+  Parts s;
+  const int g = h / p.r, hr = h - g * p.r;
+  s.room = own ? p.spread_s : p.spread_p;
+  s.rows = own ? p.rows_s : p.rows_p;
+  const int nb = own ? blocks_of(len) : p.nbp;
+  s.spread = spreads(p, own, nb);
+  int id, wgs = 2, wg0 = 0;
+  if (own) {
+    id = b * p.G + g;
+    s.at = (tok - b * p.T) * p.r + hr;
+  } else {
+    const int at = tok * p.r + hr, tile = at >> 7;
+    id = g * p.npt + (tile >> 1);
+    s.at = at & 127;
+    if ((tile | 1) < p.ntile) {
+      wgs = 1;
+      wg0 = tile & 1;
+    }
   }
-  const int len = own_len(p, b);
-  if (len > 0) {
-    const int id = b * p.G + g;
-    const int2 span = __ldcg(p.span + p.nsp + id);
-    s.wgs[1] = 2;
-    s.wg0[1] = 0;
-    s.spread[1] = spreads(p, true, blocks_of(len));
-    s.per[1] = s.spread[1] ? 8 : 2;
-    s.n[1] = (span.y - span.x + 1) * s.per[1];
-    s.first[1] = 2ll * (id + span.x);
-    s.rows[1] = p.rows_s;
-    s.at[1] = t * p.r + hr;
+  s.per = wgs * (s.spread ? 4 : 1);
+  s.n = 0;
+  s.first = 0;
+  if (nb > 0) {
+    const int2 span = __ldcg(p.span + (own ? p.nsp + id : id));
+    s.n = (span.y - span.x + 1) * s.per;
+    s.first = 2 * (id + span.x) + wg0;
   }
   return s;
 }
 
-// Index of the row in partial k of segment kind own.
-__device__ __forceinline__ long long part_row(const PrefixParams& p, const RowParts& s, int own, int k) {
-  const bool spread = s.spread[own], room = own ? p.spread_s : p.spread_p;
-  const int c = s.wgs[own] == 2 ? k >> (spread ? 3 : 1) : k >> (spread ? 2 : 0);
-  const int in = k - c * s.per[own];
-  const long long part = s.first[own] + 2 * c + s.wg0[own] + (spread ? in >> 2 : in);
-  return (room ? part * 4 + (spread ? in & 3 : 0) : part) * s.rows[own] + s.at[own];
+// Index of the row in partial k.
+__device__ __forceinline__ int part_row(const Parts& s, int k) {
+  const int c = k / s.per, in = k - c * s.per;
+  const int part = s.first + 2 * c + (s.spread ? in >> 2 : in);
+  return (s.room ? part * 4 + (s.spread ? in & 3 : 0) : part) * s.rows + s.at;
 }
 
-// With m and l the running maximum and sum of a partial, M = max m and
-// *den = sum 2^(m - M) l, by a warp.  *den is NaN when a logit was NaN or +inf
-// (fmaxf drops a NaN, the sums do not).
-__device__ __forceinline__ float row_norm(const PrefixParams& p, const RowParts& s, float* den) {
-  const int lane = threadIdx.x & 31;
-  float m = -INFINITY, l = 0.f;
-  bool bad = false;
-#pragma unroll
-  for (int own = 0; own < 2; ++own) {
-    const float2* ml = own ? p.ml_s : p.ml_p;
-#pragma unroll 2
-    for (int k = lane; k < s.n[own]; k += 32) {
-      const float2 v = __ldcg(ml + part_row(p, s, own, k));
-      bad |= v.x != v.x || v.y != v.y;
-      const float mn = fmaxf(m, v.x);
-      if (mn != -INFINITY) l = l * fast_exp2(m - mn) + v.y * fast_exp2(v.x - mn);
-      m = mn;
-    }
+// Partials k0 + lane of a row: adds them to the row's maximum and sum, and
+// returns the lane's weight 2^(m - M); *keep is what scales what was added
+// before.  A NaN of a partial (a logit was NaN or +inf) makes *den NaN: the
+// maximum drops it, the sums do not.
+__device__ __forceinline__ float add_norm(const float2* ml, const Parts& s, int k, int* at, float* M,
+                                          float* den, float* keep) {
+  float2 v = make_float2(-INFINITY, 0.f);
+  *at = 0;
+  if (k < s.n) {
+    *at = part_row(s, k);
+    v = __ldcg(ml + *at);
   }
-  float M = m;
+  float mx = v.x;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  l = m == -INFINITY ? 0.f : l * fast_exp2(m - M);
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  const float Mn = fmaxf(*M, mx), base = Mn == -INFINITY ? 0.f : Mn;
+  *keep = fast_exp2(*M - base);
+  const float w = fast_exp2(v.x - base);
+  float l = w * v.y;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  if (__any_sync(0xffffffffu, bad)) {
-    M = fmaxf(M, 0.f);
-    l = __int_as_float(0x7fffffff);
-  }
-  *den = l;
-  return M;
+  *den = *den * *keep + l;
+  *M = Mn;
+  return w;
 }
 
 // The first CTAs merge the partials: o = sum 2^(m - M) O / sum 2^(m - M) l and
 // lse = M + log2 of the denominator, kMergeWarps / split rows a CTA, split
 // warps sharing a row's partials (few rows have many).  The others add the
-// weights of kScoreKeys own keys of a (sequence, group), from their logits and
-// the normalisers of the rows, which each finds for itself: that is a few
-// hundred cached loads, against a launch more and its wait.
+// weights of ``keys`` own keys of a (sequence, group), from their logits and
+// the normalisers of the rows, which each finds for itself: a few hundred
+// cached loads, against one launch more and its wait.
 template <int D>
 __global__ void __launch_bounds__(kMergeWarps * 32)
-    prefix_finish_kernel(const __grid_constant__ PrefixParams p, int merge_ctas, int split) {
+    prefix_finish_kernel(const __grid_constant__ PrefixParams p, int merge_ctas, int split, int keys) {
   constexpr int V = D / 32;
-  __shared__ float part[kMergeWarps][D];
+  __shared__ __align__(16) float buf[kMergeWarps * 128];   // merge: D a warp; scores: 4 a thread
   __shared__ float norm[128];
-  griddep_wait();
-  griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (static_cast<int>(blockIdx.x) < merge_ctas) {
     const int sub = warp % split;
     const long long row = (static_cast<long long>(blockIdx.x) * kMergeWarps + warp) / split;
     const bool in = row < static_cast<long long>(p.B) * p.T * p.H;
+    const int tok = in ? static_cast<int>(row / p.H) : 0, h = in ? static_cast<int>(row % p.H) : 0;
+    const int b = tok / p.T, len = own_len(p, b);
+    griddep_wait();
+    griddep_launch_dependents();
     float acc[V];
 #pragma unroll
     for (int y = 0; y < V; ++y) acc[y] = 0.f;
     float M = -INFINITY, den = 0.f;
-    if (in) {
-      const int tok = static_cast<int>(row / p.H), h = static_cast<int>(row - static_cast<long long>(tok) * p.H);
-      const RowParts s = row_parts(p, tok, h);
-      M = row_norm(p, s, &den);
 #pragma unroll 1
-      for (int own = 0; own < 2; ++own) {
-        const float* po = own ? p.o_s : p.o_p;
-        const float2* ml = own ? p.ml_s : p.ml_p;
-        constexpr int U = 8;         // partial rows in flight
+    for (int own = 0; own < 2; ++own) {
+      const Parts s = parts_of(p, own != 0, tok, b, h, len);
+      const float* po = (own ? p.o_s : p.o_p) + lane * V;
 #pragma unroll 1
-        for (int k0 = sub; k0 < s.n[own]; k0 += U * split) {
-          float w[U], x[U][V];
+      for (int k0 = 0; k0 < s.n; k0 += 32) {
+        int at;
+        float keep;
+        const float w = add_norm(own ? p.ml_s : p.ml_p, s, k0 + lane, &at, &M, &den, &keep);
+#pragma unroll
+        for (int y = 0; y < V; ++y) acc[y] *= keep;
+        // a partial of weight 0 may never have been written
+        unsigned todo = __ballot_sync(0xffffffffu, w > 0.f && (lane & (split - 1)) == sub);
+        while (todo) {
+          constexpr int U = 8;         // partial rows in flight
+          float x[U][V], wk[U];
 #pragma unroll
           for (int u = 0; u < U; ++u) {
-            const int k = k0 + u * split;
-            w[u] = 0.f;
+            const int src = todo ? __ffs(todo) - 1 : 0;
+            wk[u] = __shfl_sync(0xffffffffu, w, src);
+            const int a = __shfl_sync(0xffffffffu, at, src);
+            if (todo) {
+              const float* f = po + static_cast<long long>(a) * D;
+              if constexpr (V == 4)
+                *reinterpret_cast<float4*>(x[u]) = __ldcg(reinterpret_cast<const float4*>(f));
+              else
+                *reinterpret_cast<float2*>(x[u]) = __ldcg(reinterpret_cast<const float2*>(f));
+            } else {
+              wk[u] = 0.f;
 #pragma unroll
-            for (int y = 0; y < V; ++y) x[u][y] = 0.f;
-            if (k < s.n[own]) {
-              const long long at = part_row(p, s, own, k);
-              const float mk = __ldcg(&ml[at].x);
-              if (mk != -INFINITY) {     // else its output was never written
-                const float* f = po + at * D + lane * V;
-                if constexpr (V == 4)
-                  *reinterpret_cast<float4*>(x[u]) = __ldcg(reinterpret_cast<const float4*>(f));
-                else
-                  *reinterpret_cast<float2*>(x[u]) = __ldcg(reinterpret_cast<const float2*>(f));
-                w[u] = fast_exp2(mk - M);
-              }
+              for (int y = 0; y < V; ++y) x[u][y] = 0.f;
             }
+            todo &= todo - 1;
           }
 #pragma unroll
           for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int y = 0; y < V; ++y) acc[y] = fmaf(w[u], x[u][y], acc[y]);
+            for (int y = 0; y < V; ++y) acc[y] = fmaf(wk[u], x[u][y], acc[y]);
         }
       }
     }
     if (split > 1) {
 #pragma unroll
-      for (int y = 0; y < V; ++y) part[warp][lane * V + y] = acc[y];
+      for (int y = 0; y < V; ++y) buf[warp * D + lane * V + y] = acc[y];
       __syncthreads();
       if (sub != 0) return;
+#pragma unroll 1
       for (int u = 1; u < split; ++u)
 #pragma unroll
-        for (int y = 0; y < V; ++y) acc[y] += part[warp + u][lane * V + y];
+        for (int y = 0; y < V; ++y) acc[y] += buf[(warp + u) * D + lane * V + y];
     }
     if (!in) return;
-    const float inv = M == -INFINITY ? 0.f : 1.f / den;
+    const bool none = M == -INFINITY && den == 0.f;
+    const float inv = none ? 0.f : 1.f / den;
     uint16_t* out = p.o + row * D + lane * V;
     if constexpr (V == 4)
       *reinterpret_cast<uint2*>(out) =
           make_uint2(pack2(acc[0] * inv, acc[1] * inv), pack2(acc[2] * inv, acc[3] * inv));
     else
       *reinterpret_cast<uint32_t*>(out) = pack2(acc[0] * inv, acc[1] * inv);
-    if (lane == 0 && p.lse) p.lse[row] = M == -INFINITY ? -INFINITY : (M + log2f(den)) / kLog2e;
+    if (lane == 0 && p.lse) p.lse[row] = none ? -INFINITY : (M + log2f(den)) / kLog2e;
     return;
   }
+  // a thread: four keys, and one of 4 * 256 / keys shares of the rows
   const int id = static_cast<int>(blockIdx.x) - merge_ctas;
-  const int chunks = (p.C + kScoreKeys - 1) / kScoreKeys;
+  const int chunks = (p.C + keys - 1) / keys;
   const int bg = id / chunks, b = bg / p.G, g = bg - b * p.G;
-  const int len = own_len(p, b), x0 = (id - bg * chunks) * kScoreKeys;
+  const int len = own_len(p, b), x0 = (id - bg * chunks) * keys;
+  griddep_wait();
+  griddep_launch_dependents();
   if (x0 >= len) return;
+#pragma unroll 1
   for (int i = warp; i < p.rows_s; i += kMergeWarps) {
     const int t = i / p.r;
-    float den;
-    const float M = row_norm(p, row_parts(p, b * p.T + t, g * p.r + i - t * p.r), &den);
+    float M = -INFINITY, den = 0.f, keep;
+    int at;
+#pragma unroll 1
+    for (int own = 0; own < 2; ++own) {
+      const Parts s = parts_of(p, own != 0, b * p.T + t, b, g * p.r + i - t * p.r, len);
+#pragma unroll 1
+      for (int k0 = 0; k0 < s.n; k0 += 32)
+        add_norm(own ? p.ml_s : p.ml_p, s, k0 + lane, &at, &M, &den, &keep);
+    }
     // a row that sees no key has logits of -inf alone
-    if (lane == 0) norm[i] = M == -INFINITY ? 0.f : M + log2f(den);
+    if (lane == 0) norm[i] = M == -INFINITY && den == 0.f ? 0.f : M + log2f(den);
   }
   __syncthreads();
-  const long long stride = static_cast<long long>(p.nb) * 128;
-  const int x = x0 + 4 * static_cast<int>(threadIdx.x);
-  if (x >= len) return;
-  const float* s = p.logits + static_cast<long long>(bg) * p.rows_s * stride + x;
-  float w[4] = {0.f, 0.f, 0.f, 0.f};
+  const int quads = keys / 4, share = static_cast<int>(threadIdx.x) / quads;
+  const int shares = kMergeWarps * 32 / quads, quad = static_cast<int>(threadIdx.x) - share * quads;
+  const int x = x0 + 4 * quad;
+  float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (x < len) {
+    const size_t stride = static_cast<size_t>(p.nb) * 128;
+    const float* s = p.logits + static_cast<size_t>(bg) * p.rows_s * stride + x;
 #pragma unroll 8
-  for (int i = 0; i < p.rows_s; ++i) {
-    const float4 v = __ldcg(reinterpret_cast<const float4*>(s + i * stride));
-    w[0] += fast_exp2(v.x - norm[i]);
-    w[1] += fast_exp2(v.y - norm[i]);
-    w[2] += fast_exp2(v.z - norm[i]);
-    w[3] += fast_exp2(v.w - norm[i]);
+    for (int i = share; i < p.rows_s; i += shares) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(s + i * stride));
+      const float n = norm[i];
+      w.x += fast_exp2(v.x - n);
+      w.y += fast_exp2(v.y - n);
+      w.z += fast_exp2(v.z - n);
+      w.w += fast_exp2(v.w - n);
+    }
+  }
+  if (shares > 1) {
+    float4* sums = reinterpret_cast<float4*>(buf);
+    if (share > 0) sums[threadIdx.x - quads] = w;
+    __syncthreads();
+    if (share > 0) return;
+    for (int u = 0; u + 1 < shares; ++u) {
+      const float4 v = sums[u * quads + quad];
+      w.x += v.x;
+      w.y += v.y;
+      w.z += v.z;
+      w.w += v.w;
+    }
   }
   const long long at = static_cast<long long>(bg) * p.C + x;
+  const float we[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int e = 0; e < 4; ++e)      // rows of C elements need not be 16-byte aligned
-    if (x + e < len) p.w_out[at + e] = (p.w_in ? p.w_in[at + e] : 0.f) + w[e];
+    if (x + e < len) p.w_out[at + e] = (p.w_in ? p.w_in[at + e] : 0.f) + we[e];
 }
 
 // Workspace layout.
@@ -1187,11 +1208,13 @@ cudaError_t launch(const msa_shape& s, const PrefixDecodeArgs& a, const PrefixPa
   int split = 1;
   while (split < kMergeWarps && all * split < 16ll * grid) split *= 2;
   const int64_t merge = ceil_div(all * split, kMergeWarps);
-  const int64_t score = p.w_out ? static_cast<int64_t>(p.B) * p.G * ceil_div(p.C, kScoreKeys) : 0;
+  // keys of a scoring CTA: short caches have fewer, their rows shared by 4 threads
+  const int keys = p.C <= 1024 ? 256 : 1024;
+  const int64_t score = p.w_out ? static_cast<int64_t>(p.B) * p.G * ceil_div(p.C, keys) : 0;
   if (merge + score >= (1ll << 31)) return cudaErrorInvalidValue;
   ProfScope ps_("prefix_finish", st);
   return launch_dependent(prefix_finish_kernel<D>, dim3(static_cast<unsigned>(merge + score)),
-                          dim3(kMergeWarps * 32), 0, st, p, static_cast<int>(merge), split);
+                          dim3(kMergeWarps * 32), 0, st, p, static_cast<int>(merge), split, keys);
 }
 
 }  // namespace
