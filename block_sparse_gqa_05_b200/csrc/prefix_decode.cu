@@ -52,7 +52,7 @@ constexpr float kRescaleLog2 = 8.f;   // a row's reference follows its maximum w
 
 // Cost of a block on the line, in some 500 clocks: of a pair, of a spread tile, of
 // another single tile; and of a segment.
-constexpr int kCostPair = 7, kCostSpread = 5, kCostSingle = 8, kCostSegment = 2;
+constexpr int kCostPair = 7, kCostSpread = 5, kCostSingle = 8, kCostSegment = 2, kCostPairSegment = 14;
 constexpr int kCostMost = 8;
 
 struct PrefixParams {
@@ -164,7 +164,7 @@ struct Walk {
         q.rows = p.Np;
         nb = p.nbp;
         w = pair ? kCostPair : single_cost(p, false, nb);
-        pos += nb * w + kCostSegment;
+        pos += nb * w + (pair ? kCostPairSegment : kCostSegment);
         ++s;
       } else {
         if (b < p.B && len < 0) len = own_len(p, b);
@@ -979,9 +979,9 @@ __device__ __forceinline__ float add_norm(const float2* ml, const Parts& s, int 
   return w;
 }
 
-// The first CTAs merge the partials: o = sum 2^(m - M) O / sum 2^(m - M) l and
+// The last CTAs merge the partials: o = sum 2^(m - M) O / sum 2^(m - M) l and
 // lse = M + log2 of the denominator, kMergeWarps / split rows a CTA, split
-// warps sharing a row's partials (few rows have many).  The others add the
+// warps sharing a row's partials (few rows have many).  The first add the
 // weights of ``keys`` own keys of a (sequence, group), from their logits and
 // the normalisers of the rows, which each finds for itself: a few hundred
 // cached loads, against one launch more and its wait.
@@ -992,9 +992,10 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   __shared__ __align__(16) float buf[kMergeWarps * 128];   // merge: D a warp; scores: 4 a thread
   __shared__ float norm[128];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (static_cast<int>(blockIdx.x) < merge_ctas) {
+  const int score_ctas = static_cast<int>(gridDim.x) - merge_ctas;
+  if (static_cast<int>(blockIdx.x) >= score_ctas) {
     const int sub = warp % split;
-    const long long row = (static_cast<long long>(blockIdx.x) * kMergeWarps + warp) / split;
+    const long long row = (static_cast<long long>(blockIdx.x - score_ctas) * kMergeWarps + warp) / split;
     const bool in = row < static_cast<long long>(p.B) * p.T * p.H;
     const int tok = in ? static_cast<int>(row / p.H) : 0, h = in ? static_cast<int>(row % p.H) : 0;
     const int b = tok / p.T, len = own_len(p, b);
@@ -1068,27 +1069,47 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     return;
   }
   // a thread: four keys, and one of 4 * 256 / keys shares of the rows
-  const int id = static_cast<int>(blockIdx.x) - merge_ctas;
+  const int id = static_cast<int>(blockIdx.x);
   const int chunks = (p.C + keys - 1) / keys;
   const int bg = id / chunks, b = bg / p.G, g = bg - b * p.G;
   const int len = own_len(p, b), x0 = (id - bg * chunks) * keys;
   griddep_wait();
   griddep_launch_dependents();
   if (x0 >= len) return;
+  // normalisers: a lane per row, the warps share its partials
 #pragma unroll 1
-  for (int i = warp; i < p.rows_s; i += kMergeWarps) {
-    const int t = i / p.r;
-    float M = -INFINITY, den = 0.f, keep;
-    int at;
+  for (int i0 = 0; i0 < p.rows_s; i0 += 32) {
+    const int i = i0 + lane, t = i / p.r;
+    float M = -INFINITY, den = 0.f;
+    if (i < p.rows_s) {
 #pragma unroll 1
-    for (int own = 0; own < 2; ++own) {
-      const Parts s = parts_of(p, own != 0, b * p.T + t, b, g * p.r + i - t * p.r, len);
-#pragma unroll 1
-      for (int k0 = 0; k0 < s.n; k0 += 32)
-        add_norm(own ? p.ml_s : p.ml_p, s, k0 + lane, &at, &M, &den, &keep);
+      for (int own = 0; own < 2; ++own) {
+        const Parts s = parts_of(p, own != 0, b * p.T + t, b, g * p.r + i - t * p.r, len);
+        const float2* ml = own ? p.ml_s : p.ml_p;
+#pragma unroll 4
+        for (int k = warp; k < s.n; k += kMergeWarps) {
+          const float2 v = __ldcg(ml + part_row(s, k));
+          const float Mn = fmaxf(M, v.x), base = Mn == -INFINITY ? 0.f : Mn;
+          den = den * fast_exp2(M - base) + fast_exp2(v.x - base) * v.y;
+          M = Mn;
+        }
+      }
     }
-    // a row that sees no key has logits of -inf alone
-    if (lane == 0) norm[i] = M == -INFINITY && den == 0.f ? 0.f : M + log2f(den);
+    __syncthreads();
+    buf[warp * 64 + lane] = M;
+    buf[warp * 64 + 32 + lane] = den;
+    __syncthreads();
+    if (warp == 0 && i < p.rows_s) {
+      M = -INFINITY;
+      den = 0.f;
+#pragma unroll
+      for (int u = 0; u < kMergeWarps; ++u) M = fmaxf(M, buf[u * 64 + lane]);
+      const float base = M == -INFINITY ? 0.f : M;
+#pragma unroll
+      for (int u = 0; u < kMergeWarps; ++u) den += buf[u * 64 + 32 + lane] * fast_exp2(buf[u * 64 + lane] - base);
+      // a row that sees no key has logits of -inf alone
+      norm[i] = M == -INFINITY && den == 0.f ? 0.f : M + log2f(den);
+    }
   }
   __syncthreads();
   const int quads = keys / 4, share = static_cast<int>(threadIdx.x) / quads;
@@ -1224,7 +1245,7 @@ bool prefix_decode_supported(const msa_shape& s, int prefix_len) {
   const int64_t r = s.n_q_heads / s.n_kv_heads, rows = static_cast<int64_t>(s.batch) * s.seq_q * r;
   const int64_t bg = static_cast<int64_t>(s.batch) * s.n_kv_heads;
   const int64_t nsp = ceil_div(ceil_div(rows, 128), 2) * s.n_kv_heads;
-  const int64_t line = nsp * (ceil_div(prefix_len, 128) * kCostMost + kCostSegment) +
+  const int64_t line = nsp * (ceil_div(prefix_len, 128) * kCostMost + kCostPairSegment) +
                        bg * (ceil_div(s.seq_kv, 128) * kCostMost + kCostSegment);
   const int64_t parts = std::max(2 * (nsp + kMaxGrid) * 128, 2 * (bg + kMaxGrid) * std::max<int64_t>(s.seq_q * r, 64));
   return line < (1ll << 31) && parts < (1ll << 31);
@@ -1275,7 +1296,7 @@ cudaError_t launch_prefix_decode(const msa_shape& s, const PrefixDecodeArgs& a, 
   p.spread_s = p.rows_s <= static_cast<int>(kSpreadOwn);
   p.two_q = p.rows_s <= 64;
   p.q_stage = (p.spread_s ? 16 : p.rows_s <= 32 ? 32 : 64) * 128;
-  p.cost_pair = p.nbp * kCostPair + kCostSegment;
+  p.cost_pair = p.nbp * kCostPair + kCostPairSegment;
   const int single = p.spread_p && p.nbp >= kSpreadBlocks ? kCostSpread : kCostSingle;
   p.cost_group = (p.npt - 1) * p.cost_pair + ((p.ntile & 1) ? p.nbp * single + kCostSegment : p.cost_pair);
   p.cost_prefix = p.Np > 0 ? p.cost_group * p.G : 0;
