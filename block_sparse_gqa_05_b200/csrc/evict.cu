@@ -10,13 +10,16 @@
 // weights and positions, and by latency.
 //
 // A cluster of CTAs shares one (sequence, group), each with a contiguous slice
-// of its rows in shared memory when they fit.  The n-th largest key is found
+// of its rows, whose keys it keeps in shared memory when they fit (4 bytes a
+// row: two CTAs an SM up to some 20,000 rows).  The n-th largest key is found
 // digit by digit (11, 11 and 10 bits) from histograms in shared memory that
 // every CTA of the cluster reads over distributed shared memory: three passes
-// over the slice whatever the values, no order of atomics can change the
-// result.  Each warp then owns a contiguous run of rows, counts, and writes
-// the lists of holes and movers at ranks that follow from the counts of the
-// warps and CTAs before it.
+// over the slice whatever the values, and no order of atomics can change the
+// result.  Each warp then owns a contiguous run of rows, counts, and writes the
+// lists of holes and movers at ranks that follow from the counts of the warps
+// and CTAs before it.  A lane takes four consecutive rows at a time, two such
+// loads in flight: with one row a lane a slice of 131,072 rows was read at 16
+// GB/s an SM.
 #include <cooperative_groups.h>
 #include <math.h>
 
@@ -34,14 +37,15 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kPer = kBins / kThreads;       // bins a thread sums
-constexpr int kMaxCluster = 8;
-// Most rows a CTA keeps in shared memory (position and key, 8 bytes each).
-constexpr int kMaxStash = 24576;
+constexpr int kMaxCluster = 16;              // past the portable 8: long rows of few sequences
+constexpr int kStep = 128;                   // rows a warp takes at a time, four a lane
+// Most rows whose keys a CTA keeps in shared memory.
+constexpr int kMaxStash = 49152;
 // Most rows a CTA moves itself; past it a second kernel moves them with the
 // whole GPU (one launch more, against one CTA's share of the bandwidth).
-constexpr int kMaxFusedMoves = 512;
+constexpr int kMaxFusedMoves = 128;
 constexpr int kMoveThreads = 256;
-constexpr int kMoveRows = 64;                // rows of a CTA of the second kernel
+constexpr int kMoveRows = 256;                // rows of a CTA of the second kernel
 
 // A moved row: where it came from, and its weight and position.
 struct __align__(16) Mover {
@@ -92,63 +96,86 @@ __device__ __forceinline__ long long row_at(const EvictParams& p, int b, int g, 
 }
 
 // Moves pairs first, first + step, ... < n of (b, g): a warp takes 32 / (d / 4)
-// rows at a time, 16 bytes of K or V a lane, four pairs of loads in flight.
+// rows at a time, 16 bytes of K or V a lane, kMoveDeep of them in flight.
+constexpr int kMoveDeep = 4;
 __device__ __forceinline__ void move_rows(const EvictParams& p, int bg, int n, int first, int step) {
   const int b = bg / p.G, g = bg - b * p.G;
   const int lane = threadIdx.x & 31;
   const int per = p.d / 4;                     // 16-byte pieces of a row's K and V
   const int at_once = 32 / per, sub = lane / per, piece = lane - sub * per;
   const bool is_v = piece >= per / 2;
-  uint16_t* cache = is_v ? p.v : p.k;
-  const int off = (is_v ? piece - per / 2 : piece) * 8;
+  uint16_t* cache = (is_v ? p.v : p.k) + (is_v ? piece - per / 2 : piece) * 8;
   const Mover* movers = p.movers + static_cast<long long>(bg) * p.half;
   const int32_t* holes = p.holes + static_cast<long long>(bg) * p.half;
   const long long base = static_cast<long long>(bg) * p.C;
-  constexpr int U = 4;
-  for (int i0 = first * at_once; i0 < n; i0 += step * at_once * U) {
-    uint4 x[U];
-    long long to[U];
+#pragma unroll 1
+  for (int i0 = first * at_once; i0 < n; i0 += step * at_once * kMoveDeep) {
+    int4 mover[kMoveDeep];
+    int hole[kMoveDeep];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * step * at_once + sub;
+    for (int u = 0; u < kMoveDeep; ++u) {
+      const int i = min(i0 + u * step * at_once + sub, n - 1);
+      mover[u] = __ldcg(reinterpret_cast<const int4*>(movers + i));
+      hole[u] = __ldcg(holes + i);
+    }
+    uint4 x[kMoveDeep];
+    long long to[kMoveDeep];
+#pragma unroll
+    for (int u = 0; u < kMoveDeep; ++u) {
       to[u] = -1;
-      if (i < n) {
-        const int4 raw = __ldcg(reinterpret_cast<const int4*>(movers + i));
-        const int hole = __ldcg(holes + i);
+      if (i0 + u * step * at_once + sub < n) {
         if (piece == 0) {
-          p.w_out[base + hole] = __int_as_float(raw.y);
-          p.pos_out[base + hole] = raw.z;
+          p.w_out[base + hole[u]] = __int_as_float(mover[u].y);
+          p.pos_out[base + hole[u]] = mover[u].z;
         }
-        const long long s = row_at(p, b, g, raw.x), t = row_at(p, b, g, hole);
+        const long long s = row_at(p, b, g, mover[u].x), t = row_at(p, b, g, hole[u]);
         if (s >= 0 && t >= 0) {
-          x[u] = *reinterpret_cast<const uint4*>(cache + s + off);
+          x[u] = __ldcs(reinterpret_cast<const uint4*>(cache + s));
           to[u] = t;
         }
       }
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (to[u] >= 0) *reinterpret_cast<uint4*>(cache + to[u] + off) = x[u];
+    for (int u = 0; u < kMoveDeep; ++u)
+      if (to[u] >= 0) *reinterpret_cast<uint4*>(cache + to[u]) = x[u];
   }
 }
 
 // What the CTAs of a cluster tell one another.
 struct __align__(16) Shared {
   uint32_t hist[3][kBins];
+  uint32_t coarse[3][kBins / 32];   // sums of 32 bins
   int top;                // largest position of the slice
   int fixed;              // rows of the slice that always stay
   int counts[4];          // of the slice: above / at the cut, before / past row n
   int wcounts[kWarps][4]; // of its warps
-  int scan[kWarps];
   uint32_t digit;
   int need;
   int red[kWarps];
 };
 
-template <bool STASH>
-__global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams p) {
+// Four consecutive elements from x; of those at or past ``end`` the value is
+// whatever is there (the arrays go on to a multiple of four), or 0.
+template <bool VEC, typename T>
+__device__ __forceinline__ void load4(const T* p, int x, int end, T* v) {
+  if constexpr (VEC) {
+    const int4 q = __ldcg(reinterpret_cast<const int4*>(p + x));
+    const T* t = reinterpret_cast<const T*>(&q);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = t[e];
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = x + e < end ? __ldcg(p + x + e) : T(0);
+  }
+}
+
+// VEC: every row of four starts on a 16-byte boundary in all arrays.
+template <bool STASH, bool VEC>
+__global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constant__ EvictParams p) {
+  // Steps whose loads are in flight together where rows are read from memory
+  constexpr int U = STASH ? 1 : 4;
   __shared__ Shared sh;
-  extern __shared__ __align__(16) uint32_t stash[];
+  extern __shared__ __align__(16) uint32_t s_key[];
   cg::cluster_group cl = cg::this_cluster();
   const int cs = p.cluster, rank = cs > 1 ? static_cast<int>(cl.block_rank()) : 0;
   const int bg = static_cast<int>(blockIdx.x) / cs, b = bg / p.G, g = bg - b * p.G;
@@ -160,7 +187,9 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams p)
       __syncthreads();
   };
   auto of_rank = [&](int r) { return cs > 1 ? cl.map_shared_rank(&sh, r) : &sh; };
-  for (int i = tid; i < 3 * kBins; i += kThreads) (&sh.hist[0][0])[i] = 0;
+#pragma unroll 1
+  for (int i = tid; i < 3 * kBins / 4; i += kThreads)
+    reinterpret_cast<uint4*>(&sh.hist[0][0])[i] = make_uint4(0, 0, 0, 0);
   griddep_wait();
   griddep_launch_dependents();
   int len = __ldg(p.lens + b);
@@ -178,189 +207,258 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams p)
   const int32_t* pos = p.pos_in + base;
   float* wo = p.w_out + base;
   int32_t* po = p.pos_out + base;
-  // this CTA's slice [x0, x1), and each warp's run of it, in whole warps' rows
-  const int slice = ((len + cs - 1) / cs + 31) & ~31;
+  // this CTA's slice [x0, x1), and each warp's run [y0, y1) of it, in whole steps
+  const int slice = ((len + cs - 1) / cs + kStep - 1) / kStep * kStep;
   const int x0 = min(len, rank * slice), x1 = min(len, x0 + slice);
   const bool same_w = wo == w, same_p = po == pos;
   if (n == len) {
+#pragma unroll 1
     for (int x = x0 + tid; x < x1; x += kThreads) {
       if (!same_w) wo[x] = w[x];
       if (!same_p) po[x] = pos[x];
     }
     return;
   }
-  const int run = ((slice + kWarps - 1) / kWarps + 31) & ~31;
+  const int run = (slice / kStep + kWarps - 1) / kWarps * kStep;
   const int y0 = min(x1, x0 + warp * run), y1 = min(x1, y0 + run);
-  int* s_pos = reinterpret_cast<int*>(stash);
-  uint32_t* s_key = stash + slice;
 
-  // largest position
+  // largest position; the weights come nearer meanwhile
   int top = INT32_MIN;
 #pragma unroll 4
-  for (int x = y0 + lane; x < y1; x += 32) {
-    const int q = __ldg(pos + x);
-    top = max(top, q);
-    if (STASH) {
-      s_pos[x - x0] = q;
-      s_key[x - x0] = __float_as_uint(__ldcg(w + x));
-    }
+  for (int x = y0 + 4 * lane; x < y1; x += kStep) {
+    int q[4];
+    load4<VEC>(pos, x, y1, q);
+    if ((lane & 7) == 0) prefetch_l2(w + x);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (x + e < y1) top = max(top, q[e]);
   }
   top = __reduce_max_sync(0xffffffffu, top);
   if (lane == 0) sh.red[warp] = top;
   __syncthreads();
-  if (tid == 0) {
-    for (int i = 0; i < kWarps; ++i) top = max(top, sh.red[i]);
-    sh.top = top;
+  if (warp == 0) {
+    top = __reduce_max_sync(0xffffffffu, lane < kWarps ? sh.red[lane] : INT32_MIN);
+    if (lane == 0) sh.top = top;
   }
   sync_all();
+  top = INT32_MIN;
+#pragma unroll 1
   for (int r = 0; r < cs; ++r) top = max(top, of_rank(r)->top);
 
-  // Key of row x.  By default rows that always stay come before all; when
-  // there are more of them than fit, only they have keys, by weight.
+  // Keys of four rows from x of positions q and weights wx.  By default rows that
+  // always stay come before all; when there are more of them than fit, only
+  // they have keys, by weight.
   bool only_fixed = false;
-  auto make_key = [&](int q, float wx) -> uint32_t {
-    const bool f = stays(p, q, top);
-    if (only_fixed) return f ? weight_key(wx) : 0u;
-    return f ? kStays : weight_key(wx);
-  };
-  auto key_at = [&](int x) -> uint32_t {
-    if (STASH) return s_key[x - x0];
-    return make_key(__ldg(pos + x), __ldcg(w + x));
-  };
-  auto count_bin = [&](uint32_t* hist, bool in, uint32_t bin) {
-    const unsigned m = __ballot_sync(0xffffffffu, in);
-    if (!m) return;
-    const uint32_t lead = __shfl_sync(0xffffffffu, bin, __ffs(m) - 1);
-    // equal keys (rows that no query looked at, ties) would queue up on one bin
-    if (__all_sync(0xffffffffu, !in || bin == lead)) {
-      if (lane == 0) atomicAdd(hist + lead, static_cast<uint32_t>(__popc(m)));
-    } else if (in) {
-      atomicAdd(hist + bin, 1u);
+  auto make_keys = [&](int x, const int* q, const float* wx, uint32_t* key) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const bool f = stays(p, q[e], top);
+      key[e] = only_fixed ? (f ? weight_key(wx[e]) : 0u) : f ? kStays : weight_key(wx[e]);
+      if (x + e >= y1) key[e] = 0u;
     }
   };
-  // Sums bins [tid * kPer, + kPer) over the cluster and finds the bin that holds
-  // the need-th largest key; leaves it in sh.digit and the rank in it in sh.need.
-  auto find_digit = [&](int h, int need) {
-    uint32_t c[kPer];
-    uint32_t mine = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) c[i] = 0;
-    for (int r = 0; r < cs; ++r) {
-      const uint4 v = *reinterpret_cast<const uint4*>(&of_rank(r)->hist[h][tid * kPer]);
-      c[0] += v.x;
-      c[1] += v.y;
-      c[2] += v.z;
-      c[3] += v.w;
+  // Calls f(x, keys, positions, weights) for every step of this warp's rows;
+  // ``fresh``: from memory (positions and weights too), else the keys kept.
+  auto for_rows = [&](bool fresh, auto f) {
+    if (STASH && !fresh) {
+#pragma unroll 1
+      for (int xb = y0; xb < y1; xb += kStep) {
+        const int x = xb + 4 * lane;
+        uint32_t key[4] = {0, 0, 0, 0};
+        if (x < y1) *reinterpret_cast<uint4*>(key) = *reinterpret_cast<const uint4*>(s_key + x - x0);
+        f(x, key, nullptr, nullptr);
+      }
+      return;
     }
+#pragma unroll 1
+    for (int xb = y0; xb < y1; xb += U * kStep) {
+      int q[U][4];
+      float wx[U][4];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) mine += c[i];
-    // keys in higher bins: an exclusive scan from the top
-    uint32_t inc = mine;
+      for (int u = 0; u < U; ++u) {
+        const int x = xb + u * kStep + 4 * lane;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t v = __shfl_down_sync(0xffffffffu, inc, o);
-      if (lane + o < 32) inc += v;
-    }
-    if (lane == 0) sh.scan[warp] = static_cast<int>(inc);
-    __syncthreads();
-    uint32_t above = inc - mine;
-    for (int i = warp + 1; i < kWarps; ++i) above += static_cast<uint32_t>(sh.scan[i]);
-    if (above < static_cast<uint32_t>(need) && above + mine >= static_cast<uint32_t>(need)) {
-#pragma unroll
-      for (int i = kPer - 1; i >= 0; --i) {
-        if (above < static_cast<uint32_t>(need) && above + c[i] >= static_cast<uint32_t>(need)) {
-          sh.digit = static_cast<uint32_t>(tid * kPer + i);
-          sh.need = need - static_cast<int>(above);
+        for (int e = 0; e < 4; ++e) {
+          q[u][e] = 0;
+          wx[u][e] = 0.f;
         }
-        above += c[i];
+        if (x < y1) {
+          load4<VEC>(w, x, y1, wx[u]);
+          load4<VEC>(pos, x, y1, q[u]);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int x = xb + u * kStep + 4 * lane;
+        uint32_t key[4] = {0, 0, 0, 0};
+        if (xb + u * kStep < y1) {                 // the warp's own bound: uniform
+          make_keys(x, q[u], wx[u], key);
+          f(x, key, q[u], wx[u]);
+        }
+      }
+    }
+  };
+  // Counts the bins of four rows a lane where in.  Equal keys (rows that no query
+  // looked at, ties) would queue up on one bin.
+  auto count_bins = [&](uint32_t* hist, const bool* in, const uint32_t* bin) {
+    const bool any = in[0] || in[1] || in[2] || in[3];
+    const unsigned m = __ballot_sync(0xffffffffu, any);
+    if (!m) return;
+    const uint32_t own = in[0] ? bin[0] : in[1] ? bin[1] : in[2] ? bin[2] : bin[3];
+    const uint32_t lead = __shfl_sync(0xffffffffu, own, __ffs(m) - 1);
+    bool same = true;
+    int c = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      same &= !in[e] || bin[e] == lead;
+      c += in[e] ? 1 : 0;
+    }
+    if (__all_sync(0xffffffffu, same)) {
+      c = __reduce_add_sync(0xffffffffu, c);
+      if (lane == 0) atomicAdd(hist + lead, static_cast<uint32_t>(c));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (in[e]) atomicAdd(hist + bin[e], 1u);
+    }
+  };
+  // Makes the histogram's sums of 32 bins and lets the cluster see both.
+  auto show_hist = [&](int h) {
+    __syncthreads();
+    const uint4 v = *reinterpret_cast<const uint4*>(&sh.hist[h][tid * kPer]);
+    uint32_t c = v.x + v.y + v.z + v.w;
+#pragma unroll
+    for (int o = 1; o < 32 / kPer; o <<= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+    if ((lane & (32 / kPer - 1)) == 0) sh.coarse[h][tid / (32 / kPer)] = c;
+    sync_all();
+  };
+  // Finds the bin that holds the need-th largest key over the cluster, first
+  // among the sums of 32 bins and then in one of them; leaves it in sh.digit and
+  // the rank in it in sh.need.  One warp: a few remote loads of each CTA.
+  auto find_digit = [&](int h, int need) {
+    if (warp == 0) {
+      uint32_t c0 = 0, c1 = 0;
+#pragma unroll 4
+      for (int r = 0; r < cs; ++r) {
+        const uint2 v = *reinterpret_cast<const uint2*>(&of_rank(r)->coarse[h][2 * lane]);
+        c0 += v.x;
+        c1 += v.y;
+      }
+      // keys in higher groups: an exclusive scan from the top
+      auto above_of = [&](uint32_t mine) {
+        uint32_t inc = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t v = __shfl_down_sync(0xffffffffu, inc, o);
+          if (lane + o < 32) inc += v;
+        }
+        return inc - mine;
+      };
+      const uint32_t nd = static_cast<uint32_t>(need);
+      uint32_t above = above_of(c0 + c1);
+      const bool in1 = above < nd && above + c1 >= nd;
+      const bool in0 = above + c1 < nd && above + c1 + c0 >= nd;
+      const unsigned who = __ballot_sync(0xffffffffu, in0 || in1);
+      const int src = __ffs(who) - 1;
+      const int group = __shfl_sync(0xffffffffu, 2 * lane + (in1 ? 1 : 0), src);
+      const uint32_t before = __shfl_sync(0xffffffffu, in1 ? above : above + c1, src);
+      uint32_t c = 0;
+#pragma unroll 4
+      for (int r = 0; r < cs; ++r) c += of_rank(r)->hist[h][32 * group + lane];
+      above = before + above_of(c);
+      if (above < nd && above + c >= nd) {
+        sh.digit = static_cast<uint32_t>(32 * group + lane);
+        sh.need = need - static_cast<int>(above);
       }
     }
     __syncthreads();
   };
 
   // first digit, and the number of rows that always stay
+  auto first_digit = [&] {
+    int fixed = 0;
+    for_rows(true, [&](int x, const uint32_t* key, const int*, const float*) {
+      if (STASH && x < y1) *reinterpret_cast<uint4*>(s_key + x - x0) = *reinterpret_cast<const uint4*>(key);
+      bool in[4];
+      uint32_t bin[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        in[e] = x + e < y1;
+        bin[e] = key[e] >> 21;
+        fixed += key[e] == kStays ? 1 : 0;
+      }
+      count_bins(sh.hist[0], in, bin);
+    });
+    return __reduce_add_sync(0xffffffffu, fixed);
+  };
   int fixed = 0;
-#pragma unroll 2
-  for (int xb = y0; xb < y1; xb += 32) {
-    const int x = xb + lane;
-    const bool in = x < y1;
-    uint32_t key = 0;
-    if (in) {
-      key = STASH ? make_key(s_pos[x - x0], __uint_as_float(s_key[x - x0])) : key_at(x);
-      if (STASH) s_key[x - x0] = key;
+#pragma unroll 1
+  for (;;) {                            // a second time when too many rows always stay
+    const int f = first_digit();
+    if (lane == 0) sh.red[warp] = f;
+    __syncthreads();
+    if (warp == 0) {
+      fixed = __reduce_add_sync(0xffffffffu, lane < kWarps ? sh.red[lane] : 0);
+      if (lane == 0) sh.fixed = fixed;
     }
-    fixed += __popc(__ballot_sync(0xffffffffu, in && key == kStays));
-    count_bin(sh.hist[0], in, key >> 21);
-  }
-  if (lane == 0) sh.red[warp] = fixed;
-  __syncthreads();
-  if (tid == 0) {
+    show_hist(0);
+    if (only_fixed) break;
     fixed = 0;
-    for (int i = 0; i < kWarps; ++i) fixed += sh.red[i];
-    sh.fixed = fixed;
-  }
-  sync_all();
-  fixed = 0;
-  for (int r = 0; r < cs; ++r) fixed += of_rank(r)->fixed;
-  if (fixed > n) {
+#pragma unroll 1
+    for (int r = 0; r < cs; ++r) fixed += of_rank(r)->fixed;
+    if (fixed <= n) break;
     only_fixed = true;
-    sync_all();                        // every CTA has read the counts
+    sync_all();                         // every CTA has read the counts
     for (int i = tid; i < kBins; i += kThreads) sh.hist[0][i] = 0;
     __syncthreads();
-    for (int xb = y0; xb < y1; xb += 32) {
-      const int x = xb + lane;
-      const bool in = x < y1;
-      uint32_t key = 0;
-      if (in) {
-        key = make_key(__ldg(pos + x), __ldcg(w + x));
-        if (STASH) s_key[x - x0] = key;
-      }
-      count_bin(sh.hist[0], in, key >> 21);
-    }
-    sync_all();
   }
   find_digit(0, n);
   uint32_t cut = sh.digit << 21;
   int need = sh.need;
-#pragma unroll 2
-  for (int xb = y0; xb < y1; xb += 32) {
-    const int x = xb + lane;
-    const uint32_t key = x < y1 ? key_at(x) : 0u;
-    count_bin(sh.hist[1], x < y1 && (key >> 21) == (cut >> 21), (key >> 10) & 2047u);
+#pragma unroll 1
+  for (int d = 1; d < 3; ++d) {        // the other two digits
+    const int hi = d == 1 ? 21 : 10, lo = d == 1 ? 10 : 0;
+    const uint32_t mask = d == 1 ? 2047u : 1023u;
+    for_rows(false, [&](int x, const uint32_t* key, const int*, const float*) {
+      bool in[4];
+      uint32_t bin[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        in[e] = x + e < y1 && (key[e] >> hi) == (cut >> hi);
+        bin[e] = (key[e] >> lo) & mask;
+      }
+      count_bins(sh.hist[d], in, bin);
+    });
+    show_hist(d);
+    find_digit(d, need);
+    cut |= sh.digit << lo;
+    need = sh.need;
   }
-  sync_all();
-  find_digit(1, need);
-  cut |= sh.digit << 10;
-  need = sh.need;
-#pragma unroll 2
-  for (int xb = y0; xb < y1; xb += 32) {
-    const int x = xb + lane;
-    const uint32_t key = x < y1 ? key_at(x) : 0u;
-    count_bin(sh.hist[2], x < y1 && (key >> 10) == (cut >> 10), key & 1023u);
-  }
-  sync_all();
-  find_digit(2, need);
-  cut |= sh.digit;
-  need = sh.need;                      // rows equal to the cut that stay, the lowest ones
+  // need: rows equal to the cut that stay, the lowest ones
 
   // rows above and at the cut, before and past row n
   int c4[4] = {0, 0, 0, 0};
-#pragma unroll 2
-  for (int xb = y0; xb < y1; xb += 32) {
-    const int x = xb + lane;
-    const uint32_t key = x < y1 ? key_at(x) : 0u;
-    const unsigned gt = __ballot_sync(0xffffffffu, x < y1 && key > cut);
-    const unsigned eq = __ballot_sync(0xffffffffu, x < y1 && key == cut);
-    const unsigned lo = __ballot_sync(0xffffffffu, x < n);
-    c4[0] += __popc(gt & lo);
-    c4[1] += __popc(eq & lo);
-    c4[2] += __popc(gt & ~lo);
-    c4[3] += __popc(eq & ~lo);
+  for_rows(false, [&](int x, const uint32_t* key, const int*, const float*) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const bool in = x + e < y1;
+      const int hi = x + e < n ? 0 : 2;
+      const bool gt = in && key[e] > cut, eq = in && key[e] == cut;
+      c4[0] += hi == 0 && gt ? 1 : 0;
+      c4[1] += hi == 0 && eq ? 1 : 0;
+      c4[2] += hi == 2 && gt ? 1 : 0;
+      c4[3] += hi == 2 && eq ? 1 : 0;
+    }
+  });
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    c4[e] = __reduce_add_sync(0xffffffffu, c4[e]);
+    if (lane == 0) sh.wcounts[warp][e] = c4[e];
   }
-  if (lane < 4) sh.wcounts[warp][lane] = lane == 0 ? c4[0] : lane == 1 ? c4[1] : lane == 2 ? c4[2] : c4[3];
   __syncthreads();
   if (tid < 4) {
     int s = 0;
+#pragma unroll 1
     for (int i = 0; i < kWarps; ++i) s += sh.wcounts[i][tid];
     sh.counts[tid] = s;
   }
@@ -376,6 +474,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams p)
   auto rows_before_n = [&](int a, int z) { return max(0, min(z, n) - min(a, n)); };
   {
     int e = 0, hl = 0, mv = 0;
+#pragma unroll 1
     for (int r = 0; r < cs; ++r) {
       if (r == rank) {
         eq_at = e;
@@ -390,6 +489,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams p)
     }
     moves = mv;
   }
+#pragma unroll 1
   for (int i = 0; i < warp; ++i) {
     const int a = min(x1, x0 + i * run);
     add_run(sh.wcounts[i], rows_before_n(a, min(x1, a + run)), eq_at, hole_at, move_at);
@@ -397,36 +497,63 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams p)
   Mover* movers = p.movers + static_cast<long long>(bg) * p.half;
   int32_t* holes = p.holes + static_cast<long long>(bg) * p.half;
   const unsigned below = (1u << lane) - 1u;
-#pragma unroll 2
-  for (int xb = y0; xb < y1; xb += 32) {
-    const int x = xb + lane;
-    const bool in = x < y1;
-    const uint32_t key = in ? key_at(x) : 0u;
-    const unsigned eq = __ballot_sync(0xffffffffu, in && key == cut);
-    const bool keep = in && (key > cut || (key == cut && eq_at + __popc(eq & below) < need));
-    eq_at += __popc(eq);
-    const bool lo = x < n;
-    const unsigned hl = __ballot_sync(0xffffffffu, in && lo && !keep);
-    const unsigned mv = __ballot_sync(0xffffffffu, keep && !lo);
-    if (in) {
-      if (lo) {
-        if (keep) {
-          if (!same_w) wo[x] = __ldcg(w + x);
-          if (!same_p) po[x] = STASH ? s_pos[x - x0] : __ldg(pos + x);
-        } else {
-          holes[hole_at + __popc(hl & below)] = x;
+  // rank of this lane's first such row among the warp's, and their number
+  auto rank4 = [&](const bool* f, int* count) {
+    int before = 0, all = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const unsigned m = __ballot_sync(0xffffffffu, f[e]);
+      before += __popc(m & below);
+      all += __popc(m);
+    }
+    *count = all;
+    return before;
+  };
+  for_rows(true, [&](int x, const uint32_t* key, int* q, float* wx) {
+    bool eq[4], keep[4], hole[4], move[4];
+    int count;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) eq[e] = x + e < y1 && key[e] == cut;
+    int re = eq_at + rank4(eq, &count);
+    eq_at += count;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const bool in = x + e < y1, lo = x + e < n;
+      keep[e] = in && (key[e] > cut || (eq[e] && re < need));
+      re += eq[e] ? 1 : 0;
+      hole[e] = in && lo && !keep[e];
+      move[e] = keep[e] && !lo;
+    }
+    int rh = hole_at + rank4(hole, &count);
+    hole_at += count;
+    int rm = move_at + rank4(move, &count);
+    move_at += count;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (hole[e]) holes[rh++] = x + e;
+      if (move[e]) movers[rm++] = Mover{x + e, wx[e], q[e], 0};
+    }
+    // what the rows show afterwards; a hole gets its mover's with the row
+    if (x + 3 < min(n, y1) ? !(same_w && same_p) : x < y1) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (x + e >= n) {
+          wx[e] = 0.f;
+          q[e] = -1;
         }
+      if (VEC && x + 4 <= y1) {
+        *reinterpret_cast<float4*>(wo + x) = make_float4(wx[0], wx[1], wx[2], wx[3]);
+        *reinterpret_cast<int4*>(po + x) = make_int4(q[0], q[1], q[2], q[3]);
       } else {
-        if (keep)
-          movers[move_at + __popc(mv & below)] =
-              Mover{x, __ldcg(w + x), STASH ? s_pos[x - x0] : pos[x], 0};
-        wo[x] = 0.f;
-        po[x] = -1;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (x + e < y1) {
+            wo[x + e] = wx[e];
+            po[x + e] = q[e];
+          }
       }
     }
-    hole_at += __popc(hl);
-    move_at += __popc(mv);
-  }
+  });
   if (!p.fused) {
     if (rank == 0 && tid == 0) p.n_moves[bg] = moves;
     if (cs > 1) cl.sync();             // no CTA leaves while another reads its counts
@@ -438,7 +565,8 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const EvictParams p)
 }
 
 // The moves of all (sequence, group)s, kMoveRows a CTA.
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p) {
+__global__ void __launch_bounds__(kMoveThreads)
+    evict_move_kernel(const __grid_constant__ EvictParams p) {
   griddep_wait();
   griddep_launch_dependents();
   const int bg = blockIdx.x;
@@ -469,7 +597,7 @@ EvictWs ws_layout(const msa_shape& s) {
   return w;
 }
 
-cudaError_t launch_clustered(void (*kernel)(const EvictParams), unsigned grid, int cluster,
+cudaError_t launch_clustered(void (*kernel)(EvictParams), unsigned grid, int cluster,
                              size_t smem, cudaStream_t st, const EvictParams& p) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
@@ -520,27 +648,31 @@ cudaError_t launch_cache_evict(const msa_shape& s, const EvictArgs& a, void* ws,
   p.n_first = a.n_first;
   p.n_recent = a.n_recent;
   p.half = static_cast<int>(lists_half(s));
-  // CTAs of a cluster: enough to fill the GPU twice, not below 1024 rows each
+  // CTAs of a cluster: as many as run at once (two an SM), not below 1024 rows each
   const int64_t bg = static_cast<int64_t>(s.batch) * s.n_kv_heads;
   p.cluster = 1;
-  while (p.cluster < kMaxCluster && bg * p.cluster < 2ll * ctx->num_sms &&
+  while (p.cluster < kMaxCluster && 2 * bg * p.cluster <= 2ll * ctx->num_sms &&
          p.C / (2 * p.cluster) >= 1024)
     p.cluster *= 2;
   const int64_t most = std::min<int64_t>(a.budget, std::max(p.C - a.budget, 0));   // moves there can be
   p.fused = most <= static_cast<int64_t>(kMaxFusedMoves) * p.cluster;
-  const int64_t slice = align_up(static_cast<size_t>(ceil_div(p.C, p.cluster)), 32);
+  const int64_t slice = align_up(static_cast<size_t>(ceil_div(p.C, p.cluster)), kStep);
   const bool stash = slice <= kMaxStash;
-  const size_t smem = stash ? static_cast<size_t>(slice) * 8 : 0;
+  auto vec16 = [](const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15u) == 0; };
+  const bool vec = p.C % 4 == 0 && vec16(p.w_in) && vec16(p.pos_in) && vec16(p.w_out) && vec16(p.pos_out);
+  const size_t smem = stash ? static_cast<size_t>(slice) * 4 : 0;
   const unsigned grid = static_cast<unsigned>(bg * p.cluster);
+  auto kernel = stash ? (vec ? evict_kernel<true, true> : evict_kernel<true, false>)
+                      : (vec ? evict_kernel<false, true> : evict_kernel<false, false>);
   cudaError_t e = cudaSuccess;
   if (stash)
-    e = cudaFuncSetAttribute(evict_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kMaxStash * 8);
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxStash * 4);
+  if (e == cudaSuccess && p.cluster > 8)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   {
     ProfScope ps_("cache_evict", st);
-    e = launch_clustered(stash ? evict_kernel<true> : evict_kernel<false>, grid, p.cluster, smem, st,
-                         p);
+    e = launch_clustered(kernel, grid, p.cluster, smem, st, p);
   }
   if (e != cudaSuccess || p.fused) return e;
   {
