@@ -9,6 +9,7 @@ import-time loader raises instead of falling back to anything else.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 
@@ -128,7 +129,7 @@ def _ptr(t):
         raise ValueError("libmsa takes CUDA tensors")
     if not t.is_contiguous():
         raise ValueError("libmsa takes contiguous tensors")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _sizes(shape: Shape, pages: int = 0, prefix: int = 0) -> dict:
@@ -149,10 +150,18 @@ def _sizes(shape: Shape, pages: int = 0, prefix: int = 0) -> dict:
             "prefix_pages": (i32, (prefix + 127) // 128)}
 
 
+@functools.lru_cache(maxsize=64)
+def _sizes_of(fields: bytes, pages: int, prefix: int) -> dict:
+    """_sizes of the shape with these fields: a decode loop calls with one or two
+    shapes, and building the table took longer than checking the tensors."""
+    return _sizes(Shape.from_buffer_copy(fields), pages, prefix)
+
+
 def _args(shape: Shape, pages: int = 0, prefix: int = 0, **tensors) -> dict:
     """Device pointers of the named tensors after checking each one's dtype and
-    that it holds at least the elements its layout needs (None stays None)."""
-    need = _sizes(shape, pages, prefix)
+    that it holds at least the elements its layout needs (None stays None), in
+    the order given."""
+    need = _sizes_of(bytes(shape), pages, prefix)
     out = {}
     for name, t in tensors.items():
         if t is not None:
@@ -172,7 +181,7 @@ def _ws(ws):
 
 def _stream(stream):
     s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    return s.cuda_stream
 
 
 def _check(status: int, what: str):
@@ -374,11 +383,11 @@ def dense_attn_decode(shape: Shape, q, k, v, o=None, lse=None, ws=None, want_lse
     return o, lse
 
 
-def _one_device(*tensors):
+def _one_device(first, *others):
     """The device all given tensors are on (raises when there are several)."""
-    dev = tensors[0].device
-    for t in tensors[1:]:
-        if t is not None and t.device != dev:
+    index, dev = first.get_device(), first.device
+    for t in others:
+        if t is not None and (t.get_device() != index or index < 0 and t.device != dev):
             raise ValueError(f"libmsa takes tensors of one device, got {dev} and {t.device}")
     return dev
 
@@ -396,22 +405,22 @@ def _call(name, dev, stream, fresh, *args):
     _check(getattr(lib(), name)(*args, _stream(stream)), name)
 
 
-def _prefix_decode(name, shape, q, seq_lens, o, lse, weights, weights_out, ws, want_lse, stream,
-                   caches, lead, order, pages, prefix):
+def _prefix_decode(name, shape, lead, inputs, o, lse, weights, weights_out, ws, want_lse, stream,
+                   pages, prefix):
     """The common part of the two calls: ``lead`` the integers after the shape,
-    ``order`` the C order of the named pointers."""
+    ``inputs`` the tensors before the output, in the C order."""
     if weights_out is None:
         weights_out = weights
-    given = (o, lse, ws)
+    q, given = inputs["q"], (o, lse, ws)
     o, lse = _attn_out(shape, q, o, lse, want_lse)
     if ws is None:
         ws = alloc_workspace(shape, OP_PREFIX_DECODE if weights_out is None
                              else OP_PREFIX_DECODE_WEIGHTS, q.device)
     fresh = [t for t, had in zip((o, lse, ws), given) if had is None and t is not None]
-    dev = _one_device(q, seq_lens, o, lse, weights, weights_out, ws, *caches.values())
-    a = _args(shape, pages, prefix, q=q, seq_lens=seq_lens, o=o, lse=lse, weights=weights,
-              weights_out=weights_out, **caches)
-    _call(name, dev, stream, fresh, ctypes.byref(shape), *lead, *[a[n] for n in order], *_ws(ws))
+    dev = _one_device(q, *inputs.values(), o, lse, weights, weights_out, ws)
+    a = _args(shape, pages, prefix, **inputs, o=o, lse=lse, weights=weights,
+              weights_out=weights_out)
+    _call(name, dev, stream, fresh, ctypes.byref(shape), *lead, *a.values(), *_ws(ws))
     return o, lse, weights_out
 
 
@@ -428,11 +437,9 @@ def prefix_attn_decode(shape: Shape, q, k, v, seq_lens, k_prefix=None, v_prefix=
     weights_out)."""
     cap = 0 if k_prefix is None else int(k_prefix.shape[-2])
     n = cap if prefix_len is None else int(prefix_len)
-    return _prefix_decode("msa_prefix_attn_decode", shape, q, seq_lens, o, lse, weights,
-                          weights_out, ws, want_lse, stream,
-                          dict(k_prefix=k_prefix, v_prefix=v_prefix, k=k, v=v), (n, cap),
-                          ("seq_lens", "q", "k_prefix", "v_prefix", "k", "v", "o", "lse",
-                           "weights", "weights_out"), 0, cap)
+    return _prefix_decode("msa_prefix_attn_decode", shape, (n, cap),
+                          dict(seq_lens=seq_lens, q=q, k_prefix=k_prefix, v_prefix=v_prefix, k=k,
+                               v=v), o, lse, weights, weights_out, ws, want_lse, stream, 0, cap)
 
 
 def prefix_attn_decode_paged(shape: Shape, q, k_pages, v_pages, seq_lens, page_table,
@@ -443,16 +450,17 @@ def prefix_attn_decode_paged(shape: Shape, q, k_pages, v_pages, seq_lens, page_t
     [ceil(prefix_len / 128)] lists the prefix's pages, page_table int32
     [B, ceil(shape.seq_kv / 128)] those of the own caches."""
     n, P = int(prefix_len), int(k_pages.shape[0])
-    return _prefix_decode("msa_prefix_attn_decode_paged", shape, q, seq_lens, o, lse, weights,
-                          weights_out, ws, want_lse, stream,
-                          dict(prefix_pages=prefix_pages, page_table=page_table, k_pages=k_pages,
-                               v_pages=v_pages), (P, n),
-                          ("prefix_pages", "seq_lens", "page_table", "q", "k_pages", "v_pages",
-                           "o", "lse", "weights", "weights_out"), P, n)
+    return _prefix_decode("msa_prefix_attn_decode_paged", shape, (P, n),
+                          dict(prefix_pages=prefix_pages, seq_lens=seq_lens,
+                               page_table=page_table, q=q, k_pages=k_pages, v_pages=v_pages),
+                          o, lse, weights, weights_out, ws, want_lse, stream, P, n)
 
 
-def _cache_evict(name, shape, k, v, seq_lens, weights, positions, weights_out, positions_out,
-                 new_lens, ws, stream, caches, lead, order, pages=0):
+def _cache_evict(name, shape, lead, inputs, weights_out, positions_out, new_lens, ws, stream,
+                 pages=0):
+    """The common part of the two calls: ``lead`` the integers after the shape,
+    ``inputs`` the tensors before the first output, in the C order."""
+    weights, positions, seq_lens = inputs["weights"], inputs["positions"], inputs["seq_lens"]
     fresh = []
     if weights_out is None:
         weights_out = weights
@@ -462,13 +470,12 @@ def _cache_evict(name, shape, k, v, seq_lens, weights, positions, weights_out, p
         new_lens = torch.empty_like(seq_lens)
         fresh.append(new_lens)
     if ws is None:
-        ws = alloc_workspace(shape, OP_CACHE_EVICT, k.device)
+        ws = alloc_workspace(shape, OP_CACHE_EVICT, seq_lens.device)
         fresh.append(ws)
-    dev = _one_device(k, v, seq_lens, weights, positions, weights_out, positions_out, new_lens,
-                      ws, *caches.values())
-    a = _args(shape, pages, seq_lens=seq_lens, weights=weights, positions=positions,
-              weights_out=weights_out, positions_out=positions_out, new_lens=new_lens, **caches)
-    _call(name, dev, stream, fresh, ctypes.byref(shape), *lead, *[a[n] for n in order], *_ws(ws))
+    dev = _one_device(*inputs.values(), weights_out, positions_out, new_lens, ws)
+    a = _args(shape, pages, **inputs, weights_out=weights_out, positions_out=positions_out,
+              new_lens=new_lens)
+    _call(name, dev, stream, fresh, ctypes.byref(shape), *lead, *a.values(), *_ws(ws))
     return weights_out, positions_out, new_lens
 
 
@@ -480,11 +487,9 @@ def cache_evict(shape: Shape, k, v, seq_lens, weights, positions, budget, first=
     before all others.  k, v are compacted in place; weights and positions
     [B, G, shape.seq_kv] too unless weights_out / positions_out are given.
     Returns (weights_out, positions_out, new_lens)."""
-    return _cache_evict("msa_cache_evict", shape, k, v, seq_lens, weights, positions, weights_out,
-                        positions_out, new_lens, ws, stream, dict(k=k, v=v),
-                        (int(budget), int(first), int(recent)),
-                        ("seq_lens", "weights", "positions", "k", "v", "weights_out",
-                         "positions_out", "new_lens"))
+    return _cache_evict("msa_cache_evict", shape, (int(budget), int(first), int(recent)),
+                        dict(seq_lens=seq_lens, weights=weights, positions=positions, k=k, v=v),
+                        weights_out, positions_out, new_lens, ws, stream)
 
 
 def cache_evict_paged(shape: Shape, k_pages, v_pages, seq_lens, page_table, weights, positions,
@@ -493,12 +498,11 @@ def cache_evict_paged(shape: Shape, k_pages, v_pages, seq_lens, page_table, weig
     """msa_cache_evict_paged: cache_evict over paged caches k_pages / v_pages
     [P, G, 128, d] with page_table int32 [B, ceil(shape.seq_kv / 128)]."""
     P = int(k_pages.shape[0])
-    return _cache_evict("msa_cache_evict_paged", shape, k_pages, v_pages, seq_lens, weights,
-                        positions, weights_out, positions_out, new_lens, ws, stream,
-                        dict(page_table=page_table, k_pages=k_pages, v_pages=v_pages),
+    return _cache_evict("msa_cache_evict_paged", shape,
                         (P, int(budget), int(first), int(recent)),
-                        ("seq_lens", "page_table", "weights", "positions", "k_pages", "v_pages",
-                         "weights_out", "positions_out", "new_lens"), P)
+                        dict(seq_lens=seq_lens, page_table=page_table, weights=weights,
+                             positions=positions, k_pages=k_pages, v_pages=v_pages),
+                        weights_out, positions_out, new_lens, ws, stream, P)
 
 
 def profile_enable(on: bool = True):
