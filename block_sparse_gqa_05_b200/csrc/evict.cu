@@ -52,7 +52,7 @@ struct __align__(16) Mover {
   int row;
   float weight;
   int pos;
-  int to;      // unused by the list; keeps the entry one 16-byte access
+  int pad;     // one 16-byte access
 };
 
 struct EvictParams {
@@ -95,49 +95,47 @@ __device__ __forceinline__ long long row_at(const EvictParams& p, int b, int g, 
   return ((static_cast<long long>(pg) * p.G + g) * 128 + (x & 127)) * p.d;
 }
 
-// Moves pairs first, first + step, ... < n of (b, g): a warp takes 32 / (d / 4)
-// rows at a time, 16 bytes of K or V a lane, kMoveDeep of them in flight.
-constexpr int kMoveDeep = 4;
-__device__ __forceinline__ void move_rows(const EvictParams& p, int bg, int n, int first, int step) {
+// Moves entries [i0, i1) (at most kMoveRows) of (b, g)'s lists by the CTA: a
+// thread per entry finds where the row goes from and to (s_at), then a warp
+// takes 32 / (d / 4) rows at a time, 16 bytes of K or V a lane, kMoveDeep of
+// them in flight (the addresses found by every lane, with the loads of a row's
+// list entry before those of the row, made it wait more than it loaded: 172
+// against 137 us for 800 MB; 4 rows in flight 140, 512 rows a CTA 149).
+constexpr int kMoveDeep = 8;
+__device__ __forceinline__ void move_rows(const EvictParams& p, int bg, int i0, int i1,
+                                          longlong2* s_at) {
   const int b = bg / p.G, g = bg - b * p.G;
-  const int lane = threadIdx.x & 31;
-  const int per = p.d / 4;                     // 16-byte pieces of a row's K and V
+  const int threads = static_cast<int>(blockDim.x), tid = static_cast<int>(threadIdx.x);
+  const long long list = static_cast<long long>(bg) * p.half, base = static_cast<long long>(bg) * p.C;
+#pragma unroll 1
+  for (int i = i0 + tid; i < i1; i += threads) {
+    const int4 mover = __ldcg(reinterpret_cast<const int4*>(p.movers + list + i));
+    const int hole = __ldcg(p.holes + list + i);
+    p.w_out[base + hole] = __int_as_float(mover.y);
+    p.pos_out[base + hole] = mover.z;
+    const long long from = row_at(p, b, g, mover.x), to = row_at(p, b, g, hole);
+    s_at[i - i0] = make_longlong2(to < 0 ? -1 : from, to);
+  }
+  __syncthreads();
+  const int lane = tid & 31, per = p.d / 4;    // 16-byte pieces of a row's K and V
   const int at_once = 32 / per, sub = lane / per, piece = lane - sub * per;
   const bool is_v = piece >= per / 2;
   uint16_t* cache = (is_v ? p.v : p.k) + (is_v ? piece - per / 2 : piece) * 8;
-  const Mover* movers = p.movers + static_cast<long long>(bg) * p.half;
-  const int32_t* holes = p.holes + static_cast<long long>(bg) * p.half;
-  const long long base = static_cast<long long>(bg) * p.C;
+  const int rows = i1 - i0, step = threads / 32 * at_once;
 #pragma unroll 1
-  for (int i0 = first * at_once; i0 < n; i0 += step * at_once * kMoveDeep) {
-    int4 mover[kMoveDeep];
-    int hole[kMoveDeep];
-#pragma unroll
-    for (int u = 0; u < kMoveDeep; ++u) {
-      const int i = min(i0 + u * step * at_once + sub, n - 1);
-      mover[u] = __ldcg(reinterpret_cast<const int4*>(movers + i));
-      hole[u] = __ldcg(holes + i);
-    }
+  for (int r0 = (tid >> 5) * at_once + sub; r0 < rows; r0 += step * kMoveDeep) {
     uint4 x[kMoveDeep];
-    long long to[kMoveDeep];
 #pragma unroll
     for (int u = 0; u < kMoveDeep; ++u) {
-      to[u] = -1;
-      if (i0 + u * step * at_once + sub < n) {
-        if (piece == 0) {
-          p.w_out[base + hole[u]] = __int_as_float(mover[u].y);
-          p.pos_out[base + hole[u]] = mover[u].z;
-        }
-        const long long s = row_at(p, b, g, mover[u].x), t = row_at(p, b, g, hole[u]);
-        if (s >= 0 && t >= 0) {
-          x[u] = __ldcs(reinterpret_cast<const uint4*>(cache + s));
-          to[u] = t;
-        }
-      }
+      const int r = r0 + u * step;
+      const long long from = r < rows ? s_at[r].x : -1;
+      if (from >= 0) x[u] = __ldcs(reinterpret_cast<const uint4*>(cache + from));
     }
 #pragma unroll
-    for (int u = 0; u < kMoveDeep; ++u)
-      if (to[u] >= 0) *reinterpret_cast<uint4*>(cache + to[u]) = x[u];
+    for (int u = 0; u < kMoveDeep; ++u) {
+      const int r = r0 + u * step;
+      if (r < rows && s_at[r].x >= 0) *reinterpret_cast<uint4*>(cache + s_at[r].y) = x[u];
+    }
   }
 }
 
@@ -561,22 +559,26 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
   }
   __threadfence();
   sync_all();
-  move_rows(p, bg, moves, rank * kWarps + warp, cs * kWarps);
+  // this CTA's share, at most kMaxFusedMoves; the histograms' memory is free now
+  const int share = (moves + cs - 1) / cs;
+  move_rows(p, bg, min(moves, rank * share), min(moves, (rank + 1) * share),
+            reinterpret_cast<longlong2*>(&sh.hist[0][0]));
 }
 
 // The moves of all (sequence, group)s, kMoveRows a CTA.
-__global__ void __launch_bounds__(kMoveThreads)
+__global__ void __launch_bounds__(kMoveThreads, 4)
     evict_move_kernel(const __grid_constant__ EvictParams p) {
   griddep_wait();
   griddep_launch_dependents();
   const int bg = blockIdx.x;
   const int n = __ldcg(p.n_moves + bg);
-  const int at_once = 128 / p.d;
+  __shared__ longlong2 s_at[kMoveRows];
+#pragma unroll 1
   for (long long i0 = static_cast<long long>(blockIdx.y) * kMoveRows; i0 < n;
        i0 += static_cast<long long>(gridDim.y) * kMoveRows) {
-    // rows i0 .. i0 + kMoveRows - 1, at_once of them a warp and step
-    const int end = static_cast<int>(min(static_cast<long long>(n), i0 + kMoveRows));
-    move_rows(p, bg, end, static_cast<int>(i0) / at_once + (threadIdx.x >> 5), kMoveThreads / 32);
+    move_rows(p, bg, static_cast<int>(i0), static_cast<int>(min(static_cast<long long>(n), i0 + kMoveRows)),
+              s_at);
+    __syncthreads();
   }
 }
 
