@@ -10,23 +10,20 @@
 // weights and positions, and by latency.
 //
 // A cluster of CTAs shares one (sequence, group), each with a contiguous slice
-// of its rows, whose keys it keeps in shared memory when they fit (4 bytes a
-// row: two CTAs an SM up to some 20,000 rows).  The n-th largest key is found
-// digit by digit (11, 11 and 10 bits) from histograms in shared memory that
-// every CTA of the cluster reads over distributed shared memory: three passes
-// over the slice whatever the values, and no order of atomics can change the
-// result.  Each warp then owns a contiguous run of rows, counts, and writes the
-// lists of holes and movers at ranks that follow from the counts of the warps
-// and CTAs before it.  A lane takes four consecutive rows at a time, two such
-// loads in flight: with one row a lane a slice of 131,072 rows was read at 16
-// GB/s an SM.
+// of its rows, whose keys it keeps in shared memory (4 bytes a row, two CTAs an
+// SM).  The n-th largest key is found digit by digit (11, 11 and 10 bits) from
+// histograms in shared memory that every CTA of the cluster reads over
+// distributed shared memory: three passes over the slice whatever the values,
+// and no order of atomics can change the result.  Each warp then owns a
+// contiguous run of rows, counts, and writes the lists of holes and movers at
+// ranks that follow from the counts of the warps and CTAs before it.  A lane
+// takes four consecutive rows at a time: with one row a lane a slice was read at
+// 16 GB/s an SM.  Rows too long for the cluster's shared memory are chosen by
+// kernels of the whole GPU instead (evict_long.cu); the moves are the same.
 #include <cooperative_groups.h>
-#include <math.h>
-
 #include <algorithm>
 
-#include "internal.h"
-#include "ptx.cuh"
+#include "evict.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -35,65 +32,18 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 2048;
 constexpr int kPer = kBins / kThreads;       // bins a thread sums
 constexpr int kMaxCluster = 16;              // past the portable 8: long rows of few sequences
-constexpr int kStep = 128;                   // rows a warp takes at a time, four a lane
-// Most rows whose keys a CTA keeps in shared memory.
-constexpr int kMaxStash = 49152;
+// Most rows of a CTA's slice: as long as two CTAs share an SM.  Past it choosing
+// by chunks is faster (160 (sequence, group)s of 49152 rows 265 against 345 us,
+// of 32768 185 against 206; 8 of 524288 157 against 212), below it slower (64 of
+// 65536 155 against 138 us, one of 32768 34 against 26: seven kernels for one).
+constexpr int kMaxSlice = 20480;
 // Most rows a CTA moves itself; past it a second kernel moves them with the
 // whole GPU (one launch more, against one CTA's share of the bandwidth).
 constexpr int kMaxFusedMoves = 128;
 constexpr int kMoveThreads = 256;
 constexpr int kMoveRows = 256;                // rows of a CTA of the second kernel
-
-// A moved row: where it came from, and its weight and position.
-struct __align__(16) Mover {
-  int row;
-  float weight;
-  int pos;
-  int pad;     // one 16-byte access
-};
-
-struct EvictParams {
-  const int32_t* lens;
-  const float* w_in;
-  const int32_t* pos_in;
-  uint16_t *k, *v;
-  float* w_out;
-  int32_t* pos_out;
-  int32_t* new_lens;
-  const int32_t* table;
-  Mover* movers;      // [B*G, C/2]
-  int32_t* holes;     // [B*G, C/2]
-  int32_t* n_moves;   // [B*G]
-  uint32_t* err;
-  int G, C, d, nb, num_pages, budget, n_first, n_recent, half;
-  int cluster, fused;
-};
-
-// Order key of a weight: larger weight, larger key; NaN lowest (but above 0,
-// which stands for no row), -0 as 0.  Finite and infinite weights stay below
-// kStays.
-constexpr uint32_t kStays = 0xFFFFFFFFu;
-__device__ __forceinline__ uint32_t weight_key(float w) {
-  return isnan(w) ? 1u : float_order_key(w + 0.f);
-}
-
-__device__ __forceinline__ bool stays(const EvictParams& p, int pos, int top) {
-  return pos < p.n_first || static_cast<long long>(pos) > static_cast<long long>(top) - p.n_recent;
-}
-
-// Element offset of row x of (b, g), or -1 (flagged) when its page is bad.
-__device__ __forceinline__ long long row_at(const EvictParams& p, int b, int g, int x) {
-  if (!p.table) return ((static_cast<long long>(b) * p.G + g) * p.C + x) * p.d;
-  const int pg = __ldg(p.table + static_cast<long long>(b) * p.nb + (x >> 7));
-  if (pg < 0 || pg >= p.num_pages) {
-    atomicOr(p.err, kErrBadPage);
-    return -1;
-  }
-  return ((static_cast<long long>(pg) * p.G + g) * 128 + (x & 127)) * p.d;
-}
 
 // Moves entries [i0, i1) (at most kMoveRows) of (b, g)'s lists by the CTA: a
 // thread per entry finds where the row goes from and to (s_at), then a warp
@@ -152,26 +102,9 @@ struct __align__(16) Shared {
   int red[kWarps];
 };
 
-// Four consecutive elements from x; of those at or past ``end`` the value is
-// whatever is there (the arrays go on to a multiple of four), or 0.
-template <bool VEC, typename T>
-__device__ __forceinline__ void load4(const T* p, int x, int end, T* v) {
-  if constexpr (VEC) {
-    const int4 q = __ldcg(reinterpret_cast<const int4*>(p + x));
-    const T* t = reinterpret_cast<const T*>(&q);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = t[e];
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = x + e < end ? __ldcg(p + x + e) : T(0);
-  }
-}
-
 // VEC: every row of four starts on a 16-byte boundary in all arrays.
-template <bool STASH, bool VEC>
+template <bool VEC>
 __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constant__ EvictParams p) {
-  // Steps whose loads are in flight together where rows are read from memory
-  constexpr int U = STASH ? 1 : 4;
   __shared__ Shared sh;
   extern __shared__ __align__(16) uint32_t s_key[];
   cg::cluster_group cl = cg::this_cluster();
@@ -258,66 +191,22 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
   // Calls f(x, keys, positions, weights) for every step of this warp's rows;
   // ``fresh``: from memory (positions and weights too), else the keys kept.
   auto for_rows = [&](bool fresh, auto f) {
-    if (STASH && !fresh) {
 #pragma unroll 1
-      for (int xb = y0; xb < y1; xb += kStep) {
-        const int x = xb + 4 * lane;
-        uint32_t key[4] = {0, 0, 0, 0};
-        if (x < y1) *reinterpret_cast<uint4*>(key) = *reinterpret_cast<const uint4*>(s_key + x - x0);
-        f(x, key, nullptr, nullptr);
-      }
-      return;
-    }
-#pragma unroll 1
-    for (int xb = y0; xb < y1; xb += U * kStep) {
-      int q[U][4];
-      float wx[U][4];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int x = xb + u * kStep + 4 * lane;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          q[u][e] = 0;
-          wx[u][e] = 0.f;
-        }
+    for (int xb = y0; xb < y1; xb += kStep) {
+      const int x = xb + 4 * lane;
+      uint32_t key[4] = {0, 0, 0, 0};
+      int q[4] = {0, 0, 0, 0};
+      float wx[4] = {0.f, 0.f, 0.f, 0.f};
+      if (fresh) {
         if (x < y1) {
-          load4<VEC>(w, x, y1, wx[u]);
-          load4<VEC>(pos, x, y1, q[u]);
+          load4<VEC>(w, x, y1, wx);
+          load4<VEC>(pos, x, y1, q);
         }
+        make_keys(x, q, wx, key);
+      } else if (x < y1) {
+        *reinterpret_cast<uint4*>(key) = *reinterpret_cast<const uint4*>(s_key + x - x0);
       }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int x = xb + u * kStep + 4 * lane;
-        uint32_t key[4] = {0, 0, 0, 0};
-        if (xb + u * kStep < y1) {                 // the warp's own bound: uniform
-          make_keys(x, q[u], wx[u], key);
-          f(x, key, q[u], wx[u]);
-        }
-      }
-    }
-  };
-  // Counts the bins of four rows a lane where in.  Equal keys (rows that no query
-  // looked at, ties) would queue up on one bin.
-  auto count_bins = [&](uint32_t* hist, const bool* in, const uint32_t* bin) {
-    const bool any = in[0] || in[1] || in[2] || in[3];
-    const unsigned m = __ballot_sync(0xffffffffu, any);
-    if (!m) return;
-    const uint32_t own = in[0] ? bin[0] : in[1] ? bin[1] : in[2] ? bin[2] : bin[3];
-    const uint32_t lead = __shfl_sync(0xffffffffu, own, __ffs(m) - 1);
-    bool same = true;
-    int c = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      same &= !in[e] || bin[e] == lead;
-      c += in[e] ? 1 : 0;
-    }
-    if (__all_sync(0xffffffffu, same)) {
-      c = __reduce_add_sync(0xffffffffu, c);
-      if (lane == 0) atomicAdd(hist + lead, static_cast<uint32_t>(c));
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (in[e]) atomicAdd(hist + bin[e], 1u);
+      f(x, key, q, wx);
     }
   };
   // Makes the histogram's sums of 32 bins and lets the cluster see both.
@@ -376,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
   auto first_digit = [&] {
     int fixed = 0;
     for_rows(true, [&](int x, const uint32_t* key, const int*, const float*) {
-      if (STASH && x < y1) *reinterpret_cast<uint4*>(s_key + x - x0) = *reinterpret_cast<const uint4*>(key);
+      if (x < y1) *reinterpret_cast<uint4*>(s_key + x - x0) = *reinterpret_cast<const uint4*>(key);
       bool in[4];
       uint32_t bin[4];
 #pragma unroll
@@ -494,19 +383,6 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
   }
   Mover* movers = p.movers + static_cast<long long>(bg) * p.half;
   int32_t* holes = p.holes + static_cast<long long>(bg) * p.half;
-  const unsigned below = (1u << lane) - 1u;
-  // rank of this lane's first such row among the warp's, and their number
-  auto rank4 = [&](const bool* f, int* count) {
-    int before = 0, all = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const unsigned m = __ballot_sync(0xffffffffu, f[e]);
-      before += __popc(m & below);
-      all += __popc(m);
-    }
-    *count = all;
-    return before;
-  };
   for_rows(true, [&](int x, const uint32_t* key, int* q, float* wx) {
     bool eq[4], keep[4], hole[4], move[4];
     int count;
@@ -585,7 +461,7 @@ __global__ void __launch_bounds__(kMoveThreads, 4)
 size_t lists_half(const msa_shape& s) { return static_cast<size_t>(s.seq_kv) / 2; }
 
 struct EvictWs {
-  size_t movers, holes, n_moves, bytes;
+  size_t movers, holes, n_moves, chunks, bytes;
 };
 
 // Holes and movers of a (sequence, group): at most min(n, len - n) <= N / 2 each.
@@ -595,7 +471,9 @@ EvictWs ws_layout(const msa_shape& s) {
   w.movers = 0;
   w.holes = align_up(lists * sizeof(Mover), 256);
   w.n_moves = w.holes + align_up(lists * sizeof(int32_t), 256);
-  w.bytes = w.n_moves + align_up(bg * sizeof(int32_t), 256);
+  w.chunks = w.n_moves + align_up(bg * sizeof(int32_t), 256);
+  // with a cluster of one CTA; a larger one may do without
+  w.bytes = w.chunks + (s.seq_kv > kMaxSlice ? evict_long_bytes(static_cast<int64_t>(bg), s.seq_kv) : 0);
   return w;
 }
 
@@ -650,33 +528,31 @@ cudaError_t launch_cache_evict(const msa_shape& s, const EvictArgs& a, void* ws,
   p.n_first = a.n_first;
   p.n_recent = a.n_recent;
   p.half = static_cast<int>(lists_half(s));
-  // CTAs of a cluster: as many as run at once (two an SM), not below 1024 rows each
   const int64_t bg = static_cast<int64_t>(s.batch) * s.n_kv_heads;
+  const int64_t most = std::min<int64_t>(a.budget, std::max(p.C - a.budget, 0));   // moves there can be
+  auto vec16 = [](const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15u) == 0; };
+  const bool vec = p.C % 4 == 0 && vec16(p.w_in) && vec16(p.pos_in) && vec16(p.w_out) && vec16(p.pos_out);
+  // CTAs of a cluster: as many as run at once (two an SM), not below 1024 rows each
   p.cluster = 1;
   while (p.cluster < kMaxCluster && 2 * bg * p.cluster <= 2ll * ctx->num_sms &&
          p.C / (2 * p.cluster) >= 1024)
     p.cluster *= 2;
-  const int64_t most = std::min<int64_t>(a.budget, std::max(p.C - a.budget, 0));   // moves there can be
-  p.fused = most <= static_cast<int64_t>(kMaxFusedMoves) * p.cluster;
-  const int64_t slice = align_up(static_cast<size_t>(ceil_div(p.C, p.cluster)), kStep);
-  const bool stash = slice <= kMaxStash;
-  auto vec16 = [](const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15u) == 0; };
-  const bool vec = p.C % 4 == 0 && vec16(p.w_in) && vec16(p.pos_in) && vec16(p.w_out) && vec16(p.pos_out);
-  const size_t smem = stash ? static_cast<size_t>(slice) * 4 : 0;
-  const unsigned grid = static_cast<unsigned>(bg * p.cluster);
-  auto kernel = stash ? (vec ? evict_kernel<true, true> : evict_kernel<true, false>)
-                      : (vec ? evict_kernel<false, true> : evict_kernel<false, false>);
+  const size_t slice = align_up(static_cast<size_t>(ceil_div(p.C, p.cluster)), kStep);
   cudaError_t e = cudaSuccess;
-  if (stash)
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxStash * 4);
-  if (e == cudaSuccess && p.cluster > 8)
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e != cudaSuccess) return e;
-  {
+  if (slice > kMaxSlice) {
+    e = launch_evict_long(p, bg, vec, mem + w.chunks, st);
+  } else {
+    p.fused = most <= static_cast<int64_t>(kMaxFusedMoves) * p.cluster;
+    auto kernel = vec ? evict_kernel<true> : evict_kernel<false>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSlice * 4);
+    if (e == cudaSuccess && p.cluster > 8)
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
     ProfScope ps_("cache_evict", st);
-    e = launch_clustered(kernel, grid, p.cluster, smem, st, p);
+    e = launch_clustered(kernel, static_cast<unsigned>(bg * p.cluster), p.cluster,
+                         slice * sizeof(uint32_t), st, p);
   }
-  if (e != cudaSuccess || p.fused) return e;
+  if (e != cudaSuccess || p.fused || most == 0) return e;
   {
     ProfScope ps_("cache_evict_move", st);
     const int64_t slices = std::min<int64_t>(ceil_div(most, kMoveRows), 65535);   // grid limit

@@ -376,7 +376,7 @@ msa_status msa_prefix_attn_decode_paged(const msa_shape* shape, int num_pages, i
  *   (rows that always stay, weight descending, row ascending),
  * where a row always stays (before every other one) when positions < n_first
  * or positions > (largest position of its (sequence, group)) - n_recent; a
- * NaN weight counts as the lowest, -0 as 0.  The cache is compacted in place
+ * NaN weight counts as -infinity, -0 as 0.  The cache is compacted in place
  * by moving as few rows as possible: the kept rows x >= n, ascending, go to
  * the dropped rows x < n, ascending; every other kept row stays where it is.
  *   k, v           [B, G, N, d], rows of the moved keys are overwritten; rows

@@ -358,6 +358,67 @@ def test_evict(i, in_place):
     c.check(got, budget, first, recent, in_place)
 
 
+# rows too many for a cluster's shared memory: chosen by chunks of 8192
+LONG = [
+    (dict(B=1, G=1, d=64, C=330000, lens=[330000]), 30000, 4, 5000),
+    (dict(B=1, G=1, d=64, C=330001, lens=[330001], kind="ties", shuffled=True), 300000, 2, 10),
+    (dict(B=2, G=1, d=64, C=330003, lens=[329999, 8193], kind="odd"), 8000, 0, 0),
+    (dict(B=1, G=1, d=128, C=330000, lens=[327680], kind="equal", shuffled=True), 9000, 0, 77),
+    (dict(B=1, G=2, d=64, C=330004, lens=[330002], kind="close", shuffled=True), 5000, 16, 100),
+    (dict(B=1, G=1, d=64, C=330000, lens=[329990]), 1000, 50, 80000),       # more rows stay than the budget
+    (dict(B=1, G=1, d=64, C=330000, lens=[330000], kind="odd", shuffled=True), 10000, 1 << 20, 0),
+    (dict(B=3, G=1, d=64, C=330000, lens=[330000, 5000, 0]), 6000, 0, 1),   # nothing to drop for two
+    (dict(B=2, G=1, d=64, C=330000, lens=[1, 330000]), 330000, 9, 9),       # for nobody
+    (dict(B=1, G=1, d=64, C=330000, lens=[330000], kind="equal"), 1, 0, 0),
+]
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("i", range(len(LONG)))
+def test_evict_long_rows(i, in_place):
+    c, budget, first, recent = LONG[i]
+    c = Cache(seed=60 + i, **c)
+    got = c.run(budget, first, recent, in_place)
+    assert M.device_status() == 0
+    c.check(got, budget, first, recent, in_place)
+
+
+def test_evict_long_rows_that_just_fit():
+    c = Cache(B=1, G=1, d=64, C=330000, lens=[330000], seed=75)
+    pos = c.pos[0, 0].long()
+    budget = int(((pos < 100) | (pos > pos.max() - 9000)).sum())           # exactly the rows that stay
+    c.check(c.run(budget, 100, 9000), budget, 100, 9000)
+
+
+def test_evict_long_rows_captured_and_replayed():
+    c = Cache(B=1, G=1, d=64, C=330000, lens=[329000], shuffled=True, seed=76)
+    k, v, w, pos = (c.dev(x) for x in (c.k, c.v, c.w, c.pos))
+    k0, v0 = k.clone(), v.clone()
+    lens, new = (torch.tensor(c.lens, dtype=torch.int32).cuda() for _ in range(2))
+    wo, po = torch.full_like(w, -7.0), torch.full_like(pos, -7)
+    ws = M.alloc_workspace(c.shape, M.OP_CACHE_EVICT)
+    call = lambda: M.cache_evict(c.shape, k, v, lens, w, pos, 2000, 4, 20, weights_out=wo, positions_out=po,
+                                 new_lens=new, ws=ws)
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        call()
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for _ in range(2):
+        k.copy_(k0), v.copy_(v0), wo.fill_(-7.0), po.fill_(-7), new.fill_(-1)
+        graph.replay()
+        torch.cuda.synchronize()
+        c.check((k, v, wo, po, new), 2000, 4, 20)
+
+
+@pytest.mark.parametrize("budget", [300, 430, 495])
+def test_evict_nan_ties_with_minus_infinity(budget):
+    c = Cache(B=2, G=2, d=64, C=500, lens=[500, 499], kind="odd", seed=31)      # the cut reaches the lowest
+    c.check(c.run(budget, 0, 0), budget, 0, 0)
+
+
 def test_evict_again_moves_the_same_rows():
     c = Cache(B=2, G=2, d=64, C=900, lens=[900, 700], seed=30)
     k, v, w, pos = (c.dev(x) for x in (c.k, c.v, c.w, c.pos))
