@@ -159,8 +159,7 @@ def _sizes_of(fields: bytes, pages: int, prefix: int) -> dict:
 
 def _args(shape: Shape, pages: int = 0, prefix: int = 0, **tensors) -> dict:
     """Device pointers of the named tensors after checking each one's dtype and
-    that it holds at least the elements its layout needs (None stays None), in
-    the order given."""
+    that it holds at least the elements its layout needs (None stays None)."""
     need = _sizes_of(bytes(shape), pages, prefix)
     out = {}
     for name, t in tensors.items():
@@ -180,8 +179,9 @@ def _ws(ws):
 
 
 def _stream(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    # the handle alone: making a Stream object of it takes 2 us, a tenth of a decode call
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) if stream is None \
+        else stream.cuda_stream
 
 
 def _check(status: int, what: str):
@@ -383,13 +383,26 @@ def dense_attn_decode(shape: Shape, q, k, v, o=None, lse=None, ws=None, want_lse
     return o, lse
 
 
-def _one_device(first, *others):
-    """The device all given tensors are on (raises when there are several)."""
-    index, dev = first.get_device(), first.device
-    for t in others:
-        if t is not None and (t.get_device() != index or index < 0 and t.device != dev):
+def _device_args(shape: Shape, pages: int, prefix: int, ws, **tensors):
+    """_args for tensors that must share a device: (pointers in the order given,
+    the workspace's pointer and size; the device).  The tensors' own checks come
+    first, in one pass: a decode step is short enough for its host time to show."""
+    need = _sizes_of(bytes(shape), pages, prefix)
+    index, dev, out = ws.get_device(), ws.device, []
+    for name, t in tensors.items():
+        if t is None:
+            out.append(None)
+            continue
+        dtype, n = need[name]
+        if t.dtype is not dtype:
+            raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+        if t.numel() < n:
+            raise ValueError(f"{name}: {t.numel()} elements, the shape needs {n}")
+        if t.get_device() != index or index < 0 and t.device != dev:
             raise ValueError(f"libmsa takes tensors of one device, got {dev} and {t.device}")
-    return dev
+        out.append(t.data_ptr() if index >= 0 and t.is_contiguous() else _ptr(t))
+    out += _ws(ws)
+    return out, dev
 
 
 def _call(name, dev, stream, fresh, *args):
@@ -416,11 +429,11 @@ def _prefix_decode(name, shape, lead, inputs, o, lse, weights, weights_out, ws, 
     if ws is None:
         ws = alloc_workspace(shape, OP_PREFIX_DECODE if weights_out is None
                              else OP_PREFIX_DECODE_WEIGHTS, q.device)
-    fresh = [t for t, had in zip((o, lse, ws), given) if had is None and t is not None]
-    dev = _one_device(q, *inputs.values(), o, lse, weights, weights_out, ws)
-    a = _args(shape, pages, prefix, **inputs, o=o, lse=lse, weights=weights,
-              weights_out=weights_out)
-    _call(name, dev, stream, fresh, ctypes.byref(shape), *lead, *a.values(), *_ws(ws))
+    fresh = () if stream is None else \
+        [t for t, had in zip((o, lse, ws), given) if had is None and t is not None]
+    args, dev = _device_args(shape, pages, prefix, ws, **inputs, o=o, lse=lse, weights=weights,
+                             weights_out=weights_out)
+    _call(name, dev, stream, fresh, ctypes.byref(shape), *lead, *args)
     return o, lse, weights_out
 
 
@@ -472,10 +485,9 @@ def _cache_evict(name, shape, lead, inputs, weights_out, positions_out, new_lens
     if ws is None:
         ws = alloc_workspace(shape, OP_CACHE_EVICT, seq_lens.device)
         fresh.append(ws)
-    dev = _one_device(*inputs.values(), weights_out, positions_out, new_lens, ws)
-    a = _args(shape, pages, **inputs, weights_out=weights_out, positions_out=positions_out,
-              new_lens=new_lens)
-    _call(name, dev, stream, fresh, ctypes.byref(shape), *lead, *a.values(), *_ws(ws))
+    args, dev = _device_args(shape, pages, 0, ws, **inputs, weights_out=weights_out,
+                             positions_out=positions_out, new_lens=new_lens)
+    _call(name, dev, stream, fresh, ctypes.byref(shape), *lead, *args)
     return weights_out, positions_out, new_lens
 
 
