@@ -33,11 +33,11 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPer = kBins / kThreads;       // bins a thread sums
-constexpr int kMaxCluster = 16;              // past the portable 8: long rows of few sequences
+constexpr int kMaxCluster = 8;
 // Most rows of a CTA's slice: as long as two CTAs share an SM.  Past it choosing
 // by chunks is faster (160 (sequence, group)s of 49152 rows 265 against 345 us,
 // of 32768 185 against 206; 8 of 524288 157 against 212), below it slower (64 of
-// 65536 155 against 138 us, one of 32768 34 against 26: seven kernels for one).
+// 65536 155 against 138 us, one of 32768 34 against 21: seven kernels for one).
 constexpr int kMaxSlice = 20480;
 // Most rows a CTA moves itself; past it a second kernel moves them with the
 // whole GPU (one launch more, against one CTA's share of the bandwidth).
@@ -532,10 +532,15 @@ cudaError_t launch_cache_evict(const msa_shape& s, const EvictArgs& a, void* ws,
   const int64_t most = std::min<int64_t>(a.budget, std::max(p.C - a.budget, 0));   // moves there can be
   auto vec16 = [](const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15u) == 0; };
   const bool vec = p.C % 4 == 0 && vec16(p.w_in) && vec16(p.pos_in) && vec16(p.w_out) && vec16(p.pos_out);
-  // CTAs of a cluster: as many as run at once (two an SM), not below 1024 rows each
+  // CTAs of a cluster: as many as run at once, not below 2048 rows each (8 x 8192
+  // rows by 4 CTAs 15.8, by 8 17.8 us; one of 2048 by one 11.4, by two 13.6), two
+  // an SM; for a cluster of 8 two an SM only from 4096 rows each (32 x 16384 rows
+  // by 4 CTAs 28.6, by 8 36.9 us; 32 x 32768 48.5 and 44).  Clusters of 16 had to
+  // wait for one another: seven GPCs take two (16 x 65536 rows 74 us, by 8 51).
   p.cluster = 1;
   while (p.cluster < kMaxCluster && 2 * bg * p.cluster <= 2ll * ctx->num_sms &&
-         p.C / (2 * p.cluster) >= 1024)
+         p.C / (2 * p.cluster) >= 2048 &&
+         (p.cluster < 4 || 2 * bg * p.cluster <= ctx->num_sms || p.C / (2 * p.cluster) >= 4096))
     p.cluster *= 2;
   const size_t slice = align_up(static_cast<size_t>(ceil_div(p.C, p.cluster)), kStep);
   cudaError_t e = cudaSuccess;
@@ -545,8 +550,6 @@ cudaError_t launch_cache_evict(const msa_shape& s, const EvictArgs& a, void* ws,
     p.fused = most <= static_cast<int64_t>(kMaxFusedMoves) * p.cluster;
     auto kernel = vec ? evict_kernel<true> : evict_kernel<false>;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSlice * 4);
-    if (e == cudaSuccess && p.cluster > 8)
-      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     ProfScope ps_("cache_evict", st);
     e = launch_clustered(kernel, static_cast<unsigned>(bg * p.cluster), p.cluster,
