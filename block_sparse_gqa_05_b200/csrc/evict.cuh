@@ -33,7 +33,7 @@ struct EvictParams {
   int32_t* n_moves;   // [B*G]
   uint32_t* err;
   int G, C, d, nb, num_pages, budget, n_first, n_recent, half;
-  int cluster, fused;
+  int cluster, fused, keep;
 };
 
 // Order key of a weight: larger weight, larger key; NaN as -infinity, -0 as 0.
