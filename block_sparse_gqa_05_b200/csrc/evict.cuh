@@ -40,7 +40,8 @@ struct EvictParams {
 // All lie between 0, which stands for no row, and kStays.
 constexpr uint32_t kStays = 0xFFFFFFFFu;
 __device__ __forceinline__ uint32_t weight_key(float w) {
-  return float_order_key(isnan(w) ? -INFINITY : w + 0.f);
+  const int u = __float_as_int(isnan(w) ? -INFINITY : w + 0.f);
+  return static_cast<uint32_t>(u ^ (u >> 31 | INT32_MIN));     // negative: all bits flipped, else the sign
 }
 
 __device__ __forceinline__ bool stays(const EvictParams& p, int pos, int top) {

@@ -102,18 +102,17 @@ __device__ __forceinline__ void load_rows(const T* from, const Where& o, T (*v)[
   }
 }
 
-// Turns the weights of the lane's rows into keys; rows past the chunk get 0.
+// Turns the weights of the lane's rows into keys; those of rows past the chunk are
+// not meant.
 // ``fixed``: whether rows that always stay are among them, ``only_fixed``:
 // whether only these count.
 template <bool VEC>
 __device__ __forceinline__ void make_keys(const EvictParams& p, const Where& o, bool fixed, bool only_fixed,
                                           int top, const float (*w)[4], uint32_t (*key)[4]) {
 #pragma unroll
-  for (int u = 0; u < kSteps; ++u) {
-    const int left = o.x1 - (o.y0 + u * kStep + 4 * static_cast<int>(threadIdx.x & 31));
+  for (int u = 0; u < kSteps; ++u)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) key[u][e] = e < left ? weight_key(w[u][e]) : 0u;
-  }
+    for (int e = 0; e < 4; ++e) key[u][e] = weight_key(w[u][e]);
   if (!fixed && !only_fixed) return;
 #pragma unroll
   for (int u = 0; u < kSteps; ++u) {
@@ -123,7 +122,7 @@ __device__ __forceinline__ void make_keys(const EvictParams& p, const Where& o, 
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const bool f = fixed && stays(p, q[e], top);
-      if (x + e < o.x1 && f != only_fixed) key[u][e] = f ? kStays : 0u;
+      if (f != only_fixed) key[u][e] = f ? kStays : 0u;
     }
   }
 }
@@ -383,18 +382,20 @@ __global__ void __launch_bounds__(kThreads, 3) evict_middle_kernel(const __grid_
   }
   uint32_t key[kSteps][4];
   make_keys<VEC>(a.p, o, fixed, only_fixed, top, w, key);
-  // rows above the digit and at it, a bit each; no row (key 0) is neither, for the
-  // digit is that of a row's key and these are past 2^21
-  uint32_t gts = 0, ins = 0;
+  // rows at the digit or above and those above, a bit each (a row that does not
+  // count has key 0, below every digit: a row's key is past 2^21)
+  uint32_t ins = 0, gts = 0;
+  const uint32_t lo = digit << 21, hi = lo | 0x1fffffu;
 #pragma unroll
   for (int u = 0; u < kSteps; ++u)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      if (key[u][e] >> 21 > digit)
-        gts |= 1u << (4 * u + e);
-      else if (key[u][e] >> 21 == digit)
-        ins |= 1u << (4 * u + e);
+      if (key[u][e] >= lo) ins |= 1u << (4 * u + e);
+      if (key[u][e] > hi) gts |= 1u << (4 * u + e);
     }
+  const uint32_t valid = rows_below(o, o.x1);
+  gts &= valid;
+  ins &= valid & ~gts;
   const uint32_t los = rows_below(o, o.n);
   int gt[2] = {__popc(gts & los), __popc(gts & ~los)};
   // those at the digit: their lower digits and whether they lie before row n, in
@@ -562,10 +563,13 @@ __global__ void __launch_bounds__(kThreads, 3) evict_lists_kernel(const __grid_c
     for (int u = 0; u < kSteps; ++u)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        gts |= (key[u][e] > cut ? 1u : 0u) << (4 * u + e);
-        eqs |= (key[u][e] == cut ? 1u : 0u) << (4 * u + e);
+        if (key[u][e] > cut) gts |= 1u << (4 * u + e);
+        if (key[u][e] == cut) eqs |= 1u << (4 * u + e);
       }
   }
+  const uint32_t los = rows_below(o, o.n), ins = rows_below(o, o.x1);
+  gts &= ins;
+  eqs &= ins;
   // what comes before this chunk, and all rows at the cut and past row n
   int sum[7] = {0, 0, 0, 0, 0, 0, 0};
   const int nch = (o.len - 1) / kChunk + 1;
@@ -583,7 +587,6 @@ __global__ void __launch_bounds__(kThreads, 3) evict_lists_kernel(const __grid_c
   // the rows at the cut before row n come before those past it
   const int need_hi = max(need - sum[4], 0);
   if (o.c == 0 && tid == 0) p.n_moves[o.bg] = sum[5] + min(need_hi, sum[6]);
-  const uint32_t los = rows_below(o, o.n), ins = rows_below(o, o.x1);
   int c4[4] = {__popc(gts & los), __popc(gts & ~los), __popc(eqs & los), __popc(eqs & ~los)};
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
