@@ -11,8 +11,12 @@
 //
 // A cluster of CTAs shares one (sequence, group), each with a contiguous slice
 // of its rows, whose keys it keeps in shared memory (4 bytes a row, two CTAs an
-// SM).  The n-th largest key is found digit by digit (11, 11 and 10 bits) from
-// histograms in shared memory that every CTA of the cluster reads over
+// SM).  Weights and positions are read once for the keys, as if no row always
+// stayed, and each step's range of positions; once the largest position is
+// known, the steps whose range holds rows that always stay are corrected (a pass
+// for the largest position before that for the keys took 61 against 54 us at 32
+// x 128K).  The n-th largest key is found digit by digit (11, 11 and 10 bits)
+// from histograms in shared memory that every CTA of the cluster reads over
 // distributed shared memory: three passes over the slice whatever the values,
 // and no order of atomics can change the result.  Each warp then owns a
 // contiguous run of rows, counts, and writes the lists of holes and movers at
@@ -20,6 +24,10 @@
 // takes four consecutive rows at a time: with one row a lane a slice was read at
 // 16 GB/s an SM.  Rows too long for the cluster's shared memory are chosen by
 // kernels of the whole GPU instead (evict_long.cu); the moves are the same.
+//
+// 256 x 4097 rows with one to drop 14.4 us (2.5 of them at the bandwidth of HBM;
+// the rest is a chain of passes with a barrier each); 32 x 100,000 to 131,072
+// rows to 32,768: 54 us here and 137 us for the moves (floor of both 125).
 #include <cooperative_groups.h>
 #include <algorithm>
 
@@ -100,6 +108,7 @@ struct __align__(16) Shared {
   uint32_t digit;
   int need;
   int red[kWarps];
+  int2 range[kMaxSlice / kStep];    // smallest and largest position of a step
 };
 
 // VEC: every row of four starts on a 16-byte boundary in all arrays.
@@ -153,28 +162,52 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
   const int run = (slice / kStep + kWarps - 1) / kWarps * kStep;
   const int y0 = min(x1, x0 + warp * run), y1 = min(x1, y0 + run);
 
-  // largest position; short slices keep what was read, of others the weights come
-  // nearer meanwhile
+  // Keys as if no row always stayed, their first digit's histogram, and the range
+  // of positions of each step; short slices keep what was read.
   float* s_w = reinterpret_cast<float*>(s_key + slice);
   int* s_pos = reinterpret_cast<int*>(s_key + 2 * slice);
   int top = INT32_MIN;
-#pragma unroll 4
-  for (int x = y0 + 4 * lane; x < y1; x += kStep) {
-    int q[4];
-    load4<VEC>(pos, x, y1, q);
-    if (p.keep) {
-      float wx[4];
-      load4<VEC>(w, x, y1, wx);
-      *reinterpret_cast<float4*>(s_w + x - x0) = make_float4(wx[0], wx[1], wx[2], wx[3]);
-      *reinterpret_cast<int4*>(s_pos + x - x0) = make_int4(q[0], q[1], q[2], q[3]);
-    } else if ((lane & 7) == 0) {
-      prefetch_l2(w + x);
+#pragma unroll 1
+  for (int xb = y0; xb < y1; xb += 2 * kStep) {
+    int q[2][4];
+    float wx[2][4];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int x = xb + u * kStep + 4 * lane;
+      if (x < y1) {
+        load4<VEC>(pos, x, y1, q[u]);
+        load4<VEC>(w, x, y1, wx[u]);
+      }
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (x + e < y1) top = max(top, q[e]);
+    for (int u = 0; u < 2; ++u) {
+      const int x = xb + u * kStep + 4 * lane;
+      if (xb + u * kStep >= y1) break;             // the warp's own bound: uniform
+      bool in[4];
+      uint32_t key[4], bin[4];
+      int least = INT32_MAX, most = INT32_MIN;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        in[e] = x + e < y1;
+        key[e] = in[e] ? weight_key(wx[u][e]) : 0u;
+        bin[e] = key[e] >> 21;
+        least = min(least, in[e] ? q[u][e] : INT32_MAX);
+        most = max(most, in[e] ? q[u][e] : INT32_MIN);
+      }
+      if (x < y1) {
+        *reinterpret_cast<uint4*>(s_key + x - x0) = *reinterpret_cast<const uint4*>(key);
+        if (p.keep) {
+          *reinterpret_cast<float4*>(s_w + x - x0) = *reinterpret_cast<const float4*>(wx[u]);
+          *reinterpret_cast<int4*>(s_pos + x - x0) = *reinterpret_cast<const int4*>(q[u]);
+        }
+      }
+      count_bins(sh.hist[0], in, bin);
+      least = __reduce_min_sync(0xffffffffu, least);
+      most = __reduce_max_sync(0xffffffffu, most);
+      top = max(top, most);
+      if (lane == 0) sh.range[(xb - x0) / kStep + u] = make_int2(least, most);
+    }
   }
-  top = __reduce_max_sync(0xffffffffu, top);
   if (lane == 0) sh.red[warp] = top;
   __syncthreads();
   if (warp == 0) {
@@ -186,38 +219,24 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
 #pragma unroll 1
   for (int r = 0; r < cs; ++r) top = max(top, of_rank(r)->top);
 
-  // Keys of four rows from x of positions q and weights wx.  By default rows that
-  // always stay come before all; when there are more of them than fit, only
-  // they have keys, by weight.
-  bool only_fixed = false;
-  auto make_keys = [&](int x, const int* q, const float* wx, uint32_t* key) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const bool f = stays(p, q[e], top);
-      key[e] = only_fixed ? (f ? weight_key(wx[e]) : 0u) : f ? kStays : weight_key(wx[e]);
-      if (x + e >= y1) key[e] = 0u;
-    }
-  };
-  // Calls f(x, keys, positions, weights) for every step of this warp's rows;
-  // ``fresh``: from memory (positions and weights too), else the keys kept.
-  auto for_rows = [&](bool fresh, auto f) {
+  // Calls f(x, keys, positions, weights) for every step of this warp's rows, the
+  // last two only with ``values``.
+  auto for_rows = [&](bool values, auto f) {
 #pragma unroll 1
     for (int xb = y0; xb < y1; xb += kStep) {
       const int x = xb + 4 * lane;
       uint32_t key[4] = {0, 0, 0, 0};
       int q[4] = {0, 0, 0, 0};
       float wx[4] = {0.f, 0.f, 0.f, 0.f};
-      if (fresh) {
-        if (x < y1 && p.keep) {
+      if (x < y1) {
+        *reinterpret_cast<uint4*>(key) = *reinterpret_cast<const uint4*>(s_key + x - x0);
+        if (values && p.keep) {
           *reinterpret_cast<float4*>(wx) = *reinterpret_cast<const float4*>(s_w + x - x0);
           *reinterpret_cast<int4*>(q) = *reinterpret_cast<const int4*>(s_pos + x - x0);
-        } else if (x < y1) {
+        } else if (values) {
           load4<VEC>(w, x, y1, wx);
           load4<VEC>(pos, x, y1, q);
         }
-        make_keys(x, q, wx, key);
-      } else if (x < y1) {
-        *reinterpret_cast<uint4*>(key) = *reinterpret_cast<const uint4*>(s_key + x - x0);
       }
       f(x, key, q, wx);
     }
@@ -274,43 +293,59 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
     __syncthreads();
   };
 
-  // first digit, and the number of rows that always stay
-  auto first_digit = [&] {
-    int fixed = 0;
-    for_rows(true, [&](int x, const uint32_t* key, const int*, const float*) {
-      if (x < y1) *reinterpret_cast<uint4*>(s_key + x - x0) = *reinterpret_cast<const uint4*>(key);
+  // Rows that always stay come before all others: their keys become the largest,
+  // in the steps whose range holds such rows.
+  int fixed = 0;
+#pragma unroll 1
+  for (int xb = y0; xb < y1; xb += kStep) {
+    const int2 range = sh.range[(xb - x0) / kStep];
+    if (!stays(p, range.x, top) && !stays(p, range.y, top)) continue;
+    const int x = xb + 4 * lane;
+    if (x >= y1) continue;
+    int q[4];
+    if (p.keep)
+      *reinterpret_cast<int4*>(q) = *reinterpret_cast<const int4*>(s_pos + x - x0);
+    else
+      load4<VEC>(pos, x, y1, q);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (x + e < y1 && stays(p, q[e], top)) {
+        atomicSub(&sh.hist[0][s_key[x + e - x0] >> 21], 1u);
+        s_key[x + e - x0] = kStays;
+        ++fixed;
+      }
+  }
+  fixed = __reduce_add_sync(0xffffffffu, fixed);
+  if (lane == 0) {
+    sh.red[warp] = fixed;
+    atomicAdd(&sh.hist[0][kStays >> 21], static_cast<uint32_t>(fixed));
+  }
+  __syncthreads();
+  if (warp == 0) {
+    fixed = __reduce_add_sync(0xffffffffu, lane < kWarps ? sh.red[lane] : 0);
+    if (lane == 0) sh.fixed = fixed;
+  }
+  show_hist(0);
+  fixed = 0;
+#pragma unroll 1
+  for (int r = 0; r < cs; ++r) fixed += of_rank(r)->fixed;
+  if (fixed > n) {                      // more than fit: only they have keys, by weight
+    sync_all();                         // every CTA has read the histogram's sums and counts
+    for (int i = tid; i < kBins; i += kThreads) sh.hist[0][i] = 0;
+    __syncthreads();
+    for_rows(true, [&](int x, uint32_t* key, const int*, const float* wx) {
       bool in[4];
       uint32_t bin[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        in[e] = x + e < y1;
+        in[e] = key[e] == kStays;
+        key[e] = in[e] ? weight_key(wx[e]) : 0u;
         bin[e] = key[e] >> 21;
-        fixed += key[e] == kStays ? 1 : 0;
       }
+      if (x < y1) *reinterpret_cast<uint4*>(s_key + x - x0) = *reinterpret_cast<const uint4*>(key);
       count_bins(sh.hist[0], in, bin);
     });
-    return __reduce_add_sync(0xffffffffu, fixed);
-  };
-  int fixed = 0;
-#pragma unroll 1
-  for (;;) {                            // a second time when too many rows always stay
-    const int f = first_digit();
-    if (lane == 0) sh.red[warp] = f;
-    __syncthreads();
-    if (warp == 0) {
-      fixed = __reduce_add_sync(0xffffffffu, lane < kWarps ? sh.red[lane] : 0);
-      if (lane == 0) sh.fixed = fixed;
-    }
     show_hist(0);
-    if (only_fixed) break;
-    fixed = 0;
-#pragma unroll 1
-    for (int r = 0; r < cs; ++r) fixed += of_rank(r)->fixed;
-    if (fixed <= n) break;
-    only_fixed = true;
-    sync_all();                         // every CTA has read the counts
-    for (int i = tid; i < kBins; i += kThreads) sh.hist[0][i] = 0;
-    __syncthreads();
   }
   find_digit(0, n);
   uint32_t cut = sh.digit << 21;
