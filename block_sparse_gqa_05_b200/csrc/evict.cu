@@ -132,7 +132,9 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
     reinterpret_cast<uint4*>(&sh.hist[0][0])[i] = make_uint4(0, 0, 0, 0);
   griddep_wait();
   griddep_launch_dependents();
-  int len = __ldg(p.lens + b);
+  if (tid == 0) sh.red[0] = __ldcg(p.lens + b);    // by one thread: it is a hot line of L2
+  __syncthreads();                                 // and the histograms are clear
+  int len = sh.red[0];
   if (len < 0 || len > p.C) {
     if (tid == 0 && rank == 0) atomicOr(p.err, kErrBadLength);
     len = len < 0 ? 0 : p.C;
@@ -154,8 +156,8 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
   if (n == len) {
 #pragma unroll 1
     for (int x = x0 + tid; x < x1; x += kThreads) {
-      if (!same_w) wo[x] = w[x];
-      if (!same_p) po[x] = pos[x];
+      if (!same_w) wo[x] = __ldcg(w + x);
+      if (!same_p) po[x] = __ldcg(pos + x);
     }
     return;
   }
@@ -208,10 +210,10 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
       if (lane == 0) sh.range[(xb - x0) / kStep + u] = make_int2(least, most);
     }
   }
-  if (lane == 0) sh.red[warp] = top;
+  if (lane == 0) sh.wcounts[warp][0] = top;
   __syncthreads();
   if (warp == 0) {
-    top = __reduce_max_sync(0xffffffffu, lane < kWarps ? sh.red[lane] : INT32_MIN);
+    top = __reduce_max_sync(0xffffffffu, lane < kWarps ? sh.wcounts[lane][0] : INT32_MIN);
     if (lane == 0) sh.top = top;
   }
   sync_all();

@@ -1,5 +1,7 @@
 // What the two ways to choose the rows of an eviction share: its arguments, the
 // order of rows, and steps of a warp over 128 rows, four consecutive ones a lane.
+// Lengths, weights and positions are read from L2: the kernel before on the
+// stream may still write them when this one starts, after an SM cached the line.
 #pragma once
 #include <math.h>
 

@@ -73,7 +73,7 @@ __device__ __forceinline__ Where locate(const LongParams& a) {
   o.bg = static_cast<int>(blockIdx.x) / a.nch;
   o.c = static_cast<int>(blockIdx.x) - o.bg * a.nch;
   o.b = o.bg / a.p.G;
-  o.len = min(max(__ldg(a.p.lens + o.b), 0), a.p.C);
+  o.len = min(max(__ldcg(a.p.lens + o.b), 0), a.p.C);
   o.n = min(o.len, a.p.budget);
   o.x0 = static_cast<int>(min(static_cast<long long>(o.len), static_cast<long long>(o.c) * kChunk));
   o.x1 = static_cast<int>(min(static_cast<long long>(o.len), static_cast<long long>(o.x0) + kChunk));
@@ -102,8 +102,7 @@ __device__ __forceinline__ void load_rows(const T* from, const Where& o, T (*v)[
   }
 }
 
-// Turns the weights of the lane's rows into keys; those of rows past the chunk are
-// not meant.
+// Turns the weights of the lane's rows into keys (any value past the chunk).
 // ``fixed``: whether rows that always stay are among them, ``only_fixed``:
 // whether only these count.
 template <bool VEC>
@@ -258,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_first_kernel(const __grid_c
   const Where o = locate(a);
   const int tid = static_cast<int>(threadIdx.x), lane = tid & 31;
   if (o.c == 0 && tid == 0) {
-    const int len = __ldg(a.p.lens + o.b);
+    const int len = __ldcg(a.p.lens + o.b);
     if (len < 0 || len > a.p.C) atomicOr(a.p.err, kErrBadLength);
     if (o.bg == o.b * a.p.G) a.p.new_lens[o.b] = o.n;
   }
@@ -544,8 +543,8 @@ __global__ void __launch_bounds__(kThreads, 3) evict_lists_kernel(const __grid_c
     const bool same_w = p.w_out == p.w_in, same_p = p.pos_out == p.pos_in;
 #pragma unroll 1
     for (int x = o.x0 + tid; x < o.x1; x += kThreads) {
-      if (!same_w) p.w_out[o.base + x] = p.w_in[o.base + x];
-      if (!same_p) p.pos_out[o.base + x] = p.pos_in[o.base + x];
+      if (!same_w) p.w_out[o.base + x] = __ldcg(p.w_in + o.base + x);
+      if (!same_p) p.pos_out[o.base + x] = __ldcg(p.pos_in + o.base + x);
     }
     return;
   }

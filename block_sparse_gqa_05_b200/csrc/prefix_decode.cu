@@ -79,9 +79,11 @@ struct PrefixParams {
   float scale_log2;
 };
 
-// Valid rows of sequence b's own cache, clamped into [0, C].
+// Valid rows of sequence b's own cache, clamped into [0, C].  Read from L2, as the
+// scores are: the kernel before on the stream may still run when this one starts
+// and write them (an eviction's new lengths) after this SM cached the line.
 __device__ __forceinline__ int own_len(const PrefixParams& p, int b) {
-  const int n = __ldg(p.lens + b);
+  const int n = __ldcg(p.lens + b);
   if (n >= 0 && n <= p.C) return n;
   atomicOr(p.err, kErrBadLength);
   return n < 0 ? 0 : p.C;
@@ -1146,7 +1148,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   const float we[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int e = 0; e < 4; ++e)      // rows of C elements need not be 16-byte aligned
-    if (x + e < len) p.w_out[at + e] = (p.w_in ? p.w_in[at + e] : 0.f) + we[e];
+    if (x + e < len) p.w_out[at + e] = (p.w_in ? __ldcg(p.w_in + at + e) : 0.f) + we[e];
 }
 
 // Workspace layout.

@@ -545,6 +545,40 @@ def test_a_bounded_decode_loop():
     assert M.device_status() == 0 and int(lens.max()) == budget + 1
 
 
+def test_calls_back_to_back_see_the_lengths_just_written():
+    """attend and evict in turn with nothing in between, the lengths in two halves
+    of one small array, against the same calls with a synchronisation after each."""
+    c = _loop_inputs(seed=93)
+    c.k, c.v = torch.nan_to_num(c.k, 0, 0, 0), torch.nan_to_num(c.v, 0, 0, 0)
+    q = (torch.randn(12, c.B, 1, c.H, c.d, generator=torch.Generator().manual_seed(6)) * 2).bfloat16().cuda()
+    kp, vp = c.dev(c.kp), c.dev(c.vp)
+
+    def chain(packed):
+        k, v, w = c.dev(c.k), c.dev(c.v), c.dev(c.w)
+        pos = torch.arange(c.C, dtype=torch.int32).expand(c.B, c.G, c.C).contiguous().cuda()
+        both = torch.zeros(2, c.B, dtype=torch.int32).cuda()
+        lens = [both[0], both[1]] if packed else [both[0].clone(), both[1].clone()]
+        lens[0].copy_(torch.tensor(c.lens, dtype=torch.int32))
+        out = []
+        for step in range(12):
+            a, z = lens[step % 2], lens[1 - step % 2]
+            o, lse, _ = M.prefix_attn_decode(c.shape, q[step], k, v, a, kp, vp, weights=w)
+            if not packed:
+                torch.cuda.synchronize()
+            M.cache_evict(c.shape, k, v, a, w, pos, 190 - 15 * step, 2, 8, new_lens=z)
+            if not packed:
+                torch.cuda.synchronize()
+            out += [o, lse]
+        torch.cuda.synchronize()
+        return out + [k, v, w, pos, lens[0].clone()]
+
+    ref = chain(False)
+    assert ref[-1].tolist() == [min(n, 190 - 15 * 11) for n in c.lens]
+    for _ in range(3):
+        assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(ref, chain(True)))
+    assert M.device_status() == 0
+
+
 def test_captured_and_replayed():
     """One step (scored attention, then eviction) captured once and replayed
     gives the eager calls' bits, on inputs changed between replays."""
