@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_slot;   // S/P of the warpgroups at 0 and 128, O at 256 and 384
 
   if (warp < 4) {
-    regs_dec<80>();
+    regs_dec<88>();        // 4 x 88 + 8 x 208 warps' worth is what the launch has; with 80 these spilled
     if (warp == 3) {
       // ------------------------------------------------------------ the walk
       if (lane == 0) {
