@@ -50,10 +50,14 @@ constexpr int kMaxGrid = 256;      // bound of the persistent grid, for the work
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRescaleLog2 = 8.f;   // a row's reference follows its maximum when that is 2^8 above it
 
-// Cost of a block on the line, in some 500 clocks: of a pair, of a spread tile, of
-// another single tile; and of a segment.
-constexpr int kCostPair = 7, kCostSpread = 5, kCostSingle = 8, kCostSegment = 2, kCostPairSegment = 14;
-constexpr int kCostMost = 8;
+// Cost of a block on the line, in some 220 clocks: of a pair, of a spread tile, of
+// another single tile of up to 32 rows and of more; and of a segment.  Measured on
+// 32 sequences with a prefix of 8192 (the CTAs of a finer line end together: 52 to
+// 50 us) and on 24 with 5 tokens each, whose own tiles have 40 rows (18 for these
+// against 16: 112 and 115 us).
+constexpr int kCostPair = 16, kCostSpread = 10, kCostFew = 16, kCostSingle = 18, kCostSegment = 4,
+              kCostPairSegment = 28;
+constexpr int kCostMost = 18;
 
 struct PrefixParams {
   uint16_t* o;
@@ -109,17 +113,17 @@ __device__ __forceinline__ bool spreads(const PrefixParams& p, bool own, int nb)
   return (own ? p.spread_s : p.spread_p) && nb >= kSpreadBlocks;
 }
 
-// Line cost of a block of a single segment, and of one group's own segment.
-__device__ __forceinline__ int single_cost(const PrefixParams& p, bool own, int nb) {
-  return spreads(p, own, nb) ? kCostSpread : kCostSingle;
-}
-__device__ __forceinline__ int own_cost(const PrefixParams& p, int nb) {
-  return nb ? nb * single_cost(p, true, nb) + kCostSegment : 0;
-}
-
 // Whether the tiles of a kind have 32 rows or fewer.
 __device__ __forceinline__ bool few_rows(const PrefixParams& p, bool own) {
   return (own ? p.rows_s : p.rows_p) <= 32;
+}
+
+// Line cost of a block of a single segment, and of one group's own segment.
+__device__ __forceinline__ int single_cost(const PrefixParams& p, bool own, int nb) {
+  return spreads(p, own, nb) ? kCostSpread : few_rows(p, own) ? kCostFew : kCostSingle;
+}
+__device__ __forceinline__ int own_cost(const PrefixParams& p, int nb) {
+  return nb ? nb * single_cost(p, true, nb) + kCostSegment : 0;
 }
 
 // One CTA's share of a segment, as the walk hands it on (n == 0: the end).
@@ -1300,7 +1304,7 @@ cudaError_t launch_prefix_decode(const msa_shape& s, const PrefixDecodeArgs& a, 
   p.two_q = p.rows_s <= 64;
   p.q_stage = (p.spread_s ? 16 : p.rows_s <= 32 ? 32 : 64) * 128;
   p.cost_pair = p.nbp * kCostPair + kCostPairSegment;
-  const int single = p.spread_p && p.nbp >= kSpreadBlocks ? kCostSpread : kCostSingle;
+  const int single = p.spread_p && p.nbp >= kSpreadBlocks ? kCostSpread : p.rows_p <= 32 ? kCostFew : kCostSingle;
   p.cost_group = (p.npt - 1) * p.cost_pair + ((p.ntile & 1) ? p.nbp * single + kCostSegment : p.cost_pair);
   p.cost_prefix = p.Np > 0 ? p.cost_group * p.G : 0;
   p.scale_log2 = kLog2e / sqrtf(static_cast<float>(s.head_dim));

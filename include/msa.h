@@ -347,7 +347,7 @@ msa_status msa_sparse_attn_decode_static(const msa_shape* shape, const uint16_t*
  * the prefix.  Calls that can overlap need workspaces of their own.
  * Errors: T > N, prefix_len < 0 or > prefix_cap -> MSA_ERR_INVALID_SHAPE;
  * T * r > 128, G * prefix_cap >= 2^31, or more work than 32-bit positions hold
- * (some 2^28 visits of a 256-row prefix tile or of an own cache to a 128-key
+ * (some 10^8 visits of a 256-row prefix tile or of an own cache to a 128-key
  * block) -> MSA_ERR_UNSUPPORTED; weights without weights_out ->
  * MSA_ERR_NULL_PTR. */
 msa_status msa_prefix_attn_decode(const msa_shape* shape, int prefix_len, int prefix_cap,
