@@ -1236,8 +1236,10 @@ cudaError_t launch(const msa_shape& s, const PrefixDecodeArgs& a, const PrefixPa
   int split = 1;
   while (split < kMergeWarps && all * split < 8ll * grid) split *= 2;
   const int64_t merge = ceil_div(all * split, kMergeWarps);
-  // keys of a scoring CTA: short caches have fewer, their rows shared by 4 threads
-  const int keys = p.C <= 1024 ? 256 : 1024;
+  // keys of a scoring CTA: of short caches with many rows fewer, 4 threads sharing
+  // the rows (700 keys of 40 rows 112 against 126 us; 1024 keys of 8 rows 49.4
+  // against 48.3, so these have whole CTAs)
+  const int keys = p.C <= 1024 && p.rows_s > 16 ? 256 : 1024;
   const int64_t score = p.w_out ? static_cast<int64_t>(p.B) * p.G * ceil_div(p.C, keys) : 0;
   if (merge + score >= (1ll << 31)) return cudaErrorInvalidValue;
   ProfScope ps_("prefix_finish", st);
