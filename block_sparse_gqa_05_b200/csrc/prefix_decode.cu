@@ -1118,41 +1118,55 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     }
   }
   __syncthreads();
-  const int quads = keys / 4, share = static_cast<int>(threadIdx.x) / quads;
+  // 1024 keys at a time (fewer when threads share the rows: then once)
+  const int quads = min(keys, 1024) / 4, share = static_cast<int>(threadIdx.x) / quads;
   const int shares = kMergeWarps * 32 / quads, quad = static_cast<int>(threadIdx.x) - share * quads;
-  const int x = x0 + 4 * quad;
-  float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (x < len) {
-    const size_t stride = static_cast<size_t>(p.nb) * 128;
-    const float* s = p.logits + static_cast<size_t>(bg) * p.rows_s * stride + x;
+  const size_t stride = static_cast<size_t>(p.nb) * 128;
+#pragma unroll 1
+  for (int x1 = x0; x1 < min(len, x0 + keys); x1 += 4 * quads) {
+    const int x = x1 + 4 * quad;
+    float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (x < len) {
+      const float* s = p.logits + static_cast<size_t>(bg) * p.rows_s * stride + x;
 #pragma unroll 8
-    for (int i = share; i < p.rows_s; i += shares) {
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(s + i * stride));
-      const float n = norm[i];
-      w.x += fast_exp2(v.x - n);
-      w.y += fast_exp2(v.y - n);
-      w.z += fast_exp2(v.z - n);
-      w.w += fast_exp2(v.w - n);
+      for (int i = share; i < p.rows_s; i += shares) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(s + i * stride));
+        const float n = norm[i];
+        w.x += fast_exp2(v.x - n);
+        w.y += fast_exp2(v.y - n);
+        w.z += fast_exp2(v.z - n);
+        w.w += fast_exp2(v.w - n);
+      }
     }
-  }
-  if (shares > 1) {
-    float4* sums = reinterpret_cast<float4*>(buf);
-    if (share > 0) sums[threadIdx.x - quads] = w;
-    __syncthreads();
-    if (share > 0) return;
-    for (int u = 0; u + 1 < shares; ++u) {
-      const float4 v = sums[u * quads + quad];
-      w.x += v.x;
-      w.y += v.y;
-      w.z += v.z;
-      w.w += v.w;
+    if (shares > 1) {
+      float4* sums = reinterpret_cast<float4*>(buf);
+      if (share > 0) sums[threadIdx.x - quads] = w;
+      __syncthreads();
+      if (share > 0) return;
+      for (int u = 0; u + 1 < shares; ++u) {
+        const float4 v = sums[u * quads + quad];
+        w.x += v.x;
+        w.y += v.y;
+        w.z += v.z;
+        w.w += v.w;
+      }
     }
-  }
-  const long long at = static_cast<long long>(bg) * p.C + x;
-  const float we[4] = {w.x, w.y, w.z, w.w};
+    const long long at = static_cast<long long>(bg) * p.C + x;
+    const float we[4] = {w.x, w.y, w.z, w.w};
+    const float* old = p.w_in + at;
+    float* to = p.w_out + at;
+    if (x + 3 < len && ((reinterpret_cast<uintptr_t>(old) | reinterpret_cast<uintptr_t>(to)) & 15u) == 0) {
+      if (p.w_in) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(old));
+        w = make_float4(v.x + w.x, v.y + w.y, v.z + w.z, v.w + w.w);
+      }
+      *reinterpret_cast<float4*>(to) = w;
+      continue;
+    }
 #pragma unroll
-  for (int e = 0; e < 4; ++e)      // rows of C elements need not be 16-byte aligned
-    if (x + e < len) p.w_out[at + e] = (p.w_in ? __ldcg(p.w_in + at + e) : 0.f) + we[e];
+    for (int e = 0; e < 4; ++e)      // rows of C elements need not be 16-byte aligned
+      if (x + e < len) to[e] = (p.w_in ? __ldcg(old + e) : 0.f) + we[e];
+  }
 }
 
 // Workspace layout.
@@ -1238,8 +1252,9 @@ cudaError_t launch(const msa_shape& s, const PrefixDecodeArgs& a, const PrefixPa
   const int64_t merge = ceil_div(all * split, kMergeWarps);
   // keys of a scoring CTA: of short caches with many rows fewer, 4 threads sharing
   // the rows (700 keys of 40 rows 112 against 126 us; 1024 keys of 8 rows 49.4
-  // against 48.3, so these have whole CTAs)
-  const int keys = p.C <= 1024 && p.rows_s > 16 ? 256 : 1024;
+  // against 48.3, so these have whole CTAs); of long ones two rounds (16,384 keys
+  // of 8 rows 111.5 against 113.6 us, with four 121.8)
+  const int keys = p.C <= 1024 && p.rows_s > 16 ? 256 : p.C >= 8192 ? 2048 : 1024;
   const int64_t score = p.w_out ? static_cast<int64_t>(p.B) * p.G * ceil_div(p.C, keys) : 0;
   if (merge + score >= (1ll << 31)) return cudaErrorInvalidValue;
   ProfScope ps_("prefix_finish", st);
