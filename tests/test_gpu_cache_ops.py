@@ -203,6 +203,12 @@ def test_many_blocks_per_cta(kw, d):
     assert M.device_status() == 0
 
 
+@pytest.mark.parametrize("C, lens", [(9000, [9000, 8190]), (9001, [9001, 8193]), (8192, [8192, 6145])])
+def test_scores_of_long_caches(C, lens):
+    c = Case(B=2, T=2, H=8, G=2, d=64, Np=100, C=C, lens=lens, seed=77)
+    c.check(*c.run())
+
+
 def test_scores_in_place_and_from_zero():
     c = Case(seed=70, **CASES[3])
     _, _, w = c.run()
