@@ -27,7 +27,7 @@
 //
 // 256 x 4097 rows with one to drop 14.4 us (2.5 of them at the bandwidth of HBM;
 // the rest is a chain of passes with a barrier each); 32 x 100,000 to 131,072
-// rows to 32,768: 54 us here and 137 us for the moves (floor of both 125).
+// rows to 32,768: 54 us here and 136 us for the moves (floor of both 125).
 #include <cooperative_groups.h>
 #include <algorithm>
 
@@ -50,15 +50,17 @@ constexpr int kMaxSlice = 20480;
 // Most rows a CTA moves itself; past it a second kernel moves them with the
 // whole GPU (one launch more, against one CTA's share of the bandwidth).
 constexpr int kMaxFusedMoves = 128;
-constexpr int kMoveThreads = 256;
-constexpr int kMoveRows = 256;                // rows of a CTA of the second kernel
+// Threads and rows of a CTA of the second kernel: small ones end together (256 and
+// 256 192 us with the choice at 32 x 128K rows, 128 and 128 186, 128 and 64 184).
+constexpr int kMoveThreads = 128;
+constexpr int kMoveRows = 64;
 
 // Moves entries [i0, i1) (at most kMoveRows) of (b, g)'s lists by the CTA: a
 // thread per entry finds where the row goes from and to (s_at), then a warp
 // takes 32 / (d / 4) rows at a time, 16 bytes of K or V a lane, kMoveDeep of
 // them in flight (the addresses found by every lane, with the loads of a row's
 // list entry before those of the row, made it wait more than it loaded: 172
-// against 137 us for 800 MB; 4 rows in flight 140, 512 rows a CTA 149).
+// against 137 us for 800 MB; 4 rows in flight 140, more CTAs an SM 147).
 constexpr int kMoveDeep = 8;
 __device__ __forceinline__ void move_rows(const EvictParams& p, int bg, int i0, int i1,
                                           longlong2* s_at) {
@@ -492,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
 }
 
 // The moves of all (sequence, group)s, kMoveRows a CTA.
-__global__ void __launch_bounds__(kMoveThreads, 4)
+__global__ void __launch_bounds__(kMoveThreads, 8)
     evict_move_kernel(const __grid_constant__ EvictParams p) {
   griddep_wait();
   griddep_launch_dependents();
