@@ -55,7 +55,7 @@ constexpr int kMaxFusedMoves = 128;
 constexpr int kMoveThreads = 128;
 constexpr int kMoveRows = 64;
 
-// Moves entries [i0, i1) (at most kMoveRows) of (b, g)'s lists by the CTA: a
+// Moves entries [i0, i1) (no more than s_at holds) of (b, g)'s lists by the CTA: a
 // thread per entry finds where the row goes from and to (s_at), then a warp
 // takes 32 / (d / 4) rows at a time, 16 bytes of K or V a lane, kMoveDeep of
 // them in flight (the addresses found by every lane, with the loads of a row's
