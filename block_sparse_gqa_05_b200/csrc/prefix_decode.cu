@@ -1169,7 +1169,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   }
 }
 
-// Workspace layout.
+// Workspace layout, from its start rounded up to kWsAlign: the caller's is a
+// multiple of 16 bytes, and store8 needs 32.
+constexpr size_t kWsAlign = 32;
 struct PrefixWs {
   size_t span, ml_p, o_p, ml_s, o_s, logits, bytes;
 };
@@ -1195,7 +1197,7 @@ PrefixWs ws_layout(const msa_shape& s, bool weights) {
   w.ml_s = take(sr * sizeof(float2));
   w.o_s = take(sr * d * sizeof(float));
   w.logits = take(weights ? bg * s.seq_q * r * ceil_div(s.seq_kv, 128) * 128 * sizeof(float) : 0);
-  w.bytes = at;
+  w.bytes = at + kWsAlign - 16;
   return w;
 }
 
@@ -1284,7 +1286,7 @@ cudaError_t launch_prefix_decode(const msa_shape& s, const PrefixDecodeArgs& a, 
   const DevCtx* ctx = device_ctx();
   if (!ctx) return cudaErrorInitializationError;
   const PrefixWs w = ws_layout(s, a.w_out != nullptr);
-  char* base = static_cast<char*>(ws);
+  char* base = reinterpret_cast<char*>(align_up(reinterpret_cast<uintptr_t>(ws), kWsAlign));
   PrefixParams p{};
   p.o = a.o;
   p.lse = a.lse;

@@ -185,3 +185,16 @@ def test_binding_refuses(calls):  # noqa: F811
     with pytest.raises(ValueError, match="one device"):
         M.cache_evict(s, x["k"], x["v"], x["lens"], x["w"], x["pos"].to("meta"), 10)
     assert set(calls) <= {"msa_workspace_size"}             # no compute call was made
+
+
+def test_attend_workspace_has_room_for_its_alignment():
+    """The workspace may start at any multiple of 16 bytes, the attention stores
+    32 at a time: the size holds the arrays from the next multiple of 32 on."""
+    s = shape()                    # 3 sequences x 4 groups, r = 4, d = 64; 12 prefix rows, 4 own ones
+    up = lambda n: -(-n // 256) * 256
+    pre, own = 2 * (4 + 256) * 12 * 4, 2 * (12 + 256) * 4 * 4
+    plain = up(16 * 8) + up(pre * 8) + up(pre * 256) + up(own * 8) + up(own * 256)
+    assert size(s, M.OP_PREFIX_DECODE) == (0, plain + 16)
+    assert size(s, M.OP_PREFIX_DECODE_WEIGHTS) == (0, plain + 12 * 4 * 1024 * 4 + 16)
+    exact = plain + 16
+    assert attend(s, ws=ctypes.c_void_p((1 << 20) + 16), n=exact - 1) == 4

@@ -687,3 +687,21 @@ def test_nan_and_infinite_queries_stay_in_their_rows():
     hit[1, 0, 3] = hit[2, 1, 0] = True
     assert torch.equal(o.cpu()[~hit], ref[0].cpu()[~hit]) and torch.equal(lse.cpu()[~hit], ref[1].cpu()[~hit])
     assert M.device_status() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("op", [M.OP_PREFIX_DECODE, M.OP_PREFIX_DECODE_WEIGHTS])
+def test_workspace_at_any_multiple_of_16_bytes(op, d):
+    """A slice of a caller's arena that starts 16 bytes past a multiple of 32 and
+    is no longer than asked for: the same bits, nothing written beside it."""
+    c = Case(B=5, T=2, H=8, G=2, d=d, Np=700, C=600, lens=[600, 2, 0, 131, 555], seed=97)
+    scored = op == M.OP_PREFIX_DECODE_WEIGHTS
+    ref = c.run(scored)
+    n = M.workspace_size(c.shape, op)
+    arena = torch.full((n + 96,), 0x5A, dtype=torch.uint8, device="cuda")
+    at = 32 - arena.data_ptr() % 32 + 16
+    got = c.run(scored, ws=arena[at:at + n])
+    torch.cuda.synchronize()
+    assert all(x is y is None or torch.equal(x, y) for x, y in zip(ref, got))
+    assert (arena[:at] == 0x5A).all() and (arena[at + n:] == 0x5A).all()
+    assert M.device_status() == 0
