@@ -73,6 +73,7 @@ struct PrefixParams {
   float* o_s;          // [(B*G + grid) * 2, T*r, D]
   float* logits;       // [B*G, T*r, 128 nb] (log2 units; scores wanted) or nullptr
   int B, T, H, G, r, C, nb, num_pages;
+  int grid;            // CTAs of the attention
   int Np, nbp;         // prefix rows and blocks
   int ntile, npt, nsp; // prefix row tiles and tile pairs of a group; prefix segments
   int rows_p, rows_s;  // rows of a prefix / own tile: min(128, B*T*r), T*r
@@ -945,9 +946,16 @@ __device__ __forceinline__ Parts parts_of(const PrefixParams& p, bool own, int t
   s.n = 0;
   s.first = 0;
   if (nb > 0) {
+    // A CTA whose wait expired leaves without the spans of its other segments:
+    // what the workspace held there is no index.  One within the grid is, as the
+    // partials of every segment have room for that of every CTA.
     const int2 span = __ldcg(p.span + (own ? p.nsp + id : id));
-    s.n = (span.y - span.x + 1) * s.per;
-    s.first = 2 * (id + span.x) + wg0;
+    if (span.x >= 0 && span.x <= span.y && span.y < p.grid) {
+      s.n = (span.y - span.x + 1) * s.per;
+      s.first = 2 * (id + span.x) + wg0;
+    } else {
+      atomicOr(p.err, kErrTimeout);
+    }
   }
   return s;
 }
@@ -1202,7 +1210,7 @@ PrefixWs ws_layout(const msa_shape& s, bool weights) {
 }
 
 template <int D>
-cudaError_t launch(const msa_shape& s, const PrefixDecodeArgs& a, const PrefixParams& p, int grid,
+cudaError_t launch(const msa_shape& s, const PrefixDecodeArgs& a, const PrefixParams& p,
                    cudaStream_t st) {
   PrefixMaps tm;
   const uint64_t D8 = D;
@@ -1242,7 +1250,7 @@ cudaError_t launch(const msa_shape& s, const PrefixDecodeArgs& a, const PrefixPa
   if (e != cudaSuccess) return e;
   {
     ProfScope ps_("prefix_attn", st);
-    e = launch_dependent(prefix_attn_kernel<D>, dim3(static_cast<unsigned>(grid)), dim3(kThreads),
+    e = launch_dependent(prefix_attn_kernel<D>, dim3(static_cast<unsigned>(p.grid)), dim3(kThreads),
                          smem, st, tm, p);
   }
   if (e != cudaSuccess) return e;
@@ -1250,7 +1258,7 @@ cudaError_t launch(const msa_shape& s, const PrefixDecodeArgs& a, const PrefixPa
   // of 8 heads took 11.2 against 10.7 us, 32 of 64 52.7 against 52.0)
   const int64_t all = static_cast<int64_t>(p.B) * p.T * p.H;
   int split = 1;
-  while (split < kMergeWarps && all * split < 8ll * grid) split *= 2;
+  while (split < kMergeWarps && all * split < 8ll * p.grid) split *= 2;
   const int64_t merge = ceil_div(all * split, kMergeWarps);
   // keys of a scoring CTA: of short caches with many rows fewer, 4 threads sharing
   // the rows (700 keys of 40 rows 112 against 126 us; 1024 keys of 8 rows 49.4
@@ -1331,7 +1339,8 @@ cudaError_t launch_prefix_decode(const msa_shape& s, const PrefixDecodeArgs& a, 
   const int64_t most = static_cast<int64_t>(p.nsp) * p.nbp + static_cast<int64_t>(p.B) * p.G * p.nb;
   const int grid =
       static_cast<int>(std::min<int64_t>(most, std::min(std::max(ctx->num_sms, 1), kMaxGrid)));
-  return s.head_dim == 128 ? launch<128>(s, a, p, grid, st) : launch<64>(s, a, p, grid, st);
+  p.grid = grid;
+  return s.head_dim == 128 ? launch<128>(s, a, p, st) : launch<64>(s, a, p, st);
 }
 
 cudaError_t set_wait_limit_prefix(uint64_t ns) { return set_wait_limit_here(ns); }

@@ -705,3 +705,27 @@ def test_workspace_at_any_multiple_of_16_bytes(op, d):
     assert all(x is y is None or torch.equal(x, y) for x, y in zip(ref, got))
     assert (arena[:at] == 0x5A).all() and (arena[at + n:] == 0x5A).all()
     assert M.device_status() == 0
+
+
+@pytest.mark.parametrize("fill", [0, 0x7F, 0xFF])
+def test_expired_waits_leave_no_index_to_chance(fill):
+    """Some fourteen segments a CTA, of which a walk that gives up announces eight
+    at most: whatever the workspace held for the others, the second kernel ends,
+    reads no index from it and the error word says why."""
+    c = Case(B=256, T=1, H=8, G=8, d=64, Np=300, C=40, lens=[1 + 7 * i % 40 for i in range(256)], seed=98)
+    good = c.run()
+    torch.cuda.synchronize()
+    assert M.device_status() == 0
+    ws = M.alloc_workspace(c.shape, M.OP_PREFIX_DECODE_WEIGHTS)
+    ws.fill_(fill)
+    try:
+        M.set_wait_limit_ns(0)
+        c.run(ws=ws)
+        torch.cuda.synchronize()
+        flags = M.device_status()
+    finally:
+        M.set_wait_limit_ns(2_000_000_000)
+    assert flags == 1, flags
+    again = c.run(ws=ws)
+    torch.cuda.synchronize()
+    assert M.device_status() == 0 and all(torch.equal(a, b) for a, b in zip(good, again))
