@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 import os
 import re
 
@@ -184,6 +185,31 @@ def _stream(stream):
         else stream.cuda_stream
 
 
+def _own_memory(call):
+    """For the calls with ``stream`` as their last argument: what such a call
+    allocates (outputs and a workspace that were not given) comes from that
+    stream's memory.  A block of the current stream's may still be in use by what
+    is queued there.  The outputs are handed to the current stream, which must
+    wait for the given one before it uses them."""
+    at = list(inspect.signature(call).parameters).index("stream")
+
+    @functools.wraps(call)
+    def on_stream(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        if stream is None:
+            return call(*args, **kw)
+        here = torch.cuda.current_stream(stream.device)
+        with torch.cuda.stream(stream):
+            out = call(*args, **kw)
+        given = {id(x) for x in (*args, *kw.values())}
+        for t in out if isinstance(out, tuple) else (out,):
+            if t is not None and id(t) not in given:
+                t.record_stream(here)
+        return out
+
+    return on_stream
+
+
 def _check(status: int, what: str):
     if status != 0:
         raise MsaError(status, what)
@@ -200,6 +226,7 @@ def alloc_workspace(shape: Shape, op: int, device=None) -> torch.Tensor:
     return torch.empty(max(n, 16), dtype=torch.uint8, device=device or "cuda")
 
 
+@_own_memory
 def index_scores(shape: Shape, q_idx, k_idx, pooled=None, stream=None):
     if pooled is None:
         pooled = torch.empty((shape.batch, shape.seq_q, shape.n_kv_heads, shape.nb),
@@ -210,6 +237,7 @@ def index_scores(shape: Shape, q_idx, k_idx, pooled=None, stream=None):
     return pooled
 
 
+@_own_memory
 def block_topk(shape: Shape, pooled, sel=None, stream=None):
     if sel is None:
         sel = torch.empty((shape.batch, shape.seq_q, shape.n_kv_heads, shape.topk),
@@ -229,6 +257,7 @@ def _attn_out(shape, q, o, lse, want_lse):
     return o, lse
 
 
+@_own_memory
 def sparse_attn_prefill(shape: Shape, q, k, v, sel, o=None, lse=None, ws=None, want_lse=True,
                         stream=None):
     o, lse = _attn_out(shape, q, o, lse, want_lse)
@@ -240,6 +269,7 @@ def sparse_attn_prefill(shape: Shape, q, k, v, sel, o=None, lse=None, ws=None, w
     return o, lse
 
 
+@_own_memory
 def sparse_attn_decode(shape: Shape, q, k, v, sel, o=None, lse=None, ws=None, want_lse=True,
                        stream=None):
     o, lse = _attn_out(shape, q, o, lse, want_lse)
@@ -251,6 +281,7 @@ def sparse_attn_decode(shape: Shape, q, k, v, sel, o=None, lse=None, ws=None, wa
     return o, lse
 
 
+@_own_memory
 def sparse_attn_decode_static(shape: Shape, q, k, v, sel, o=None, lse=None, want_lse=True,
                               stream=None):
     """msa_sparse_attn_decode_static: decode attention whose scratch is the
@@ -264,6 +295,7 @@ def sparse_attn_decode_static(shape: Shape, q, k, v, sel, o=None, lse=None, want
     return o, lse
 
 
+@_own_memory
 def forward(shape: Shape, q, k, v, q_idx, k_idx, o=None, lse=None, sel=None, ws=None,
             want_lse=True, want_sel=True, stream=None):
     o, lse = _attn_out(shape, q, o, lse, want_lse)
@@ -278,6 +310,7 @@ def forward(shape: Shape, q, k, v, q_idx, k_idx, o=None, lse=None, sel=None, ws=
     return o, lse, sel
 
 
+@_own_memory
 def forward_alignment(shape: Shape, q, k, v, q_idx, k_idx, o=None, lse=None, sel=None,
                       kl=None, ws=None, want_lse=True, want_sel=True, stream=None):
     """msa_forward_alignment: the whole layer plus kl [B, T, G] float32, the
@@ -299,6 +332,7 @@ def forward_alignment(shape: Shape, q, k, v, q_idx, k_idx, o=None, lse=None, sel
     return o, lse, sel, kl
 
 
+@_own_memory
 def forward_decode_ragged(shape: Shape, q, k, v, q_idx, k_idx, seq_lens, o=None, lse=None,
                           sel=None, ws=None, want_lse=True, want_sel=True, stream=None):
     """msa_forward_decode_ragged: one decode step over caches of different
@@ -318,6 +352,7 @@ def forward_decode_ragged(shape: Shape, q, k, v, q_idx, k_idx, seq_lens, o=None,
     return o, lse, sel
 
 
+@_own_memory
 def forward_decode_paged(shape: Shape, q, k_pages, v_pages, q_idx, kidx_pages, seq_lens,
                          page_table, o=None, lse=None, sel=None, ws=None, want_lse=True,
                          want_sel=True, stream=None):
@@ -340,6 +375,7 @@ def forward_decode_paged(shape: Shape, q, k_pages, v_pages, q_idx, kidx_pages, s
     return o, lse, sel
 
 
+@_own_memory
 def forward_prefill_paged(shape: Shape, q, k_pages, v_pages, q_idx, kidx_pages, page_table,
                           o=None, lse=None, sel=None, ws=None, want_lse=True, want_sel=True,
                           stream=None):
@@ -363,6 +399,7 @@ def forward_prefill_paged(shape: Shape, q, k_pages, v_pages, q_idx, kidx_pages, 
     return o, lse, sel
 
 
+@_own_memory
 def dense_attn_prefill(shape: Shape, q, k, v, o=None, lse=None, want_lse=True, stream=None):
     o, lse = _attn_out(shape, q, o, lse, want_lse)
     a = _args(shape, q=q, k=k, v=v, o=o, lse=lse)
@@ -372,6 +409,7 @@ def dense_attn_prefill(shape: Shape, q, k, v, o=None, lse=None, want_lse=True, s
     return o, lse
 
 
+@_own_memory
 def dense_attn_decode(shape: Shape, q, k, v, o=None, lse=None, ws=None, want_lse=True,
                       stream=None):
     o, lse = _attn_out(shape, q, o, lse, want_lse)
@@ -405,16 +443,12 @@ def _device_args(shape: Shape, pages: int, prefix: int, ws, **tensors):
     return out, dev
 
 
-def _call(name, dev, stream, fresh, *args):
+def _call(name, dev, stream, *args):
     """Calls a C entry point (its arguments up to the stream) on ``dev`` and the
-    given or its current stream.  ``fresh``: tensors that this call allocated,
-    kept from reuse until a stream other than the current one is done with them."""
+    given or its current stream."""
     if dev.type == "cuda" and dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
-            return _call(name, dev, stream, fresh, *args)
-    if stream is not None:
-        for t in fresh:
-            t.record_stream(stream)
+            return _call(name, dev, stream, *args)
     _check(getattr(lib(), name)(*args, _stream(stream)), name)
 
 
@@ -424,19 +458,18 @@ def _prefix_decode(name, shape, lead, inputs, o, lse, weights, weights_out, ws, 
     ``inputs`` the tensors before the output, in the C order."""
     if weights_out is None:
         weights_out = weights
-    q, given = inputs["q"], (o, lse, ws)
+    q = inputs["q"]
     o, lse = _attn_out(shape, q, o, lse, want_lse)
     if ws is None:
         ws = alloc_workspace(shape, OP_PREFIX_DECODE if weights_out is None
                              else OP_PREFIX_DECODE_WEIGHTS, q.device)
-    fresh = () if stream is None else \
-        [t for t, had in zip((o, lse, ws), given) if had is None and t is not None]
     args, dev = _device_args(shape, pages, prefix, ws, **inputs, o=o, lse=lse, weights=weights,
                              weights_out=weights_out)
-    _call(name, dev, stream, fresh, ctypes.byref(shape), *lead, *args)
+    _call(name, dev, stream, ctypes.byref(shape), *lead, *args)
     return o, lse, weights_out
 
 
+@_own_memory
 def prefix_attn_decode(shape: Shape, q, k, v, seq_lens, k_prefix=None, v_prefix=None,
                        prefix_len=None, o=None, lse=None, weights=None, weights_out=None, ws=None,
                        want_lse=True, stream=None):
@@ -455,6 +488,7 @@ def prefix_attn_decode(shape: Shape, q, k, v, seq_lens, k_prefix=None, v_prefix=
                                v=v), o, lse, weights, weights_out, ws, want_lse, stream, 0, cap)
 
 
+@_own_memory
 def prefix_attn_decode_paged(shape: Shape, q, k_pages, v_pages, seq_lens, page_table,
                              prefix_pages=None, prefix_len=0, o=None, lse=None, weights=None,
                              weights_out=None, ws=None, want_lse=True, stream=None):
@@ -474,23 +508,21 @@ def _cache_evict(name, shape, lead, inputs, weights_out, positions_out, new_lens
     """The common part of the two calls: ``lead`` the integers after the shape,
     ``inputs`` the tensors before the first output, in the C order."""
     weights, positions, seq_lens = inputs["weights"], inputs["positions"], inputs["seq_lens"]
-    fresh = []
     if weights_out is None:
         weights_out = weights
     if positions_out is None:
         positions_out = positions
     if new_lens is None:
         new_lens = torch.empty_like(seq_lens)
-        fresh.append(new_lens)
     if ws is None:
         ws = alloc_workspace(shape, OP_CACHE_EVICT, seq_lens.device)
-        fresh.append(ws)
     args, dev = _device_args(shape, pages, 0, ws, **inputs, weights_out=weights_out,
                              positions_out=positions_out, new_lens=new_lens)
-    _call(name, dev, stream, fresh, ctypes.byref(shape), *lead, *args)
+    _call(name, dev, stream, ctypes.byref(shape), *lead, *args)
     return weights_out, positions_out, new_lens
 
 
+@_own_memory
 def cache_evict(shape: Shape, k, v, seq_lens, weights, positions, budget, first=0, recent=0,
                 weights_out=None, positions_out=None, new_lens=None, ws=None, stream=None):
     """msa_cache_evict: every (sequence, group) of the own caches k, v
@@ -504,6 +536,7 @@ def cache_evict(shape: Shape, k, v, seq_lens, weights, positions, budget, first=
                         weights_out, positions_out, new_lens, ws, stream)
 
 
+@_own_memory
 def cache_evict_paged(shape: Shape, k_pages, v_pages, seq_lens, page_table, weights, positions,
                       budget, first=0, recent=0, weights_out=None, positions_out=None,
                       new_lens=None, ws=None, stream=None):

@@ -729,3 +729,58 @@ def test_expired_waits_leave_no_index_to_chance(fill):
     again = c.run(ws=ws)
     torch.cuda.synchronize()
     assert M.device_status() == 0 and all(torch.equal(a, b) for a, b in zip(good, again))
+
+
+def _calls_that_allocate():
+    """name -> (call with ``stream`` still to give, workspace given)."""
+    c = Case(B=4, T=1, H=16, G=4, d=64, Np=300, C=260, lens=[260, 9, 128, 77], seed=99)
+    sh = M.Shape(4, 1, 260, 259, 16, 4, 64, 64, 128, 2)
+    g = torch.Generator().manual_seed(99)
+    lens = torch.tensor(c.lens, dtype=torch.int32).cuda()
+    q, k, v, kp, vp, w = (c.dev(torch.nan_to_num(x, 0.0, 0.0, 0.0)) for x in (c.q, c.k, c.v, c.kp, c.vp, c.w))
+    pos = torch.arange(260, dtype=torch.int32).expand(4, 4, 260).contiguous().cuda()
+    qi, ki = (torch.randn(*x, generator=g).to(torch.bfloat16).cuda() for x in ((4, 1, 4, 64), (4, 260, 64)))
+    sel = M.block_topk(sh, M.index_scores(sh, qi, ki))
+    ws = {op: M.alloc_workspace(sh, op) for op in (M.OP_PREFIX_DECODE, M.OP_CACHE_EVICT, M.OP_DENSE_DECODE,
+                                                   M.OP_SPARSE_DECODE)}
+    kept = (k.clone(), v.clone(), w.clone(), pos.clone())
+    return {
+        "prefix": lambda **kw: M.prefix_attn_decode(sh, q, k, v, lens, kp, vp, ws=ws[M.OP_PREFIX_DECODE], **kw)[:2],
+        "evict": lambda **kw: M.cache_evict(sh, *kept[:2], lens, *kept[2:], 100, ws=ws[M.OP_CACHE_EVICT], **kw)[2:],
+        "dense": lambda **kw: M.dense_attn_decode(sh, q, k, v, ws=ws[M.OP_DENSE_DECODE], **kw),
+        "sparse": lambda **kw: M.sparse_attn_decode(sh, q, k, v, sel, ws=ws[M.OP_SPARSE_DECODE], **kw),
+        "scores": lambda **kw: (M.index_scores(sh, qi, ki, **kw),),
+    }
+
+
+@pytest.mark.parametrize("name", ["prefix", "evict", "dense", "sparse", "scores"])
+def test_outputs_of_a_call_on_another_stream_are_not_written_late(name):
+    """Memory that was freed while kernels of the current stream still write to it
+    is not what a call on another stream returns its outputs in, nor is an output
+    reused while the current stream still reads it."""
+    call = _calls_that_allocate()[name]
+    ref = call()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    host = torch.empty(1 << 30, dtype=torch.uint8).pin_memory()
+    big = torch.empty_like(host, device="cuda")
+    for held in (False, True):                   # the first time to load what there is to load
+        late = [[torch.empty_like(x) for _ in range(64)] for x in ref]
+        if held:                                 # a copy of some 20 ms holds the stream, and no SM
+            big.copy_(host, non_blocking=True)
+        for xs in late:
+            torch._foreach_zero_(xs)
+        del xs, late
+    got = call(stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(ref, got))
+    # handed to the current stream: freed while it still has to read them
+    torch.cuda.current_stream().wait_stream(s)
+    big.copy_(host, non_blocking=True)
+    read = [x.clone() for x in got]
+    del got
+    with torch.cuda.stream(s):
+        over = [torch.full_like(x, 7) for x in ref for _ in range(8)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(ref, read)) and over
+    assert M.device_status() == 0
