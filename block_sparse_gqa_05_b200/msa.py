@@ -10,7 +10,6 @@ from __future__ import annotations
 
 import ctypes
 import functools
-import inspect
 import os
 import re
 
@@ -185,29 +184,25 @@ def _stream(stream):
         else stream.cuda_stream
 
 
-def _own_memory(call):
-    """For the calls with ``stream`` as their last argument: what such a call
-    allocates (outputs and a workspace that were not given) comes from that
+def _elsewhere(stream):
+    return stream != torch.cuda.current_stream(stream.device)
+
+
+def _on_stream(call, kw):
+    """A call, with all its arguments, whose ``stream`` is not the current one:
+    what it allocates (outputs and a workspace that were not given) comes from that
     stream's memory.  A block of the current stream's may still be in use by what
     is queued there.  The outputs are handed to the current stream, which must
     wait for the given one before it uses them."""
-    at = list(inspect.signature(call).parameters).index("stream")
-
-    @functools.wraps(call)
-    def on_stream(*args, **kw):
-        stream = args[at] if len(args) > at else kw.get("stream")
-        if stream is None:
-            return call(*args, **kw)
-        here = torch.cuda.current_stream(stream.device)
-        with torch.cuda.stream(stream):
-            out = call(*args, **kw)
-        given = {id(x) for x in (*args, *kw.values())}
-        for t in out if isinstance(out, tuple) else (out,):
-            if t is not None and id(t) not in given:
-                t.record_stream(here)
-        return out
-
-    return on_stream
+    stream = kw["stream"]
+    here = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        out = call(**kw)
+    given = {id(x) for x in kw.values()}
+    for t in out if isinstance(out, tuple) else (out,):
+        if t is not None and id(t) not in given:
+            t.record_stream(here)
+    return out
 
 
 def _check(status: int, what: str):
@@ -226,8 +221,9 @@ def alloc_workspace(shape: Shape, op: int, device=None) -> torch.Tensor:
     return torch.empty(max(n, 16), dtype=torch.uint8, device=device or "cuda")
 
 
-@_own_memory
 def index_scores(shape: Shape, q_idx, k_idx, pooled=None, stream=None):
+    if stream is not None and _elsewhere(stream):
+        return _on_stream(index_scores, locals())
     if pooled is None:
         pooled = torch.empty((shape.batch, shape.seq_q, shape.n_kv_heads, shape.nb),
                              dtype=torch.float32, device=q_idx.device)
@@ -237,8 +233,9 @@ def index_scores(shape: Shape, q_idx, k_idx, pooled=None, stream=None):
     return pooled
 
 
-@_own_memory
 def block_topk(shape: Shape, pooled, sel=None, stream=None):
+    if stream is not None and _elsewhere(stream):
+        return _on_stream(block_topk, locals())
     if sel is None:
         sel = torch.empty((shape.batch, shape.seq_q, shape.n_kv_heads, shape.topk),
                           dtype=torch.int32, device=pooled.device)
@@ -257,9 +254,10 @@ def _attn_out(shape, q, o, lse, want_lse):
     return o, lse
 
 
-@_own_memory
 def sparse_attn_prefill(shape: Shape, q, k, v, sel, o=None, lse=None, ws=None, want_lse=True,
                         stream=None):
+    if stream is not None and _elsewhere(stream):
+        return _on_stream(sparse_attn_prefill, locals())
     o, lse = _attn_out(shape, q, o, lse, want_lse)
     ws = alloc_workspace(shape, OP_SPARSE_PREFILL, q.device) if ws is None else ws
     a = _args(shape, q=q, k=k, v=v, sel=sel, o=o, lse=lse)
@@ -269,9 +267,10 @@ def sparse_attn_prefill(shape: Shape, q, k, v, sel, o=None, lse=None, ws=None, w
     return o, lse
 
 
-@_own_memory
 def sparse_attn_decode(shape: Shape, q, k, v, sel, o=None, lse=None, ws=None, want_lse=True,
                        stream=None):
+    if stream is not None and _elsewhere(stream):
+        return _on_stream(sparse_attn_decode, locals())
     o, lse = _attn_out(shape, q, o, lse, want_lse)
     ws = alloc_workspace(shape, OP_SPARSE_DECODE, q.device) if ws is None else ws
     a = _args(shape, q=q, k=k, v=v, sel=sel, o=o, lse=lse)
@@ -281,12 +280,13 @@ def sparse_attn_decode(shape: Shape, q, k, v, sel, o=None, lse=None, ws=None, wa
     return o, lse
 
 
-@_own_memory
 def sparse_attn_decode_static(shape: Shape, q, k, v, sel, o=None, lse=None, want_lse=True,
                               stream=None):
     """msa_sparse_attn_decode_static: decode attention whose scratch is the
     library's static device array, so nothing is allocated for it.  Calls
     that may overlap on the GPU share that array and must be serialised."""
+    if stream is not None and _elsewhere(stream):
+        return _on_stream(sparse_attn_decode_static, locals())
     o, lse = _attn_out(shape, q, o, lse, want_lse)
     a = _args(shape, q=q, k=k, v=v, sel=sel, o=o, lse=lse)
     _check(lib().msa_sparse_attn_decode_static(ctypes.byref(shape), a["q"], a["k"], a["v"],
@@ -295,9 +295,10 @@ def sparse_attn_decode_static(shape: Shape, q, k, v, sel, o=None, lse=None, want
     return o, lse
 
 
-@_own_memory
 def forward(shape: Shape, q, k, v, q_idx, k_idx, o=None, lse=None, sel=None, ws=None,
             want_lse=True, want_sel=True, stream=None):
+    if stream is not None and _elsewhere(stream):
+        return _on_stream(forward, locals())
     o, lse = _attn_out(shape, q, o, lse, want_lse)
     if sel is None and want_sel:
         sel = torch.empty((shape.batch, shape.seq_q, shape.n_kv_heads, shape.topk),
@@ -310,12 +311,13 @@ def forward(shape: Shape, q, k, v, q_idx, k_idx, o=None, lse=None, sel=None, ws=
     return o, lse, sel
 
 
-@_own_memory
 def forward_alignment(shape: Shape, q, k, v, q_idx, k_idx, o=None, lse=None, sel=None,
                       kl=None, ws=None, want_lse=True, want_sel=True, stream=None):
     """msa_forward_alignment: the whole layer plus kl [B, T, G] float32, the
     divergence of the index branch's block distribution from the main
     branch's (forward only).  Returns (o, lse, sel, kl)."""
+    if stream is not None and _elsewhere(stream):
+        return _on_stream(forward_alignment, locals())
     o, lse = _attn_out(shape, q, o, lse, want_lse)
     if sel is None and want_sel:
         sel = torch.empty((shape.batch, shape.seq_q, shape.n_kv_heads, shape.topk),
@@ -332,12 +334,13 @@ def forward_alignment(shape: Shape, q, k, v, q_idx, k_idx, o=None, lse=None, sel
     return o, lse, sel, kl
 
 
-@_own_memory
 def forward_decode_ragged(shape: Shape, q, k, v, q_idx, k_idx, seq_lens, o=None, lse=None,
                           sel=None, ws=None, want_lse=True, want_sel=True, stream=None):
     """msa_forward_decode_ragged: one decode step over caches of different
     lengths.  seq_lens: int32 CUDA tensor [B], each in [1, shape.seq_kv]
     (shape.seq_kv is the cache capacity)."""
+    if stream is not None and _elsewhere(stream):
+        return _on_stream(forward_decode_ragged, locals())
     o, lse = _attn_out(shape, q, o, lse, want_lse)
     if sel is None and want_sel:
         sel = torch.empty((shape.batch, 1, shape.n_kv_heads, shape.topk), dtype=torch.int32,
@@ -352,13 +355,14 @@ def forward_decode_ragged(shape: Shape, q, k, v, q_idx, k_idx, seq_lens, o=None,
     return o, lse, sel
 
 
-@_own_memory
 def forward_decode_paged(shape: Shape, q, k_pages, v_pages, q_idx, kidx_pages, seq_lens,
                          page_table, o=None, lse=None, sel=None, ws=None, want_lse=True,
                          want_sel=True, stream=None):
     """msa_forward_decode_paged: one decode step over paged caches.
     k_pages / v_pages [P, G, 128, d] bf16, kidx_pages [P, 128, d_i] bf16,
     seq_lens int32 [B], page_table int32 [B, ceil(shape.seq_kv / 128)]."""
+    if stream is not None and _elsewhere(stream):
+        return _on_stream(forward_decode_paged, locals())
     o, lse = _attn_out(shape, q, o, lse, want_lse)
     if sel is None and want_sel:
         sel = torch.empty((shape.batch, 1, shape.n_kv_heads, shape.topk), dtype=torch.int32,
@@ -375,7 +379,6 @@ def forward_decode_paged(shape: Shape, q, k_pages, v_pages, q_idx, kidx_pages, s
     return o, lse, sel
 
 
-@_own_memory
 def forward_prefill_paged(shape: Shape, q, k_pages, v_pages, q_idx, kidx_pages, page_table,
                           o=None, lse=None, sel=None, ws=None, want_lse=True, want_sel=True,
                           stream=None):
@@ -383,6 +386,8 @@ def forward_prefill_paged(shape: Shape, q, k_pages, v_pages, q_idx, kidx_pages, 
     shape.q_offset .. + seq_q - 1) over paged caches of seq_kv keys.
     k_pages / v_pages [P, G, 128, d] bf16, kidx_pages [P, 128, d_i] bf16,
     page_table int32 [B, ceil(shape.seq_kv / 128)]."""
+    if stream is not None and _elsewhere(stream):
+        return _on_stream(forward_prefill_paged, locals())
     o, lse = _attn_out(shape, q, o, lse, want_lse)
     if sel is None and want_sel:
         sel = torch.empty((shape.batch, shape.seq_q, shape.n_kv_heads, shape.topk),
@@ -399,8 +404,9 @@ def forward_prefill_paged(shape: Shape, q, k_pages, v_pages, q_idx, kidx_pages, 
     return o, lse, sel
 
 
-@_own_memory
 def dense_attn_prefill(shape: Shape, q, k, v, o=None, lse=None, want_lse=True, stream=None):
+    if stream is not None and _elsewhere(stream):
+        return _on_stream(dense_attn_prefill, locals())
     o, lse = _attn_out(shape, q, o, lse, want_lse)
     a = _args(shape, q=q, k=k, v=v, o=o, lse=lse)
     _check(lib().msa_dense_attn_prefill(ctypes.byref(shape), a["q"], a["k"], a["v"], a["o"],
@@ -409,9 +415,10 @@ def dense_attn_prefill(shape: Shape, q, k, v, o=None, lse=None, want_lse=True, s
     return o, lse
 
 
-@_own_memory
 def dense_attn_decode(shape: Shape, q, k, v, o=None, lse=None, ws=None, want_lse=True,
                       stream=None):
+    if stream is not None and _elsewhere(stream):
+        return _on_stream(dense_attn_decode, locals())
     o, lse = _attn_out(shape, q, o, lse, want_lse)
     ws = alloc_workspace(shape, OP_DENSE_DECODE, q.device) if ws is None else ws
     a = _args(shape, q=q, k=k, v=v, o=o, lse=lse)
@@ -469,7 +476,6 @@ def _prefix_decode(name, shape, lead, inputs, o, lse, weights, weights_out, ws, 
     return o, lse, weights_out
 
 
-@_own_memory
 def prefix_attn_decode(shape: Shape, q, k, v, seq_lens, k_prefix=None, v_prefix=None,
                        prefix_len=None, o=None, lse=None, weights=None, weights_out=None, ws=None,
                        want_lse=True, stream=None):
@@ -481,6 +487,8 @@ def prefix_attn_decode(shape: Shape, q, k, v, seq_lens, k_prefix=None, v_prefix=
     the softmax weight each own key received is added to it, in place or into
     weights_out (weights_out alone starts from 0).  Returns (o, lse,
     weights_out)."""
+    if stream is not None and _elsewhere(stream):
+        return _on_stream(prefix_attn_decode, locals())
     cap = 0 if k_prefix is None else int(k_prefix.shape[-2])
     n = cap if prefix_len is None else int(prefix_len)
     return _prefix_decode("msa_prefix_attn_decode", shape, (n, cap),
@@ -488,7 +496,6 @@ def prefix_attn_decode(shape: Shape, q, k, v, seq_lens, k_prefix=None, v_prefix=
                                v=v), o, lse, weights, weights_out, ws, want_lse, stream, 0, cap)
 
 
-@_own_memory
 def prefix_attn_decode_paged(shape: Shape, q, k_pages, v_pages, seq_lens, page_table,
                              prefix_pages=None, prefix_len=0, o=None, lse=None, weights=None,
                              weights_out=None, ws=None, want_lse=True, stream=None):
@@ -496,6 +503,8 @@ def prefix_attn_decode_paged(shape: Shape, q, k_pages, v_pages, seq_lens, page_t
     k_pages / v_pages [P, G, 128, d] bf16; prefix_pages int32
     [ceil(prefix_len / 128)] lists the prefix's pages, page_table int32
     [B, ceil(shape.seq_kv / 128)] those of the own caches."""
+    if stream is not None and _elsewhere(stream):
+        return _on_stream(prefix_attn_decode_paged, locals())
     n, P = int(prefix_len), int(k_pages.shape[0])
     return _prefix_decode("msa_prefix_attn_decode_paged", shape, (P, n),
                           dict(prefix_pages=prefix_pages, seq_lens=seq_lens,
@@ -522,7 +531,6 @@ def _cache_evict(name, shape, lead, inputs, weights_out, positions_out, new_lens
     return weights_out, positions_out, new_lens
 
 
-@_own_memory
 def cache_evict(shape: Shape, k, v, seq_lens, weights, positions, budget, first=0, recent=0,
                 weights_out=None, positions_out=None, new_lens=None, ws=None, stream=None):
     """msa_cache_evict: every (sequence, group) of the own caches k, v
@@ -531,17 +539,20 @@ def cache_evict(shape: Shape, k, v, seq_lens, weights, positions, budget, first=
     before all others.  k, v are compacted in place; weights and positions
     [B, G, shape.seq_kv] too unless weights_out / positions_out are given.
     Returns (weights_out, positions_out, new_lens)."""
+    if stream is not None and _elsewhere(stream):
+        return _on_stream(cache_evict, locals())
     return _cache_evict("msa_cache_evict", shape, (int(budget), int(first), int(recent)),
                         dict(seq_lens=seq_lens, weights=weights, positions=positions, k=k, v=v),
                         weights_out, positions_out, new_lens, ws, stream)
 
 
-@_own_memory
 def cache_evict_paged(shape: Shape, k_pages, v_pages, seq_lens, page_table, weights, positions,
                       budget, first=0, recent=0, weights_out=None, positions_out=None,
                       new_lens=None, ws=None, stream=None):
     """msa_cache_evict_paged: cache_evict over paged caches k_pages / v_pages
     [P, G, 128, d] with page_table int32 [B, ceil(shape.seq_kv / 128)]."""
+    if stream is not None and _elsewhere(stream):
+        return _on_stream(cache_evict_paged, locals())
     P = int(k_pages.shape[0])
     return _cache_evict("msa_cache_evict_paged", shape,
                         (P, int(budget), int(first), int(recent)),
