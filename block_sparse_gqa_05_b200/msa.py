@@ -459,10 +459,17 @@ def _call(name, dev, stream, *args):
     _check(getattr(lib(), name)(*args, _stream(stream)), name)
 
 
+def _check_ints(name, ints):
+    """Integer arguments as the C ABI takes them: ctypes would cut them to 32 bits."""
+    if max(ints) >= 1 << 31 or min(ints) < -(1 << 31):
+        raise ValueError(f"{name}: an integer past 32 bits in {ints}")
+
+
 def _prefix_decode(name, shape, lead, inputs, o, lse, weights, weights_out, ws, want_lse, stream,
                    pages, prefix):
     """The common part of the two calls: ``lead`` the integers after the shape,
     ``inputs`` the tensors before the output, in the C order."""
+    _check_ints(name, lead)
     if weights_out is None:
         weights_out = weights
     q = inputs["q"]
@@ -516,6 +523,7 @@ def _cache_evict(name, shape, lead, inputs, weights_out, positions_out, new_lens
                  pages=0):
     """The common part of the two calls: ``lead`` the integers after the shape,
     ``inputs`` the tensors before the first output, in the C order."""
+    _check_ints(name, lead)
     weights, positions, seq_lens = inputs["weights"], inputs["positions"], inputs["seq_lens"]
     if weights_out is None:
         weights_out = weights

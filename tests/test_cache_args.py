@@ -198,3 +198,29 @@ def test_attend_workspace_has_room_for_its_alignment():
     assert size(s, M.OP_PREFIX_DECODE_WEIGHTS) == (0, plain + 12 * 4 * 1024 * 4 + 16)
     exact = plain + 16
     assert attend(s, ws=ctypes.c_void_p((1 << 20) + 16), n=exact - 1) == 4
+
+
+@pytest.mark.parametrize("past", [1 << 31, (1 << 32) + 5, -(1 << 32) + 5])
+def test_binding_refuses_integers_past_32_bits(calls, past):  # noqa: F811
+    """ctypes cuts an int to its low 32 bits: a budget of 2^32 + 5 would keep 5 rows."""
+    s = shape()
+    x = _tensors(s)
+    with pytest.raises(ValueError, match="32 bits"):
+        M.prefix_attn_decode(s, x["q"], x["k"], x["v"], x["lens"], x["kp"], x["vp"], prefix_len=past)
+    for kw in (dict(budget=past), dict(budget=5, first=past), dict(budget=5, recent=past)):
+        with pytest.raises(ValueError, match="32 bits"):
+            M.cache_evict(s, x["k"], x["v"], x["lens"], x["w"], x["pos"], **kw)
+        with pytest.raises(ValueError, match="32 bits"):
+            M.cache_evict_paged(s, x["pages"], x["pages"], x["lens"], x["table"], x["w"], x["pos"], **kw)
+    if past < 0:
+        with pytest.raises(ValueError, match="32 bits"):
+            M.prefix_attn_decode_paged(s, x["q"], x["pages"], x["pages"], x["lens"], x["table"], x["pp"], past)
+    assert set(calls) <= {"msa_workspace_size"}
+
+
+def test_binding_takes_the_largest_integers(calls):  # noqa: F811
+    s = shape()
+    x = _tensors(s)
+    M.cache_evict(s, x["k"], x["v"], x["lens"], x["w"], x["pos"], (1 << 31) - 1, first=(1 << 31) - 1,
+                  recent=(1 << 31) - 1)
+    assert "msa_cache_evict" in calls
