@@ -497,6 +497,8 @@ def prefix_attn_decode(shape: Shape, q, k, v, seq_lens, k_prefix=None, v_prefix=
     if stream is not None and _elsewhere(stream):
         return _on_stream(prefix_attn_decode, locals())
     cap = 0 if k_prefix is None else int(k_prefix.shape[-2])
+    if cap != (0 if v_prefix is None else int(v_prefix.shape[-2])):
+        raise ValueError("k_prefix and v_prefix: [G, capacity, d] of one capacity")
     n = cap if prefix_len is None else int(prefix_len)
     return _prefix_decode("msa_prefix_attn_decode", shape, (n, cap),
                           dict(seq_lens=seq_lens, q=q, k_prefix=k_prefix, v_prefix=v_prefix, k=k,

@@ -224,3 +224,18 @@ def test_binding_takes_the_largest_integers(calls):  # noqa: F811
     M.cache_evict(s, x["k"], x["v"], x["lens"], x["w"], x["pos"], (1 << 31) - 1, first=(1 << 31) - 1,
                   recent=(1 << 31) - 1)
     assert "msa_cache_evict" in calls
+
+
+def test_binding_refuses_prefixes_of_two_capacities(calls):  # noqa: F811
+    """The capacity is a stride: the groups of a longer v_prefix would be read at
+    the wrong rows.  Half a prefix would be taken for none."""
+    s = shape()
+    x = _tensors(s)
+    longer = torch.zeros(4, 201, 64, dtype=torch.bfloat16)
+    for kp, vp in ((x["kp"], longer), (longer, x["vp"]), (None, x["vp"]), (x["kp"], None)):
+        with pytest.raises(ValueError, match="one capacity"):
+            M.prefix_attn_decode(s, x["q"], x["k"], x["v"], x["lens"], kp, vp)
+    assert not calls
+    empty = longer[:, :0]                     # no prefix, as tensors without rows
+    M.prefix_attn_decode(s, x["q"], x["k"], x["v"], x["lens"], empty, empty)
+    assert "msa_prefix_attn_decode" in calls
