@@ -65,7 +65,9 @@ struct PrefixParams {
   const float* w_in;
   float* w_out;
   const int32_t *lens, *prefix_pages, *table;
+  const uint16_t* v;   // own caches
   uint32_t* err;
+  int2* dropped;       // [B*G] whether the last block and the one before left out values of V (T > 1)
   int2* span;          // [nsp + B*G] first and last CTA with blocks of a segment
   float2* ml_p;        // [(nsp + grid) * 2, rows_p]  (maximum, sum) of prefix partials
   float* o_p;          // [(nsp + grid) * 2, rows_p, D]
@@ -372,6 +374,37 @@ __device__ __forceinline__ void exp_keys(const float* sv, uint64_t sc2, uint64_t
   }
 }
 
+// Whether either bf16 of a word is an infinity or a NaN; and the word with zeros for them.
+__device__ __forceinline__ bool not_finite2(uint32_t w) {
+  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+__device__ __forceinline__ uint32_t finite2(uint32_t w) {
+  if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+  if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
+  return w;
+}
+
+// Rows [y0, y1) of the V tile of an own block, which not all of the T queries of the
+// sequence see.  Their weight is 0 there, but 0 times an infinity or a NaN is not: a
+// warp sets these to zero and returns whether there were any, for the finishing
+// kernel to add them where they are seen.
+template <int D>
+__device__ __forceinline__ bool drop_not_finite(uint8_t* tile, int y0, int y1) {
+  bool any = false;
+#pragma unroll 1
+  for (int u = y0 * 8 + static_cast<int>(threadIdx.x & 31); u < y1 * 8; u += 32)
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
+      uint4* at = reinterpret_cast<uint4*>(tile + c * 16384) + u;
+      const uint4 w = *at;
+      if (not_finite2(w.x) || not_finite2(w.y) || not_finite2(w.z) || not_finite2(w.w)) {
+        *at = make_uint4(finite2(w.x), finite2(w.y), finite2(w.z), finite2(w.w));
+        any = true;
+      }
+    }
+  return __any_sync(0xffffffffu, any) != 0;
+}
+
 // A value all lanes of the warp hold, in the form the compiler knows as such.
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 
@@ -473,7 +506,10 @@ __device__ __forceinline__ void plan(const PrefixParams& p, int* scratch, Walk* 
   }
 }
 
-template <int D>
+// MANY: T > 1, with V rows that some queries of the sequence do not see.  Compiled
+// apart: the look at them costs the one token nothing (32 sequences with a prefix of
+// 8192 48.4 against 47.7 us in one kernel) and 24 of 5 tokens 1.4 in 112.
+template <int D, bool MANY>
 __global__ void __launch_bounds__(kThreads, 1)
     prefix_attn_kernel(const __grid_constant__ PrefixMaps tm, const __grid_constant__ PrefixParams p) {
   using L = PrefixSmem<D>;
@@ -681,6 +717,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t qd =
               smem_desc(uniform(smem_u32(qbuf) + (early ? (jobs & 1) * p.q_stage : 0)), 16, 1024, 2);
           const bool rag = q.ragged(), pair = q.pair();
+          // first block with V rows to clean: past the length, or not seen by every query
+          const int clean = MANY && q.own() ? (max(q.rows - p.T + 1, 0) >> 7) - q.j0 : rag ? q.n - 1 : q.n;
           // S = Q K^T of block x, over the P that the product before has read
           auto wait_k = [&](int x) {
             return warp_wait_tile<R>(m, issued, 2 * (q.n0 + x), w);
@@ -710,16 +748,24 @@ __global__ void __launch_bounds__(kThreads, 1)
               break;
             uint8_t* v = smem + L::kOffRing + st * L::kTile;
             int steps = 8;
-            if (rag && x == q.n - 1) {
-              steps = q.tail_steps();
-              const int tail = q.rows & 127, units = (steps * 16 - tail) * 8;
-              for (int y = lane; y < units; y += 32)
+            if (x >= clean) {
+              if (rag && x == q.n - 1) {
+                steps = q.tail_steps();
+                const int tail = q.rows & 127, units = (steps * 16 - tail) * 8;
+                for (int y = lane; y < units; y += 32)
 #pragma unroll
-                for (int c = 0; c < D / 64; ++c)
-                  *reinterpret_cast<uint4*>(v + c * 16384 + tail * 128 + y * 16) =
-                      make_uint4(0, 0, 0, 0);
+                  for (int c = 0; c < D / 64; ++c)
+                    *reinterpret_cast<uint4*>(v + c * 16384 + tail * 128 + y * 16) =
+                        make_uint4(0, 0, 0, 0);
+              }
+              const bool some = MANY && q.own();
+              const int j = q.j0 + x;
+              bool any = false;
+              if (some) any = drop_not_finite<D>(v, max(q.rows - p.T + 1 - j * 128, 0), min(q.rows - j * 128, 128));
               fence_proxy_async_smem();
               __syncwarp();
+              // after the fence, which would wait for it
+              if (some && lane == 0) (&p.dropped[q.id - p.nsp].x)[blocks_of(q.rows) - 1 - j] = any;
             }
             // Of a pair the two warpgroups take turns at the tensor cores, O +=
             // P V and the next S together, so that one is in its softmax while
@@ -993,13 +1039,34 @@ __device__ __forceinline__ float add_norm(const float2* ml, const Parts& s, int 
   return w;
 }
 
+// Adds to a lane's columns of the output of query t what drop_not_finite left out
+// of the rows that it sees: a weight times an infinity or a NaN is that itself.
+template <int V>
+__device__ __forceinline__ void add_not_finite(const PrefixParams& p, int b, int g, int t, int len, float* acc) {
+  const int lane = static_cast<int>(threadIdx.x & 31);
+#pragma unroll 1
+  for (int x = max(len - p.T + 1, 0); x <= len - p.T + t; ++x) {
+    const long long row =
+        p.table ? (static_cast<long long>(page_of(p.table, p.nb, p.num_pages, b, x >> 7, p.err)) * p.G + g) * 128 +
+                      (x & 127)
+                : (static_cast<long long>(b) * p.G + g) * p.C + x;
+    const uint32_t* v = reinterpret_cast<const uint32_t*>(p.v + row * (V * 32) + lane * V);
+#pragma unroll
+    for (int c = 0; c < V / 2; ++c) {
+      const uint32_t w = __ldcg(v + c);
+      if ((w & 0x7f80u) == 0x7f80u) acc[2 * c] += __uint_as_float(w << 16);
+      if ((w & 0x7f800000u) == 0x7f800000u) acc[2 * c + 1] += __uint_as_float(w & 0xffff0000u);
+    }
+  }
+}
+
 // The last CTAs merge the partials: o = sum 2^(m - M) O / sum 2^(m - M) l and
 // lse = M + log2 of the denominator, kMergeWarps / split rows a CTA, split
 // warps sharing a row's partials (few rows have many).  The first add the
 // weights of ``keys`` own keys of a (sequence, group), from their logits and
 // the normalisers of the rows, which each finds for itself: a few hundred
-// cached loads, against one launch more and its wait.
-template <int D>
+// cached loads, against one launch more and its wait.  MANY: as above.
+template <int D, bool MANY>
 __global__ void __launch_bounds__(kMergeWarps * 32)
     prefix_finish_kernel(const __grid_constant__ PrefixParams p, int merge_ctas, int split, int keys) {
   constexpr int V = D / 32;
@@ -1015,6 +1082,11 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
     const int b = tok / p.T, len = own_len(p, b);
     griddep_wait();
     griddep_launch_dependents();
+    int dropped = 0;
+    if (MANY && len > 0) {
+      const int2 d = __ldcg(p.dropped + b * p.G + h / p.r);
+      dropped = d.x | (len - p.T + 1 < ((len - 1) & ~127) ? d.y : 0);   // unset when one block has all such rows
+    }
     float acc[V];
 #pragma unroll
     for (int y = 0; y < V; ++y) acc[y] = 0.f;
@@ -1071,6 +1143,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
         for (int y = 0; y < V; ++y) acc[y] += buf[(warp + u) * D + lane * V + y];
     }
     if (!in) return;
+    if (MANY && dropped) add_not_finite<V>(p, b, h / p.r, tok - b * p.T, len, acc);
     const bool none = M == -INFINITY && den == 0.f;
     const float inv = none ? 0.f : 1.f / den;
     uint16_t* out = p.o + row * D + lane * V;
@@ -1181,7 +1254,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
 // multiple of 16 bytes, and store8 needs 32.
 constexpr size_t kWsAlign = 32;
 struct PrefixWs {
-  size_t span, ml_p, o_p, ml_s, o_s, logits, bytes;
+  size_t span, dropped, ml_p, o_p, ml_s, o_s, logits, bytes;
 };
 
 PrefixWs ws_layout(const msa_shape& s, bool weights) {
@@ -1200,6 +1273,7 @@ PrefixWs ws_layout(const msa_shape& s, bool weights) {
     return x;
   };
   w.span = take((nsp + bg) * sizeof(int2));
+  w.dropped = take(s.seq_q > 1 ? bg * sizeof(int2) : 0);
   w.ml_p = take(pr * sizeof(float2));
   w.o_p = take(pr * d * sizeof(float));
   w.ml_s = take(sr * sizeof(float2));
@@ -1244,14 +1318,14 @@ cudaError_t launch(const msa_shape& s, const PrefixDecodeArgs& a, const PrefixPa
     tm.kp = tm.k, tm.vp = tm.v, tm.kp16 = tm.k16, tm.vp16 = tm.v16;
   if (!ok) return cudaErrorInvalidValue;
   const size_t smem = PrefixSmem<D>::kBytes;
-  cudaError_t e = cudaFuncSetAttribute(prefix_attn_kernel<D>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+  const auto attn = p.T > 1 ? prefix_attn_kernel<D, true> : prefix_attn_kernel<D, false>;
+  const auto finish = p.T > 1 ? prefix_finish_kernel<D, true> : prefix_finish_kernel<D, false>;
+  cudaError_t e = cudaFuncSetAttribute(attn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   {
     ProfScope ps_("prefix_attn", st);
-    e = launch_dependent(prefix_attn_kernel<D>, dim3(static_cast<unsigned>(p.grid)), dim3(kThreads),
-                         smem, st, tm, p);
+    e = launch_dependent(attn, dim3(static_cast<unsigned>(p.grid)), dim3(kThreads), smem, st, tm, p);
   }
   if (e != cudaSuccess) return e;
   // warps a row: enough to have some 8 warps on every SM (with 16, two sequences
@@ -1268,8 +1342,8 @@ cudaError_t launch(const msa_shape& s, const PrefixDecodeArgs& a, const PrefixPa
   const int64_t score = p.w_out ? static_cast<int64_t>(p.B) * p.G * ceil_div(p.C, keys) : 0;
   if (merge + score >= (1ll << 31)) return cudaErrorInvalidValue;
   ProfScope ps_("prefix_finish", st);
-  return launch_dependent(prefix_finish_kernel<D>, dim3(static_cast<unsigned>(merge + score)),
-                          dim3(kMergeWarps * 32), 0, st, p, static_cast<int>(merge), split, keys);
+  return launch_dependent(finish, dim3(static_cast<unsigned>(merge + score)), dim3(kMergeWarps * 32), 0, st, p,
+                          static_cast<int>(merge), split, keys);
 }
 
 }  // namespace
@@ -1301,11 +1375,13 @@ cudaError_t launch_prefix_decode(const msa_shape& s, const PrefixDecodeArgs& a, 
   p.w_in = a.w_in;
   p.w_out = a.w_out;
   p.lens = a.lens;
+  p.v = a.v;
   p.prefix_pages = a.prefix_len > 0 ? a.prefix_pages : nullptr;
   p.table = a.pages.table;
   p.num_pages = a.pages.num_pages;
   p.err = ctx->err;
   p.span = reinterpret_cast<int2*>(base + w.span);
+  p.dropped = reinterpret_cast<int2*>(base + w.dropped);
   p.ml_p = reinterpret_cast<float2*>(base + w.ml_p);
   p.o_p = reinterpret_cast<float*>(base + w.o_p);
   p.ml_s = reinterpret_cast<float2*>(base + w.ml_s);

@@ -337,6 +337,8 @@ msa_status msa_sparse_attn_decode_static(const msa_shape* shape, const uint16_t*
  * for x < seq_lens[b]; entries at or past seq_lens[b] are neither read nor
  * written.  weights may be NULL (taken as 0) or equal to weights_out (update
  * in place); they must not overlap otherwise.
+ * An infinity or a NaN in V makes the outputs of the queries that see its row
+ * infinite or NaN in its column, and touches no other query.
  * shape.q_offset is ignored.  Rows past a length (prefix or own) may hold any
  * bits.  A length outside [0, N] is clamped into it and sets bit 1 of the
  * device error word.  Softmax statistics, partial outputs and scores are held

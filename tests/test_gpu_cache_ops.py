@@ -784,3 +784,39 @@ def test_outputs_of_a_call_on_another_stream_are_not_written_late(name):
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(ref, read)) and over
     assert M.device_status() == 0
+
+
+NOT_FINITE = [
+    dict(B=3, T=3, H=8, G=2, d=128, Np=300, C=300, lens=[300, 3, 130]),        # spread and whole tiles, two blocks
+    dict(B=3, T=5, H=16, G=2, d=64, Np=0, C=700, lens=[700, 2, 643]),          # a length below T; 40 rows
+    dict(B=2, T=2, H=4, G=4, d=64, Np=5000, C=1200, lens=[1200, 1025]),        # spread tiles of 2 rows
+    dict(B=2, T=16, H=16, G=2, d=128, Np=40, C=2000, lens=[2000, 1930]),       # a tile of 128 rows
+    dict(B=2, T=128, H=2, G=2, d=128, Np=129, C=260, lens=[255, 100]),         # most rows are unseen by some
+]
+
+
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("i", range(len(NOT_FINITE)))
+def test_values_of_later_tokens_stay_out_of_earlier_queries(i, paged):
+    """Infinities and NaNs in V of the new tokens reach the queries that see them
+    and no other: those give the bits they give with finite values there.  (Which of
+    them a query gets is not told: a weight times an infinity is one, but a weight
+    that was rounded to 0, or a tile's zero for another warp's key, makes it NaN.)"""
+    c = Case(**NOT_FINITE[i], seed=120 + i)
+    run = (lambda: c.run_paged()) if paged else (lambda: c.run())
+    ref = run()
+    rng = np.random.default_rng(i)
+    r, hit = c.H // c.G, torch.zeros(c.q.shape, dtype=torch.bool)
+    for b, n in enumerate(c.lens):
+        for g in range(c.G):
+            for x in rng.choice(range(max(n - c.T, 0), n), size=min(3, n, c.T), replace=False):
+                for col, val in zip(rng.choice(c.d, 3, replace=False), rng.permutation([NAN, np.inf, -np.inf])):
+                    c.v[b, g, int(x), int(col)] = float(val)
+                    hit[b, max(int(x) - n + c.T, 0):, g * r:(g + 1) * r, int(col)] = True
+    o, lse, w = run()
+    torch.cuda.synchronize()
+    assert hit.any() and not hit.all()
+    assert torch.equal(torch.isfinite(o.cpu()), ~hit)
+    assert torch.equal(o.cpu()[~hit], ref[0].cpu()[~hit])
+    assert torch.equal(lse, ref[1]) and torch.equal(w, ref[2])
+    assert M.device_status() == 0
