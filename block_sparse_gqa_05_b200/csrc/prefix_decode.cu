@@ -1015,15 +1015,17 @@ __device__ __forceinline__ int part_row(const Parts& s, int k) {
 
 // Partials k0 + lane of a row: adds them to the row's maximum and sum, and
 // returns the lane's weight 2^(m - M); *keep is what scales what was added
-// before.  A NaN of a partial (a logit was NaN or +inf) makes *den NaN: the
+// before, *at the lane's partial row, or -1 when that saw no key (and may never have
+// been written).  A NaN of a partial (a logit was NaN or +inf) makes *den NaN: the
 // maximum drops it, the sums do not.
 __device__ __forceinline__ float add_norm(const float2* ml, const Parts& s, int k, int* at, float* M,
                                           float* den, float* keep) {
   float2 v = make_float2(-INFINITY, 0.f);
-  *at = 0;
+  *at = -1;
   if (k < s.n) {
-    *at = part_row(s, k);
-    v = __ldcg(ml + *at);
+    const int row = part_row(s, k);
+    v = __ldcg(ml + row);
+    if (v.x != -INFINITY) *at = row;
   }
   float mx = v.x;
 #pragma unroll
@@ -1102,8 +1104,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
         const float w = add_norm(own ? p.ml_s : p.ml_p, s, k0 + lane, &at, &M, &den, &keep);
 #pragma unroll
         for (int y = 0; y < V; ++y) acc[y] *= keep;
-        // a partial of weight 0 may never have been written
-        unsigned todo = __ballot_sync(0xffffffffu, w > 0.f && (lane & (split - 1)) == sub);
+        // (one whose weight is rounded to 0 too: 0 times its infinities is not 0)
+        unsigned todo = __ballot_sync(0xffffffffu, at >= 0 && (lane & (split - 1)) == sub);
         while (todo) {
           constexpr int U = 8;         // partial rows in flight
           float x[U][V], wk[U];

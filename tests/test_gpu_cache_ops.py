@@ -820,3 +820,22 @@ def test_values_of_later_tokens_stay_out_of_earlier_queries(i, paged):
     assert torch.equal(o.cpu()[~hit], ref[0].cpu()[~hit])
     assert torch.equal(lse, ref[1]) and torch.equal(w, ref[2])
     assert M.device_status() == 0
+
+
+@pytest.mark.parametrize("B, H", [(1, 8), (40, 32)])       # spread tiles; pairs of tiles
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("d", [64, 128])
+def test_an_infinite_value_shows_at_any_weight(d, sign, B, H):
+    """A seen key's weight is positive, if smaller than fp32 tells from 0: an
+    infinity in its V is one in the output (or NaN, as 0 times it), not nothing."""
+    c = Case(B=B, T=1, H=H, G=4, d=d, Np=700, C=200, lens=[200 - i for i in range(B)], seed=140)
+    c.q[:], c.k[:], c.kp[:] = 4.0, 4.0 * sign, -4.0 * sign     # logits of +-16 d^0.5: weights of 2^-369 and less
+    c.vp[:, 650, 3], c.vp[:, 2, 5] = float("inf"), NAN
+    c.v[:, :, 130, 7], c.v[:, :, 40, 9] = float("-inf"), NAN
+    o, lse, w = c.run()
+    torch.cuda.synchronize()
+    bad = torch.zeros(d, dtype=torch.bool)
+    bad[[3, 5, 7, 9]] = True
+    assert not torch.isfinite(o[..., bad]).any()
+    assert torch.isfinite(o[..., ~bad]).all() and torch.isfinite(lse).all()
+    assert M.device_status() == 0
