@@ -346,7 +346,9 @@ msa_status msa_sparse_attn_decode_static(const msa_shape* shape, const uint16_t*
  * product with V.  Results do not depend on timing (no atomics).
  * ws >= msa_workspace_size(MSA_OP_PREFIX_DECODE, or
  * MSA_OP_PREFIX_DECODE_WEIGHTS with weights_out); the size does not depend on
- * the prefix.  Calls that can overlap need workspaces of their own.
+ * the prefix.  With scores it holds the logits of the own keys, 4 T H bytes for
+ * each of the B N rows of capacity (at T r = d / 2 as much as one of K and V).
+ * Calls that can overlap need workspaces of their own.
  * Errors: T > N, prefix_len < 0 or > prefix_cap -> MSA_ERR_INVALID_SHAPE;
  * T * r > 128, G * prefix_cap >= 2^31, or more work than 32-bit positions hold
  * (some 10^8 visits of a 256-row prefix tile or of an own cache to a 128-key
@@ -392,14 +394,17 @@ msa_status msa_prefix_attn_decode_paged(const msa_shape* shape, int num_pages, i
  *                  the inputs or each other otherwise.
  *   new_lens       [B] int32, receives n; must not be seq_lens itself
  * The attention is the same for any order of the rows before the new tokens,
- * so msa_prefix_attn_decode runs on the compacted cache with new_lens.
- * Positions are whatever increasing numbers the caller gives its rows.  With
+ * so msa_prefix_attn_decode runs on the compacted cache with new_lens.  The
+ * sparse calls do not: their blocks lie at fixed positions, and k_idx rows are
+ * not moved.  Positions are whatever increasing numbers the caller gives its rows.  With
  * the same weights, positions and lengths a repeated call moves the same rows.
- * shape.seq_q, q_offset, n_q_heads, topk and index_dim are only validated.
- * A length outside [0, N] is clamped into it and sets bit 1 of the device
- * error word.  ws >= msa_workspace_size(MSA_OP_CACHE_EVICT).
+ * shape.seq_q, q_offset and index_dim are ignored, n_q_heads and topk only
+ * validated.  A length outside [0, N] is clamped into it and sets bit 1 of the
+ * device error word.  ws >= msa_workspace_size(MSA_OP_CACHE_EVICT); calls that
+ * can overlap need workspaces of their own.
  * Errors: budget < 1, n_first < 0, n_recent < 0 -> MSA_ERR_INVALID_SHAPE;
- * overlapping arrays -> MSA_ERR_UNSUPPORTED. */
+ * weights, positions or lengths that overlap -> MSA_ERR_UNSUPPORTED (the
+ * caches and the workspace must not overlap anything either: not checked). */
 msa_status msa_cache_evict(const msa_shape* shape, int budget, int n_first, int n_recent,
                            const int32_t* seq_lens, const float* weights,
                            const int32_t* positions, uint16_t* k, uint16_t* v,

@@ -239,3 +239,11 @@ def test_binding_refuses_prefixes_of_two_capacities(calls):  # noqa: F811
     empty = longer[:, :0]                     # no prefix, as tensors without rows
     M.prefix_attn_decode(s, x["q"], x["k"], x["v"], x["lens"], empty, empty)
     assert "msa_prefix_attn_decode" in calls
+
+
+def test_evict_ignores_the_query_fields():
+    for kw in (dict(seq_q=0), dict(seq_q=77), dict(q_offset=-3), dict(q_offset=1 << 30), dict(index_dim=7)):
+        assert size(shape(**kw), M.OP_CACHE_EVICT) == size(shape(), M.OP_CACHE_EVICT)
+        assert evict(shape(**kw), n=8) == 4 and evict(shape(**kw), pages=8, n=8) == 4
+    for kw, code in ((dict(topk=65), 5), (dict(topk=0), 1), (dict(n_q_heads=18), 1)):
+        assert size(shape(**kw), M.OP_CACHE_EVICT)[0] == code
