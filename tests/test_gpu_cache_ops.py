@@ -839,3 +839,40 @@ def test_an_infinite_value_shows_at_any_weight(d, sign, B, H):
     assert not torch.isfinite(o[..., bad]).any()
     assert torch.isfinite(o[..., ~bad]).all() and torch.isfinite(lse).all()
     assert M.device_status() == 0
+
+
+@pytest.mark.parametrize("T", [1, 3])
+@pytest.mark.parametrize("Np", [0, 300])
+def test_runs_of_idle_slots(Np, T):
+    """A batch of fixed width with few sequences in it: runs of length 0 before,
+    between and behind them, longer than the CTAs of the grid."""
+    lens = [0] * 400
+    lens[160], lens[161], lens[399 if T == 1 else 290] = 130, T, 64
+    c = Case(B=400, T=T, H=4, G=2, d=64, Np=Np, C=140, lens=lens, seed=150)
+    got = c.run()
+    torch.cuda.synchronize()
+    assert M.device_status() == 0
+    c.check(*got)
+
+
+def test_a_batch_without_any_key():
+    c = Case(B=300, T=1, H=4, G=2, d=64, Np=0, C=140, lens=[0] * 300, seed=151)
+    got = c.run()
+    torch.cuda.synchronize()
+    assert M.device_status() == 0
+    c.check(*got)
+
+
+def test_capacity_far_above_the_lengths():
+    """Caches allocated for 100,000 rows that hold a few hundred."""
+    c = Case(B=2, T=2, H=8, G=2, d=64, Np=129, C=100_000, lens=[300, 2], seed=152)
+    got = c.run()
+    torch.cuda.synchronize()
+    assert M.device_status() == 0
+    c.check(*got)
+    for C in (100_001, 330_000):                           # clusters, chunks
+        c = Cache(B=2, G=2, d=64, C=C, lens=[700, 65], kind="ties", shuffled=True, seed=153)
+        for in_place in (False, True):
+            got = c.run(100, 4, 20, in_place)
+            assert M.device_status() == 0
+            c.check(got, 100, 4, 20, in_place)
