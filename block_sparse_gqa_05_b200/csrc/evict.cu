@@ -25,9 +25,9 @@
 // 16 GB/s an SM.  Rows too long for the cluster's shared memory are chosen by
 // kernels of the whole GPU instead (evict_long.cu); the moves are the same.
 //
-// 256 x 4097 rows with one to drop 14.4 us (2.5 of them at the bandwidth of HBM;
+// 256 x 4097 rows with one to drop 14.5 us (2.5 of them at the bandwidth of HBM;
 // the rest is a chain of passes with a barrier each); 32 x 100,000 to 131,072
-// rows to 32,768: 54 us here and 136 us for the moves (floor of both 125).
+// rows to 32,768: 54 us here and 131 us for the moves (floor of both 125).
 #include <cooperative_groups.h>
 #include <algorithm>
 

@@ -18,9 +18,9 @@
 //           what weights and positions show afterwards
 // Only chunks with rows that always stay read positions again.  So a row costs 8
 // bytes read once, 4 bytes twice from L2, and 8 bytes written.  8 of 1,048,576
-// rows with 65,536 to keep: 104 us (a cluster each 210: at most 16 CTAs, and
-// seven of the eight GPCs hold such a cluster); each kernel takes some 3 us when
-// there is little to do, the lists 40 us of the 104.
+// rows with 65,536 to keep: 104 us (slices of a cluster each, read again in every
+// pass, 210); each kernel takes some 3 us when there is little to do, the lists 40
+// us of the 104.
 #include <algorithm>
 
 #include "evict.cuh"

@@ -509,7 +509,7 @@ __device__ __forceinline__ void plan(const PrefixParams& p, int* scratch, Walk* 
 
 // MANY: T > 1, with V rows that some queries of the sequence do not see.  Compiled
 // apart: the look at them costs the one token nothing (32 sequences with a prefix of
-// 8192 48.4 against 47.7 us in one kernel) and 24 of 5 tokens 1.4 in 112.
+// 8192 48.4 against 47.7 us in one kernel) and 24 of 5 tokens 1.4 in 114.
 template <int D, bool MANY>
 __global__ void __launch_bounds__(kThreads, 1)
     prefix_attn_kernel(const __grid_constant__ PrefixMaps tm, const __grid_constant__ PrefixParams p) {
