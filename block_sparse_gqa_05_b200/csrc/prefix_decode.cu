@@ -154,7 +154,9 @@ struct __align__(16) Seg {
   __device__ __forceinline__ int tail_steps() const { return ((rows & 127) + 15) >> 4; }
 };
 
-// Walks a CTA's segments along the line.
+// Walks a CTA's segments along the line, by a whole warp: runs of sequences without
+// rows (idle slots of a batch) are passed 32 at a time, as one by one a few million
+// of them took longer than the other warps wait.
 struct Walk {
   int u0, u1, pos;
   int s, b, g, len, n0;
@@ -164,6 +166,7 @@ struct Walk {
     for (;;) {
       int w, nb;
       const int start = pos;
+      if (start >= u1) break;
       if (s < p.nsp) {
         const int g_ = s / p.npt, tile = 2 * (s - g_ * p.npt);
         const bool pair = tile + 1 < p.ntile;
@@ -177,12 +180,18 @@ struct Walk {
         pos += nb * w + (pair ? kCostPairSegment : kCostSegment);
         ++s;
       } else {
-        if (b < p.B && len < 0) len = own_len(p, b);
-        if (b < p.B && len == 0) {
-          ++b;
-          g = 0;
-          len = -1;
-          continue;
+        if (len < 0) {
+          const int at = b + static_cast<int>(threadIdx.x & 31);
+          const int n = at < p.B ? own_len(p, at) : 0;
+          const unsigned some = __ballot_sync(0xffffffffu, n > 0);
+          if (!some) {
+            b += 32;
+            if (b >= p.B) break;      // not before u1
+            continue;
+          }
+          const int first = __ffs(some) - 1;
+          len = __shfl_sync(0xffffffffu, n, first);
+          b += first;
         }
         q.id = p.nsp + b * p.G + g;
         q.b = b;
@@ -191,16 +200,12 @@ struct Walk {
         q.rows = len;
         nb = blocks_of(len);
         w = single_cost(p, true, nb);
-        if (b < p.B) pos += own_cost(p, nb);
+        pos += own_cost(p, nb);
         if (++g >= p.G) {
           g = 0;
           ++b;
           len = -1;
         }
-      }
-      if (start >= u1) {
-        q.n = 0;
-        return q;
       }
       q.j0 = blocks_before(u0, start, w, nb);
       q.n = blocks_before(u1, start, w, nb) - q.j0;
@@ -212,6 +217,8 @@ struct Walk {
         return q;
       }
     }
+    q.n = 0;
+    return q;
   }
 };
 
@@ -588,19 +595,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_dec<88>();        // 4 x 88 + 8 x 208 warps' worth is what the launch has; with 80 these spilled
     if (warp == 3) {
       // ------------------------------------------------------------ the walk
-      if (lane == 0) {
-        Walk walk = *walk0;
-        for (int k = 0;; ++k) {
-          const Seg q = walk.next(p);
-          const int slot = k % kSegRing;
-          if (!wait_bar(&m.dempty[slot], ((k / kSegRing) & 1) ^ 1, w)) break;
+      Walk walk = *walk0;
+      for (int k = 0;; ++k) {
+        const Seg q = walk.next(p);
+        const int slot = k % kSegRing;
+        if (!warp_wait(&m.dempty[slot], ((k / kSegRing) & 1) ^ 1, w)) break;
+        if (lane == 0) {
           reinterpret_cast<int4*>(segs + slot)[0] = reinterpret_cast<const int4*>(&q)[0];
           reinterpret_cast<int4*>(segs + slot)[1] = reinterpret_cast<const int4*>(&q)[1];
           mbar_arrive(&m.dfull[slot]);
-          if (q.n == 0) break;
         }
+        __syncwarp();
+        if (q.n == 0) break;
       }
-      __syncwarp();
     } else if (warp == 0) {
       // ------------------------------------------------------- K and V tiles
       if (lane == 0) {

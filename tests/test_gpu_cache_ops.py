@@ -876,3 +876,40 @@ def test_capacity_far_above_the_lengths():
             got = c.run(100, 4, 20, in_place)
             assert M.device_status() == 0
             c.check(got, 100, 4, 20, in_place)
+
+
+def test_idle_slots_between_two_sequences_take_no_wait_limit():
+    """The warp that looks for the next sequence passes 600,000 idle slots well within
+    30 ms, while the others wait for it (one at a time took ten times that)."""
+    B, C, d = 600_000, 4, 64
+    sh = mshape(B, 1, 1, 1, d, C)
+    g = torch.Generator(device="cuda").manual_seed(154)
+    q = torch.randn(B, 1, 1, d, generator=g, device="cuda").to(torch.bfloat16)
+    k, v = (torch.full((B, 1, C, d), NAN, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    busy = [0, 299_999, B - 1]
+    for b, n in zip(busy, (3, 4, 1)):
+        lens[b] = n
+        k[b, 0, :n], v[b, 0, :n] = (torch.randn(n, d, generator=g, device="cuda").to(torch.bfloat16)
+                                    for _ in range(2))
+    ws = M.alloc_workspace(sh, M.OP_PREFIX_DECODE)
+    M.prefix_attn_decode(sh, q, k, v, lens, ws=ws)
+    torch.cuda.synchronize()
+    M.device_status()
+    try:
+        M.set_wait_limit_ns(30_000_000)
+        o, lse, _ = M.prefix_attn_decode(sh, q, k, v, lens, ws=ws)
+        torch.cuda.synchronize()
+        assert M.device_status() == 0
+    finally:
+        M.set_wait_limit_ns(2_000_000_000)
+    for b in busy:
+        n = int(lens[b])
+        ro, rl, _, absum, _ = CO.prefix_attention(q[b:b + 1], torch.zeros(1, 0, d), torch.zeros(1, 0, d),
+                                                  k[b:b + 1], v[b:b + 1], [n])
+        # as Case.check, with delta far below 2^-9
+        tol = (2.0**-8 + 2.0**-9) * absum + 2.0**-8 * np.abs(ro) + 2.0**-15 * absum
+        assert np.all(np.abs(o[b:b + 1].double().cpu().numpy() - ro) <= tol)
+        assert abs(float(lse[b]) - float(rl[0, 0, 0])) < 2.0**-12
+        o[b], lse[b] = 0, -float("inf")
+    assert not o.any() and torch.isneginf(lse).all()
