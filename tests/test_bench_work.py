@@ -72,3 +72,9 @@ def test_prefill_step_bound_is_the_sum_of_stage_bounds(bench):
                   + bench.selected_attention_flops(sp, sel) / 1e15)
     assert out["ms_at_bounds"] == pytest.approx(want, abs=1e-3)
     assert out["frac"] == pytest.approx(want / 2.0, abs=1e-4)
+
+
+def test_the_traffic_capture_is_of_the_current_sources(bench):
+    """A change of the files that the dominant kernel is built from leaves its line
+    without DRAM bytes until it is captured again."""
+    assert bench.ncu_traffic("kvouter_attn") > 0
