@@ -195,6 +195,9 @@ def _on_stream(call, kw):
     is queued there.  The outputs are handed to the current stream, which must
     wait for the given one before it uses them."""
     stream = kw["stream"]
+    for name, x in kw.items():
+        if isinstance(x, torch.Tensor) and x.device != stream.device:
+            raise ValueError(f"{name}: on {x.device}, the stream on {stream.device}")
     here = torch.cuda.current_stream(stream.device)
     with torch.cuda.stream(stream):
         out = call(**kw)

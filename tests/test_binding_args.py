@@ -107,3 +107,17 @@ def test_workspace_size_is_passed_in_bytes(calls, monkeypatch):
     msa.sparse_attn_prefill(sh, x.q, x.k, x.v, torch.zeros((2, 130, 4, 5), dtype=torch.int32),
                             ws=ws)
     assert seen["bytes"] == 400
+
+
+def test_a_stream_of_another_device_is_refused(calls, monkeypatch):
+    """Its device would be the one the call is launched on, with tensors of another."""
+    class Stream:
+        device, cuda_stream = torch.device("cuda", 1), 0
+
+    monkeypatch.setattr(msa, "_elsewhere", lambda s: True)
+    sp, sh, x = _prefill()
+    with pytest.raises(ValueError, match="q_idx: on cpu, the stream on cuda:1"):
+        msa.index_scores(sh, x.q_idx, x.k_idx, stream=Stream())
+    with pytest.raises(ValueError, match="q: on cpu, the stream on cuda:1"):
+        msa.forward(sh, x.q, x.k, x.v, x.q_idx, x.k_idx, stream=Stream())
+    assert not calls
